@@ -14,6 +14,9 @@ missing the calls raise.
     kvq_decode_attn_append(...), kvq_tag_check_append(...)   fused forms
     kvq_decode_step(...)    tag check + append + attention of a decode step, one launch
     kvq_amax_scales(...), kvq_quantize_pages(...)            prefill -> decode handoff
+    kvq_append_blocks(...), kvq_decode_attn_blocks(...)      the block-scaled cache
+    kvq_decode_attn_window(...), kvq_tag_check_window(...)   a sliding window with sinks
+    kvq_copy_pages(...)     pages copied inside every cache of a pool
     kvq_w4a16_gemm(...)     INT4 weight-only product for decode
 """
 from __future__ import annotations
@@ -28,6 +31,7 @@ KVQ_CACHE_FP8_E4M3 = 0
 KVQ_CACHE_BF16 = 1
 KVQ_OUT_BF16 = 0
 KVQ_OUT_FP32 = 1
+BLOCK_TOKENS = 16        # tokens of one KV head that share an exponent in a block-scaled cache
 
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "workspace too small",
            4: "CUDA error"}
@@ -78,6 +82,15 @@ _SIGS = {
     "kvq_decode_plan_mt": ["desc", "i32", "i32", "i32", "i32", "i32", "p", "p", "p"],
     "kvq_decode_attn_mt": ["desc", "p", "i32", "i32", "i32", "p", "p", "p", "p", "p", "i32", "p", "f32",
                            "p", "p", "i32", "p", "size", "i32", "p"],
+    "kvq_decode_plan_window": ["desc", "i32", "i32", "i32", "i32", "i32", "i32", "i32", "p", "p", "p"],
+    "kvq_decode_plan_blocks": ["desc", "i32", "i32", "i32", "i32", "i32", "i32", "i32", "p", "p", "p"],
+    "kvq_decode_attn_window": ["desc", "p", "i32", "i32", "i32", "p", "p", "p", "p", "p", "i32", "p",
+                               "f32", "i32", "i32", "p", "p", "i32", "p", "size", "i32", "p"],
+    "kvq_decode_attn_blocks": ["desc", "p", "i32", "i32", "i32", "p", "p", "p", "p", "p", "i32", "p",
+                               "f32", "i32", "i32", "p", "p", "i32", "p", "size", "i32", "p"],
+    "kvq_tag_check_window": ["p", "p", "p", "i32", "i32", "i32", "p", "i32", "i32", "i32", "i32", "p", "p"],
+    "kvq_append_blocks": ["desc", "p", "p", "i32", "p", "p", "i32", "p", "i32", "p", "p", "p", "p", "p", "p"],
+    "kvq_copy_pages": ["desc", "p", "i32", "p", "i32", "p", "p", "i32", "p"],
     "kvq_amax_scales": ["desc", "p", "p", "p", "i32", "p", "p", "p"],
     "kvq_quantize_pages": ["desc", "p", "p", "p", "desc", "p", "p", "p", "i32", "p", "p", "p"],
     "kvq_tag_check_append": ["desc", "p", "p", "p", "i32", "i32", "p", "p", "p", "p", "p", "p",
@@ -308,6 +321,211 @@ def kvq_decode_attn_mt(desc, q, k_cache, v_cache, k_scale, v_scale, block_table,
         ctypes.c_float(softmax_scale), _ptr(abort_flags), _ptr(out), out_dtype, _ptr(workspace),
         ws_bytes, num_splits, _stream(stream))
     _check("kvq_decode_attn_mt", st)
+
+
+def _on_device(fn, stream, *tensors):
+    """The device that holds every tensor (None entries aside), as a context to
+    launch in: ValueError if they are on different devices, or on another one
+    than the given stream."""
+    import torch
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{fn}: expected a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{fn}: tensors on {dev} and {t.device}")
+    if getattr(stream, "device", dev) != dev:
+        raise ValueError(f"{fn}: a stream of {stream.device} for tensors on {dev}")
+    return torch.cuda.device(dev)
+
+
+def _expect_cache(desc: CacheDesc, t, name):
+    import torch
+    _expect(t, torch.uint8 if desc.cache_dtype == KVQ_CACHE_FP8_E4M3 else torch.bfloat16,
+            (desc.num_pages, desc.num_kv_heads, desc.page_size, desc.head_dim), name)
+
+
+def _expect_exps(desc: CacheDesc, t, name):
+    import torch
+    _expect(t, torch.int8, (desc.num_pages, desc.num_kv_heads, desc.page_size // BLOCK_TOKENS), name)
+
+
+def _plan_view(fn, desc, batch, num_query_tokens, num_q_heads, max_pages_per_seq, window, num_sinks,
+               num_splits):
+    a, b, c = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_size_t()
+    st = getattr(load(), fn)(ctypes.byref(desc.c()), batch, num_query_tokens, num_q_heads,
+                             max_pages_per_seq, window, num_sinks, num_splits, ctypes.byref(a),
+                             ctypes.byref(b), ctypes.byref(c))
+    _check(fn, st)
+    return a.value, b.value, c.value
+
+
+def kvq_decode_plan_window(desc: CacheDesc, batch: int, num_query_tokens: int, num_q_heads: int,
+                           max_pages_per_seq: int, window: int, num_sinks: int = 0,
+                           num_splits: int = 0):
+    """(split_tokens, max_splits, workspace_bytes) that kvq_decode_attn_window will use."""
+    return _plan_view("kvq_decode_plan_window", desc, batch, num_query_tokens, num_q_heads,
+                      max_pages_per_seq, window, num_sinks, num_splits)
+
+
+def kvq_decode_plan_blocks(desc: CacheDesc, batch: int, num_query_tokens: int, num_q_heads: int,
+                           max_pages_per_seq: int, window: int = 0, num_sinks: int = 0,
+                           num_splits: int = 0):
+    """(split_tokens, max_splits, workspace_bytes) that kvq_decode_attn_blocks will use."""
+    return _plan_view("kvq_decode_plan_blocks", desc, batch, num_query_tokens, num_q_heads,
+                      max_pages_per_seq, window, num_sinks, num_splits)
+
+
+def workspace_for_window(desc: CacheDesc, batch, num_query_tokens, num_q_heads, max_pages_per_seq,
+                         window, num_sinks=0, num_splits=0, device="cuda"):
+    """Allocate (with torch) the zero-filled workspace of a windowed decode call."""
+    import torch
+    with torch.cuda.device(device):                       # the plan goes by that device's SMs
+        nbytes = kvq_decode_plan_window(desc, batch, num_query_tokens, num_q_heads, max_pages_per_seq,
+                                        window, num_sinks, num_splits)[2]
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def workspace_for_blocks(desc: CacheDesc, batch, num_query_tokens, num_q_heads, max_pages_per_seq,
+                         window=0, num_sinks=0, num_splits=0, device="cuda"):
+    """Allocate (with torch) the zero-filled workspace of a call over the block-scaled cache."""
+    import torch
+    with torch.cuda.device(device):
+        nbytes = kvq_decode_plan_blocks(desc, batch, num_query_tokens, num_q_heads, max_pages_per_seq,
+                                        window, num_sinks, num_splits)[2]
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def _decode_view(fn, desc, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, softmax_scale,
+                 window, num_sinks, abort_flags, out, workspace, num_splits, stream):
+    import torch
+    B, n, Hq, D = q.shape
+    _expect(q, torch.bfloat16, (B, n, Hq, desc.head_dim), "q")
+    _expect_cache(desc, k_cache, "k_cache")
+    _expect_cache(desc, v_cache, "v_cache")
+    maxp = block_table.shape[1]
+    _expect(block_table, torch.int32, (B, maxp), "block_table")
+    _expect(seq_lens, torch.int32, (B,), "seq_lens")
+    if out.dtype not in (torch.bfloat16, torch.float32) or tuple(out.shape) != (B, n, Hq, D):
+        raise ValueError("out: expected bf16 or fp32 [B][n][Hq][D]")
+    if abort_flags is not None:
+        _expect(abort_flags, torch.uint8, (B,), "abort_flags")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _on_device(fn, stream, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                    abort_flags, out, workspace):
+        st = getattr(load(), fn)(
+            ctypes.byref(desc.c()), _ptr(q), B, n, Hq, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+            _ptr(v_scale), _ptr(block_table), maxp, _ptr(seq_lens), ctypes.c_float(softmax_scale),
+            window, num_sinks, _ptr(abort_flags), _ptr(out),
+            KVQ_OUT_FP32 if out.dtype == torch.float32 else KVQ_OUT_BF16, _ptr(workspace), ws_bytes,
+            num_splits, _stream(stream))
+    _check(fn, st)
+    return out
+
+
+def kvq_decode_attn_window(desc: CacheDesc, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                           softmax_scale, window: int, num_sinks: int, abort_flags, out, workspace,
+                           num_splits: int = 0, stream=None):
+    """Decode attention of n query tokens per request (q bf16 [B][n][Hq][D]), each
+    seeing the last ``window`` positions up to its own (0: all) and the first
+    ``num_sinks``, into ``out`` (bf16 or fp32 [B][n][Hq][D])."""
+    import torch
+    if desc.cache_dtype == KVQ_CACHE_FP8_E4M3:
+        _expect(k_scale, torch.float32, (desc.num_kv_heads,), "k_scale")
+        _expect(v_scale, torch.float32, (desc.num_kv_heads,), "v_scale")
+    return _decode_view("kvq_decode_attn_window", desc, q, k_cache, v_cache, k_scale, v_scale, block_table,
+                        seq_lens, softmax_scale, window, num_sinks, abort_flags, out, workspace,
+                        num_splits, stream)
+
+
+def kvq_decode_attn_blocks(desc: CacheDesc, q, k_cache, v_cache, k_exp, v_exp, block_table, seq_lens,
+                           softmax_scale, window: int, num_sinks: int, abort_flags, out, workspace,
+                           num_splits: int = 0, stream=None):
+    """kvq_decode_attn_window over a block-scaled cache: uint8 e4m3 codes with
+    exponents int8 [num_pages][Hkv][page_size / 16] (window 0: every position)."""
+    _expect_exps(desc, k_exp, "k_exp")
+    _expect_exps(desc, v_exp, "v_exp")
+    return _decode_view("kvq_decode_attn_blocks", desc, q, k_cache, v_cache, k_exp, v_exp, block_table,
+                        seq_lens, softmax_scale, window, num_sinks, abort_flags, out, workspace,
+                        num_splits, stream)
+
+
+def kvq_tag_check_window(block_table, expected_tags, seq_lens, page_size: int, page_tags, window: int,
+                         num_sinks: int, num_query_tokens: int, abort_flags, stream=None):
+    """kvq_tag_check over the entries that a window of ``window`` positions with
+    ``num_sinks`` sinks shows a call of ``num_query_tokens`` query tokens."""
+    import torch
+    B, maxp = block_table.shape
+    _expect(block_table, torch.int32, None, "block_table")
+    if expected_tags.element_size() != 4 or tuple(expected_tags.shape) != (B, maxp):
+        raise ValueError("expected_tags: expected 32-bit tags [B][max_pages]")
+    if page_tags.element_size() != 4 or page_tags.dim() != 1:
+        raise ValueError("page_tags: expected 32-bit tags [num_pages]")
+    _expect(seq_lens, torch.int32, (B,), "seq_lens")
+    _expect(abort_flags, torch.uint8, (B,), "abort_flags")
+    fn = "kvq_tag_check_window"
+    with _on_device(fn, stream, block_table, expected_tags, seq_lens, page_tags, abort_flags):
+        st = load().kvq_tag_check_window(_ptr(block_table), _ptr(expected_tags), _ptr(seq_lens), B, maxp,
+                                         page_size, _ptr(page_tags), page_tags.shape[0], window,
+                                         num_sinks, num_query_tokens, _ptr(abort_flags),
+                                         _stream(stream))
+    _check(fn, st)
+
+
+def kvq_append_blocks(desc: CacheDesc, k_new, v_new, token_offsets, block_table, seq_lens, abort_flags,
+                      k_cache, v_cache, k_exp, v_exp, stream=None):
+    """Quantise-on-append into a block-scaled cache: request r's new tokens are
+    rows token_offsets[r] .. token_offsets[r + 1] - 1 of k_new / v_new (bf16
+    [T][Hkv][D]; token_offsets int32 [B + 1], or None for T / B tokens each), at
+    the request's last positions (seq_lens counts them)."""
+    import torch
+    T = k_new.shape[0]
+    B, maxp = block_table.shape
+    _expect(k_new, torch.bfloat16, (T, desc.num_kv_heads, desc.head_dim), "k_new")
+    _expect(v_new, torch.bfloat16, (T, desc.num_kv_heads, desc.head_dim), "v_new")
+    _expect(block_table, torch.int32, None, "block_table")
+    _expect(seq_lens, torch.int32, (B,), "seq_lens")
+    if token_offsets is not None:
+        _expect(token_offsets, torch.int32, (B + 1,), "token_offsets")
+    if abort_flags is not None:
+        _expect(abort_flags, torch.uint8, (B,), "abort_flags")
+    _expect_cache(desc, k_cache, "k_cache")
+    _expect_cache(desc, v_cache, "v_cache")
+    _expect_exps(desc, k_exp, "k_exp")
+    _expect_exps(desc, v_exp, "v_exp")
+    fn = "kvq_append_blocks"
+    with _on_device(fn, stream, k_new, v_new, token_offsets, block_table, seq_lens, abort_flags, k_cache,
+                    v_cache, k_exp, v_exp):
+        st = load().kvq_append_blocks(ctypes.byref(desc.c()), _ptr(k_new), _ptr(v_new), T,
+                                      _ptr(token_offsets), _ptr(block_table), maxp, _ptr(seq_lens), B,
+                                      _ptr(abort_flags), _ptr(k_cache), _ptr(v_cache), _ptr(k_exp),
+                                      _ptr(v_exp), _stream(stream))
+    _check(fn, st)
+
+
+def kvq_copy_pages(desc: CacheDesc, caches, exps, src_pages, dst_pages, stream=None):
+    """Page src_pages[i] becomes page dst_pages[i] in every tensor of ``caches``
+    (K and V caches of any number of layers, all described by ``desc``) and of
+    ``exps`` (their exponents, if the caches are block-scaled; else empty)."""
+    import torch
+    for i, t in enumerate(caches):
+        _expect_cache(desc, t, f"caches[{i}]")
+    for i, t in enumerate(exps):
+        _expect_exps(desc, t, f"exps[{i}]")
+    n = src_pages.numel()
+    _expect(src_pages, torch.int32, (n,), "src_pages")
+    _expect(dst_pages, torch.int32, (n,), "dst_pages")
+    fn = "kvq_copy_pages"
+    with _on_device(fn, stream, src_pages, dst_pages, *caches, *exps):
+        c = (ctypes.c_void_p * max(1, len(caches)))(*[_ptr(t) for t in caches])
+        e = (ctypes.c_void_p * max(1, len(exps)))(*[_ptr(t) for t in exps])
+        st = load().kvq_copy_pages(ctypes.byref(desc.c()), c, len(caches), e, len(exps), _ptr(src_pages),
+                                   _ptr(dst_pages), n, _stream(stream))
+    _check(fn, st)
 
 
 def kvq_decode_attn_append(desc, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,

@@ -172,8 +172,33 @@ int64_t single_wave_splits(int64_t pairs, int64_t max_ctx, int64_t unit, int64_t
 // The most new query tokens per request a multi-token call takes.
 constexpr int kMaxQueryTokens = 16;
 
+// What a call reads of each request's context beyond the plain form: a window
+// with sinks (window 0: everything), and for the block-scaled cache the
+// exponents in place of the per-head scales.
+struct View {
+    int32_t window, num_sinks;
+    bool blocks;
+    const int8_t *k_exp, *v_exp;
+};
+
+// Pages a request of at most max_pages pages can show a call with this
+// window: the sinks' pages, and the window of the call's first query through
+// its last, window + n - 1 positions, which touch at most
+// (window + n - 2) / page_size + 2 pages.
+int32_t visible_pages(const View &v, int32_t page_size, int32_t max_pages, int32_t n_query)
+{
+    if (v.window == 0)
+        return max_pages;
+    const int64_t sinks = (static_cast<int64_t>(v.num_sinks) + page_size - 1) / page_size;
+    const int64_t span = static_cast<int64_t>(v.window) + n_query - 1;
+    const int64_t pages = sinks + (span - 1) / page_size + 2;
+    return pages < max_pages ? static_cast<int32_t>(pages) : max_pages;
+}
+
+// view: null for the calls that read every token with per-head scales.
 kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads,
-                     int32_t max_pages, int32_t num_splits, Plan *p, int32_t n_query = 1)
+                     int32_t max_pages, int32_t num_splits, Plan *p, int32_t n_query = 1,
+                     const View *view = nullptr)
 {
     kvq_status st = check_desc(d);
     if (st != KVQ_OK)
@@ -182,6 +207,13 @@ kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads
         return KVQ_ERR_INVALID_ARG;
     if (n_query > kMaxQueryTokens)
         return KVQ_ERR_UNSUPPORTED;
+    if (view != nullptr) {
+        if (view->window < 0 || view->num_sinks < 0)
+            return KVQ_ERR_INVALID_ARG;
+        if (view->blocks && d->cache_dtype != KVQ_CACHE_FP8_E4M3)
+            return KVQ_ERR_INVALID_ARG;
+        max_pages = visible_pages(*view, d->page_size, max_pages, n_query);
+    }
     if (batch > 65535)
         return KVQ_ERR_UNSUPPORTED;
     if (num_q_heads % d->num_kv_heads != 0)
@@ -195,7 +227,7 @@ kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads
     // Many query rows over an FP8 cache: the tensor-memory kernel, one CTA
     // per (split, request, KV head) for all n g rows, splits in whole
     // 64-token tiles, combined through the workspace.
-    const bool umma = kvq::use_umma(bf16, n_query, g);
+    const bool umma = view == nullptr && kvq::use_umma(bf16, n_query, g);
     const int64_t min_unit = umma ? kvq::kUmmaTileTokens : kChunkTokens;
     const int64_t unit = d->page_size > min_unit ? d->page_size : min_unit;
     // CTAs per split: one per (request, KV head), or in the BF16 multi-token
@@ -337,10 +369,10 @@ kvq_status prepare_decode(const kvq_cache_desc *desc, const void *q, int32_t bat
                           int32_t max_pages_per_seq, const int32_t *seq_lens, float softmax_scale,
                           const uint8_t *abort_flags, void *out, int32_t out_dtype,
                           void *workspace, size_t workspace_bytes, int32_t num_splits,
-                          DecodeCall *call, int32_t n_query = 1)
+                          DecodeCall *call, int32_t n_query = 1, const View *view = nullptr)
 {
     kvq_status st = make_plan(desc, batch, num_q_heads, max_pages_per_seq, num_splits, &call->plan,
-                              n_query);
+                              n_query, view);
     if (st != KVQ_OK)
         return st;
     if (out_dtype != KVQ_OUT_BF16 && out_dtype != KVQ_OUT_FP32)
@@ -351,7 +383,8 @@ kvq_status prepare_decode(const kvq_cache_desc *desc, const void *q, int32_t bat
     if (batch > 0) {
         if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out)
             return KVQ_ERR_INVALID_ARG;
-        if (!bf16 && (!k_scale || !v_scale))
+        const bool blocks = view != nullptr && view->blocks;
+        if (blocks ? !view->k_exp || !view->v_exp : !bf16 && (!k_scale || !v_scale))
             return KVQ_ERR_INVALID_ARG;
         if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
             return KVQ_ERR_INVALID_ARG;
@@ -390,6 +423,10 @@ kvq_status prepare_decode(const kvq_cache_desc *desc, const void *q, int32_t bat
     a.cluster = call->plan.cluster;
     a.n_query = n_query;
     a.row_blocks = call->plan.row_blocks;
+    a.window = view ? view->window : 0;
+    a.num_sinks = view ? view->num_sinks : 0;
+    a.k_exp = view ? view->k_exp : nullptr;
+    a.v_exp = view ? view->v_exp : nullptr;
     a.qk_scale_log2 = softmax_scale * 1.4426950408889634f;
     a.copy_wait_ns = kvq::decode_copy_wait_ns();
     a.out_fp32 = out_dtype == KVQ_OUT_FP32;
@@ -669,6 +706,213 @@ kvq_status kvq_decode_attn_mt(const kvq_cache_desc *desc, const void *q, int32_t
     return to_status(kvq::launch_decode(call.args, km, vm, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+static kvq_status plan_view(const kvq_cache_desc *desc, int32_t batch, int32_t num_query_tokens,
+                            int32_t num_q_heads, int32_t max_pages_per_seq, int32_t num_splits,
+                            const View &view, int32_t *split_tokens, int32_t *max_splits,
+                            size_t *workspace_bytes)
+{
+    Plan p;
+    kvq_status st = make_plan(desc, batch, num_q_heads, max_pages_per_seq, num_splits, &p,
+                              num_query_tokens, &view);
+    if (st != KVQ_OK)
+        return st;
+    if (split_tokens)
+        *split_tokens = p.split_tokens;
+    if (max_splits)
+        *max_splits = p.max_splits;
+    if (workspace_bytes)
+        *workspace_bytes = p.counter_bytes + p.lse_bytes + p.o_bytes;
+    return KVQ_OK;
+}
+
+kvq_status kvq_decode_plan_window(const kvq_cache_desc *desc, int32_t batch, int32_t num_query_tokens,
+                                  int32_t num_q_heads, int32_t max_pages_per_seq, int32_t window,
+                                  int32_t num_sinks, int32_t num_splits, int32_t *split_tokens,
+                                  int32_t *max_splits, size_t *workspace_bytes)
+{
+    const View view = {window, num_sinks, false, nullptr, nullptr};
+    return plan_view(desc, batch, num_query_tokens, num_q_heads, max_pages_per_seq, num_splits, view,
+                     split_tokens, max_splits, workspace_bytes);
+}
+
+kvq_status kvq_decode_plan_blocks(const kvq_cache_desc *desc, int32_t batch, int32_t num_query_tokens,
+                                  int32_t num_q_heads, int32_t max_pages_per_seq, int32_t window,
+                                  int32_t num_sinks, int32_t num_splits, int32_t *split_tokens,
+                                  int32_t *max_splits, size_t *workspace_bytes)
+{
+    const View view = {window, num_sinks, true, nullptr, nullptr};
+    return plan_view(desc, batch, num_query_tokens, num_q_heads, max_pages_per_seq, num_splits, view,
+                     split_tokens, max_splits, workspace_bytes);
+}
+
+kvq_status kvq_decode_attn_window(const kvq_cache_desc *desc, const void *q, int32_t batch,
+                                  int32_t num_query_tokens, int32_t num_q_heads, const void *k_cache,
+                                  const void *v_cache, const float *k_scale, const float *v_scale,
+                                  const int32_t *block_table, int32_t max_pages_per_seq,
+                                  const int32_t *seq_lens, float softmax_scale, int32_t window,
+                                  int32_t num_sinks, const uint8_t *abort_flags, void *out,
+                                  int32_t out_dtype, void *workspace, size_t workspace_bytes,
+                                  int32_t num_splits, kvq_stream_t stream)
+{
+    const View view = {window, num_sinks, false, nullptr, nullptr};
+    DecodeCall call;
+    kvq_status st = prepare_decode(desc, q, batch, num_q_heads, k_cache, v_cache, k_scale, v_scale,
+                                   block_table, max_pages_per_seq, seq_lens, softmax_scale,
+                                   abort_flags, out, out_dtype, workspace, workspace_bytes,
+                                   num_splits, &call, num_query_tokens, &view);
+    if (st != KVQ_OK || batch == 0)
+        return st;
+    CUtensorMap km, vm;
+    if (!make_cache_map(&km, desc, k_cache) || !make_cache_map(&vm, desc, v_cache))
+        return KVQ_ERR_CUDA;
+    return to_status(kvq::launch_decode_window(call.args, km, vm, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_decode_attn_blocks(const kvq_cache_desc *desc, const void *q, int32_t batch,
+                                  int32_t num_query_tokens, int32_t num_q_heads, const void *k_cache,
+                                  const void *v_cache, const int8_t *k_exp, const int8_t *v_exp,
+                                  const int32_t *block_table, int32_t max_pages_per_seq,
+                                  const int32_t *seq_lens, float softmax_scale, int32_t window,
+                                  int32_t num_sinks, const uint8_t *abort_flags, void *out,
+                                  int32_t out_dtype, void *workspace, size_t workspace_bytes,
+                                  int32_t num_splits, kvq_stream_t stream)
+{
+    const View view = {window, num_sinks, true, k_exp, v_exp};
+    DecodeCall call;
+    kvq_status st = prepare_decode(desc, q, batch, num_q_heads, k_cache, v_cache, nullptr, nullptr,
+                                   block_table, max_pages_per_seq, seq_lens, softmax_scale,
+                                   abort_flags, out, out_dtype, workspace, workspace_bytes,
+                                   num_splits, &call, num_query_tokens, &view);
+    if (st != KVQ_OK || batch == 0)
+        return st;
+    CUtensorMap km, vm;
+    if (!make_cache_map(&km, desc, k_cache) || !make_cache_map(&vm, desc, v_cache))
+        return KVQ_ERR_CUDA;
+    return to_status(kvq::launch_decode_blocks(call.args, km, vm, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_tag_check_window(const int32_t *block_table, const uint32_t *expected_tags,
+                                const int32_t *seq_lens, int32_t batch, int32_t max_pages_per_seq,
+                                int32_t page_size, const uint32_t *page_tags, int32_t num_pages,
+                                int32_t window, int32_t num_sinks, int32_t num_query_tokens,
+                                uint8_t *abort_flags, kvq_stream_t stream)
+{
+    if (batch < 0 || max_pages_per_seq <= 0 || page_size <= 0 || num_pages <= 0 || window < 0 ||
+        num_sinks < 0 || num_query_tokens < 1)
+        return KVQ_ERR_INVALID_ARG;
+    if (num_query_tokens > kMaxQueryTokens)
+        return KVQ_ERR_UNSUPPORTED;
+    if (batch == 0)
+        return KVQ_OK;
+    if (!block_table || !expected_tags || !seq_lens || !page_tags || !abort_flags)
+        return KVQ_ERR_INVALID_ARG;
+    kvq::TagWindowArgs a;
+    a.t.block_table = block_table;
+    a.t.expected_tags = expected_tags;
+    a.t.seq_lens = seq_lens;
+    a.t.page_tags = page_tags;
+    a.t.abort_flags = abort_flags;
+    a.t.batch = batch;
+    a.t.max_pages_per_seq = max_pages_per_seq;
+    a.t.page_size = page_size;
+    a.t.num_pages = num_pages;
+    a.window = window;
+    a.num_sinks = num_sinks;
+    a.num_query_tokens = num_query_tokens;
+    return to_status(kvq::launch_tag_check_window(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_append_blocks(const kvq_cache_desc *desc, const void *k_new, const void *v_new,
+                             int32_t num_tokens, const int32_t *token_offsets,
+                             const int32_t *block_table, int32_t max_pages_per_seq,
+                             const int32_t *seq_lens, int32_t batch, const uint8_t *abort_flags,
+                             void *k_cache, void *v_cache, int8_t *k_exp, int8_t *v_exp,
+                             kvq_stream_t stream)
+{
+    kvq_status st = check_desc(desc);
+    if (st != KVQ_OK)
+        return st;
+    if (desc->cache_dtype != KVQ_CACHE_FP8_E4M3)
+        return KVQ_ERR_INVALID_ARG;
+    if (num_tokens < 0 || batch < 0 || max_pages_per_seq <= 0)
+        return KVQ_ERR_INVALID_ARG;
+    if (batch == 0 && num_tokens != 0)
+        return KVQ_ERR_INVALID_ARG;
+    if (batch > 65535 || desc->num_kv_heads > 65535 * 4)   // the grid's second dimension: 8 of 2 Hkv each
+        return KVQ_ERR_UNSUPPORTED;
+    if (batch == 0 || num_tokens == 0)
+        return KVQ_OK;
+    if (!token_offsets && num_tokens % batch != 0)
+        return KVQ_ERR_INVALID_ARG;
+    if (!k_new || !v_new || !block_table || !seq_lens || !k_cache || !v_cache || !k_exp || !v_exp)
+        return KVQ_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache))
+        return KVQ_ERR_INVALID_ARG;
+    kvq::AppendBlocksArgs a;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.token_offsets = token_offsets;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.abort_flags = abort_flags;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_exp = k_exp;
+    a.v_exp = v_exp;
+    a.num_tokens = num_tokens;
+    a.batch = batch;
+    a.max_pages_per_seq = max_pages_per_seq;
+    a.num_kv_heads = desc->num_kv_heads;
+    a.page_size = desc->page_size;
+    a.num_pages = desc->num_pages;
+    return to_status(kvq::launch_append_blocks(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_copy_pages(const kvq_cache_desc *desc, void *const *caches, int32_t num_caches,
+                          void *const *exps, int32_t num_exps, const int32_t *src_pages,
+                          const int32_t *dst_pages, int32_t num_listed, kvq_stream_t stream)
+{
+    kvq_status st = check_desc(desc);
+    if (st != KVQ_OK)
+        return st;
+    if (num_caches < 0 || num_exps < 0 || num_listed < 0)
+        return KVQ_ERR_INVALID_ARG;
+    if (num_exps > 0 && desc->cache_dtype != KVQ_CACHE_FP8_E4M3)
+        return KVQ_ERR_INVALID_ARG;
+    if ((num_caches > 0 && !caches) || (num_exps > 0 && !exps))
+        return KVQ_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < num_caches; ++i)
+        if (!caches[i] || !aligned16(caches[i]))
+            return KVQ_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < num_exps; ++i)
+        if (!exps[i])
+            return KVQ_ERR_INVALID_ARG;
+    if (num_listed == 0 || num_caches + static_cast<int64_t>(num_exps) == 0)
+        return KVQ_OK;
+    if (!src_pages || !dst_pages)
+        return KVQ_ERR_INVALID_ARG;
+    const int64_t row = static_cast<int64_t>(desc->num_kv_heads) * desc->page_size;
+    kvq::CopyPagesArgs a;
+    a.src_pages = src_pages;
+    a.dst_pages = dst_pages;
+    a.cache_page_bytes = row * kHeadDim * (desc->cache_dtype == KVQ_CACHE_BF16 ? 2 : 1);
+    a.exp_page_bytes = row / kvq::kBlockTokens;
+    a.num_listed = num_listed;
+    a.num_pages = desc->num_pages;
+    const int64_t total = static_cast<int64_t>(num_caches) + num_exps;
+    for (int64_t at = 0; at < total; at += kvq::kCopyMaxArrays) {    // kCopyMaxArrays arrays per launch
+        a.num_caches = a.num_exps = 0;
+        for (int64_t i = at; i < total && i < at + kvq::kCopyMaxArrays; ++i) {
+            a.arrays[i - at] = i < num_caches ? caches[i] : exps[i - num_caches];
+            ++(i < num_caches ? a.num_caches : a.num_exps);
+        }
+        const cudaError_t e = kvq::launch_copy_pages(a, reinterpret_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess)
+            return KVQ_ERR_CUDA;
+    }
+    return KVQ_OK;
+}
+
 kvq_status kvq_decode_attn_append(const kvq_cache_desc *desc, const void *q, int32_t batch,
                                   int32_t num_q_heads, void *k_cache, void *v_cache,
                                   const float *k_scale, const float *v_scale,
@@ -754,14 +998,18 @@ KVQ_API kvq_status kvq_phase_stamps(int32_t which, unsigned long long *host, siz
 
 kvq_status kvq_device_error(uint32_t *bits, int32_t clear)
 {
-    uint32_t a = 0, b = 0, c = 0;
+    uint32_t a = 0, b = 0, c = 0, d = 0, f = 0;
     cudaError_t e = kvq::read_device_error(&a, clear != 0);
     if (e == cudaSuccess)
         e = kvq::read_w4_error(&b, clear != 0);
     if (e == cudaSuccess)
         e = kvq::read_umma_error(&c, clear != 0);
+    if (e == cudaSuccess)
+        e = kvq::read_window_error(&d, clear != 0);
+    if (e == cudaSuccess)
+        e = kvq::read_blocks_error(&f, clear != 0);
     if (bits)
-        *bits = a | b | c;
+        *bits = a | b | c | d | f;
     return to_status(e);
 }
 

@@ -11,6 +11,8 @@ namespace kvq {
 
 constexpr int kHeadDim = 128;
 constexpr int kChunkTokens = 32;     // tokens one warp consumes per pipeline stage
+constexpr int kBlockTokens = 16;     // tokens of one KV head that share an exponent (block-scaled cache)
+constexpr int kBlockExpMin = -48, kBlockExpMax = 48;   // exponents the append makes
 constexpr int kMaxGroup = 8;         // query heads per KV head on one mma n-tile
 constexpr int kMaxCluster = 8;       // splits merged inside one thread-block cluster
 constexpr int kMaxSplitsTotal = 1024;  // splits of one (request, KV head)
@@ -53,6 +55,38 @@ cudaError_t launch_quantize_pages(const HandoffArgs &a, cudaStream_t stream);
 // Tag check of every request, then the append of token r for request r
 // unless it was aborted (decode step: one new token per request).
 cudaError_t launch_tag_check_append(const TagCheckArgs &t, const AppendArgs &a, cudaStream_t stream);
+
+// The tag check of requests that hold only the pages a window shows.
+struct TagWindowArgs {
+    TagCheckArgs t;
+    int32_t window, num_sinks, num_query_tokens;
+};
+cudaError_t launch_tag_check_window(const TagWindowArgs &a, cudaStream_t stream);
+
+// Quantise-on-append into the block-scaled cache.
+struct AppendBlocksArgs {
+    const void *k_new, *v_new;       // bf16 [num_tokens][Hkv][D]
+    const int32_t *token_offsets;    // [batch + 1], or null: num_tokens / batch tokens per request
+    const int32_t *block_table;      // [batch][max_pages]
+    const int32_t *seq_lens;         // [batch], the new tokens included
+    const uint8_t *abort_flags;      // [batch] or null
+    void *k_cache, *v_cache;         // e4m3 codes
+    int8_t *k_exp, *v_exp;           // [num_pages][Hkv][page_size / 16]
+    int32_t num_tokens, batch, max_pages_per_seq, num_kv_heads, page_size, num_pages;
+};
+cudaError_t launch_append_blocks(const AppendBlocksArgs &a, cudaStream_t stream);
+
+// Pages copied inside every cache of a pool.  One launch takes kCopyMaxArrays
+// arrays: num_caches of cache_page_bytes per page (a multiple of 2,048), then
+// num_exps of exp_page_bytes.
+constexpr int kCopyMaxArrays = 256;
+struct CopyPagesArgs {
+    void *arrays[kCopyMaxArrays];
+    const int32_t *src_pages, *dst_pages;   // [num_listed]
+    int64_t cache_page_bytes, exp_page_bytes;
+    int32_t num_caches, num_exps, num_listed, num_pages;
+};
+cudaError_t launch_copy_pages(const CopyPagesArgs &a, cudaStream_t stream);
 
 // INT4 weight-only product y[m][n] = sum_k x[m][k] q[n][k] s[n][k / 128] for
 // up to 16 rows of x per launch.  The weights are read through a 2-D tensor
@@ -104,6 +138,9 @@ struct DecodeArgs {
     uint8_t *abort_out;              // abort_flags (if any) is read instead
     int32_t n_query;                 // new query tokens per request (q, out: [B][n_query][Hq][D])
     int32_t row_blocks;              // CTAs per (split, request, KV head): ceil(n_query * g / 8)
+    int32_t window, num_sinks;       // windowed builds: last positions a query sees (0: all) and
+                                     // first positions that stay visible
+    const int8_t *k_exp, *v_exp;     // block-scaled cache: [num_pages][Hkv][page_size / 16]
     float qk_scale_log2;             // softmax_scale * log2(e)
     uint64_t copy_wait_ns;           // a consumer's limit on one copy wait (0: give up at once)
     bool out_fp32, bf16_cache;
@@ -121,6 +158,15 @@ uint64_t decode_copy_wait_ns();
 // swizzle.
 cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                           cudaStream_t stream);
+// The same kernel's builds with a window (any cache of launch_decode) and for
+// the block-scaled cache (a window or none); the plan is made for the pages
+// that visible_pages says a request can show.
+cudaError_t launch_decode_window(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                                 cudaStream_t stream);
+cudaError_t launch_decode_blocks(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                                 cudaStream_t stream);
+cudaError_t read_window_error(uint32_t *bits, bool clear);
+cudaError_t read_blocks_error(uint32_t *bits, bool clear);
 // Resident decode CTAs per SM for the cache type (occupancy of the kernel;
 // multi: the multi-token build, 16 query rows per CTA).
 int decode_ctas_per_sm(bool bf16_cache, bool multi = false);

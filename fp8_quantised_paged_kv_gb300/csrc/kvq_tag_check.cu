@@ -47,7 +47,67 @@ __global__ void __launch_bounds__(kTagThreads) tag_check_kernel(TagCheckArgs a)
     KVQ_TAG_STAMP(1);
 }
 
+// The check of a request that holds only the pages a window shows: the entries
+// of the sinks' pages, then those from the page where the window of the
+// request's first new token starts.  The entries between are not read (their
+// pages may have been given back).  The visible entries are numbered in one
+// run, so a pass takes 2,048 of them whatever the hole; unlike the check of
+// every entry it needs the length before its first table load (three rounds
+// of dependent loads).
+constexpr int kWindowUnroll = 4;
+__global__ void __launch_bounds__(kTagThreads) tag_check_window_kernel(const TagWindowArgs w)
+{
+    grid_launch_dependents();              // a dependent decode launch may begin now
+    const TagCheckArgs &a = w.t;
+    const int64_t r = blockIdx.x;
+    const int32_t *bt = a.block_table + r * a.max_pages_per_seq;
+    const uint32_t *exp = a.expected_tags + r * a.max_pages_per_seq;
+    const int32_t seq = a.seq_lens[r];
+    const int64_t len = seq > 0 ? seq : 0;
+    int64_t used = (len + a.page_size - 1) / a.page_size;
+    bool bad = used > a.max_pages_per_seq;
+    if (bad)
+        used = a.max_pages_per_seq;
+    int64_t sink_pages = used, hole = 0;                   // window 0: every entry
+    if (w.window > 0) {
+        const int64_t w0 = max(len - w.num_query_tokens + 1 - w.window, static_cast<int64_t>(0));
+        sink_pages = (min(len, static_cast<int64_t>(w.num_sinks)) + a.page_size - 1) / a.page_size;
+        hole = max(w0 / a.page_size - sink_pages, static_cast<int64_t>(0));
+    }
+    const int64_t seen = used - hole;
+    for (int64_t base = 0; base < seen; base += kTagThreads * kWindowUnroll) {
+        int32_t p[kWindowUnroll];
+        uint32_t want[kWindowUnroll], live[kWindowUnroll];
+        bool look[kWindowUnroll];
+#pragma unroll
+        for (int k = 0; k < kWindowUnroll; ++k) {
+            const int64_t v = base + k * kTagThreads + threadIdx.x;
+            const int64_t i = v < sink_pages ? v : v + hole;
+            look[k] = v < seen;
+            p[k] = look[k] ? __ldg(bt + i) : 0;
+            want[k] = look[k] ? __ldg(exp + i) : 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < kWindowUnroll; ++k)
+            live[k] = look[k] && p[k] >= 0 && p[k] < a.num_pages ? __ldg(a.page_tags + p[k]) : 0u;
+#pragma unroll
+        for (int k = 0; k < kWindowUnroll; ++k)
+            bad |= look[k] && (p[k] < 0 || p[k] >= a.num_pages || live[k] != want[k]);
+    }
+    const bool any = __syncthreads_or(bad) != 0;
+    if (threadIdx.x == 0)
+        a.abort_flags[r] = any ? 1 : 0;
+}
+
 } // namespace
+
+cudaError_t launch_tag_check_window(const TagWindowArgs &a, cudaStream_t stream)
+{
+    if (a.t.batch == 0)
+        return cudaSuccess;
+    tag_check_window_kernel<<<static_cast<unsigned>(a.t.batch), kTagThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_tag_check(const TagCheckArgs &a, cudaStream_t stream)
 {

@@ -1,7 +1,9 @@
 /*
  * kvq.h -- C ABI of the FP8 paged-KV decode path for GB300 (sm_103a).
  *
- * Three operations, each one hand-written CUDA kernel family:
+ * Three operations, each one hand-written CUDA kernel family, and the calls
+ * built around them (fused forms, several query tokens, a sliding window, a
+ * cache scaled by blocks, page copies):
  *
  *   kvq_tag_check    per-page integrity tags: the separate batched check that
  *                    runs before decode reads the cache and aborts a request
@@ -43,6 +45,12 @@
  *     (page, KV head) tile is one contiguous run of page_size * head_dim
  *     elements.  A token at logical position j of request r lives in page
  *     block_table[r][j / page_size], slot j % page_size.
+ *   - A block-scaled cache (kvq_append_blocks, kvq_decode_attn_blocks) is an
+ *     e4m3 cache of the same layout whose scales are exponents,
+ *     exp[num_pages][num_kv_heads][page_size / 16] int8 for K and for V: slots
+ *     16 b .. 16 b + 15 of a (page, KV head) tile share exp[page][head][b], and
+ *     a code c there stands for c * 2^exp.  Its descriptor says
+ *     KVQ_CACHE_FP8_E4M3; exponent arrays need no alignment.
  *   - Supported: head_dim 128; page_size 16, 32, 64 or 128; query heads per
  *     KV head (g = num_q_heads / num_kv_heads) 1 to 8; up to 65535 requests
  *     per decode call.  Others return KVQ_ERR_UNSUPPORTED.
@@ -309,6 +317,161 @@ KVQ_API kvq_status kvq_decode_attn_mt(const kvq_cache_desc *desc, const void *q,
                                       const uint8_t *abort_flags, void *out, int32_t out_dtype,
                                       void *workspace, size_t workspace_bytes, int32_t num_splits,
                                       kvq_stream_t stream);
+
+/*
+ * kvq_decode_plan_window / kvq_decode_attn_window -- decode attention behind a
+ * sliding window whose first tokens stay visible (sinks), for the
+ * n = num_query_tokens last positions of each request (1 to 16, as in
+ * kvq_decode_attn_mt): query token i, at position p = seq_lens[r] - n + i, sees
+ *   { j <= p : j < num_sinks or j > p - window },
+ * its own position among them.  window = 0: no window, every j <= p (num_sinks
+ * is then ignored).
+ *
+ *   window, num_sinks   0 or more (KVQ_ERR_INVALID_ARG below).
+ *   block_table    only the entries of pages that hold a position some query
+ *                  of the call sees are read: those of positions below
+ *                  num_sinks, and those from the first query's window start
+ *                  on.  The entries between may hold anything (-1, say, for
+ *                  pages that were given back), and a row needs them only as
+ *                  places: entry j / page_size is still position j's.
+ *   seq_lens       the whole context, tokens outside the window included.
+ *   Every other argument as in kvq_decode_attn_mt, with either cache type; the
+ *   workspace size comes from kvq_decode_plan_window with the same window,
+ *   num_sinks and n.  The plan's max_splits and splits count the tokens that
+ *   a request can show, not its whole context.
+ * A query that sees no position gets zeros, as does every query of a request
+ * that is aborted, empty, longer than its table row or that names a page
+ * outside [0, num_pages) in an entry the call reads.  What positions outside
+ * every query's view hold (NaN, infinities) does not matter; a NaN in a
+ * position that a query sees reaches its output, and one in the V row of a
+ * position that only some of a request's queries see may reach the others.
+ * Only the visible tokens' pages are read: the time goes with min(context,
+ * window + num_sinks), not with the context.
+ */
+KVQ_API kvq_status kvq_decode_plan_window(const kvq_cache_desc *desc, int32_t batch,
+                                          int32_t num_query_tokens, int32_t num_q_heads,
+                                          int32_t max_pages_per_seq, int32_t window,
+                                          int32_t num_sinks, int32_t num_splits,
+                                          int32_t *split_tokens, int32_t *max_splits,
+                                          size_t *workspace_bytes);
+KVQ_API kvq_status kvq_decode_attn_window(const kvq_cache_desc *desc, const void *q, int32_t batch,
+                                          int32_t num_query_tokens, int32_t num_q_heads,
+                                          const void *k_cache, const void *v_cache,
+                                          const float *k_scale, const float *v_scale,
+                                          const int32_t *block_table, int32_t max_pages_per_seq,
+                                          const int32_t *seq_lens, float softmax_scale,
+                                          int32_t window, int32_t num_sinks,
+                                          const uint8_t *abort_flags, void *out, int32_t out_dtype,
+                                          void *workspace, size_t workspace_bytes,
+                                          int32_t num_splits, kvq_stream_t stream);
+
+/*
+ * kvq_tag_check_window -- kvq_tag_check of requests that hold only the pages a
+ * window shows: the flag of request r looks at the entries of positions below
+ * min(num_sinks, seq_lens[r]) and at those from position
+ * max(0, seq_lens[r] - num_query_tokens + 1 - window) to the last used one --
+ * exactly the entries that kvq_decode_attn_window (and kvq_decode_attn_blocks)
+ * with the same window, num_sinks and number of query tokens reads.  window =
+ * 0 looks at every used entry.  Arguments as in kvq_tag_check.
+ */
+KVQ_API kvq_status kvq_tag_check_window(const int32_t *block_table, const uint32_t *expected_tags,
+                                        const int32_t *seq_lens, int32_t batch,
+                                        int32_t max_pages_per_seq, int32_t page_size,
+                                        const uint32_t *page_tags, int32_t num_pages, int32_t window,
+                                        int32_t num_sinks, int32_t num_query_tokens,
+                                        uint8_t *abort_flags, kvq_stream_t stream);
+
+/*
+ * kvq_append_blocks -- quantise-on-append into a block-scaled cache: the new
+ * tokens of each request, one in a decode step or any number in a prompt, at
+ * the request's last positions.
+ *
+ *   k_new, v_new   bf16 [num_tokens][Hkv][D], the requests' tokens one request
+ *                  after another.
+ *   token_offsets  int32 [batch + 1]: request r's new tokens are rows
+ *                  token_offsets[r] .. token_offsets[r + 1] - 1 (ascending;
+ *                  none is allowed).  NULL: num_tokens / batch tokens each
+ *                  (KVQ_ERR_INVALID_ARG unless that is a whole number).
+ *   block_table, max_pages_per_seq   as in kvq_tag_check.
+ *   seq_lens       int32 [batch], the request's length with its n new tokens:
+ *                  they take positions seq_lens[r] - n .. seq_lens[r] - 1.
+ *   abort_flags    uint8 [batch] or NULL; a set flag skips the request.
+ *   k_cache, v_cache, k_exp, v_exp   written: see the block-scaled cache above.
+ * For each block (16 positions, one KV head, K or V) that gets a token:
+ *   need = the least e in [-48, 48] with amax <= 448 * 2^e, amax the largest
+ *          magnitude of the block's new tokens (NaN passed over; -48 if all
+ *          are 0, 48 if even that is too small);
+ *   e    = need if the block's first position is among the new tokens, else
+ *          max(exp, need) with exp the block's stored exponent;
+ *   the rows of the block's earlier positions become e4m3(c * 2^(exp - e))
+ *   where e > exp; the new rows are e4m3(x * 2^-e), rounded to nearest even and
+ *   saturating at +-448 (a NaN stays NaN); exp becomes e.
+ * Rows behind the request's last position are left as they were.  A request
+ * is skipped if it is longer than its table row, has fewer positions than new
+ * tokens, or has offsets outside [0, num_tokens] or descending; a block is
+ * skipped if its page id is outside [0, num_pages).  A block may be rewritten
+ * whole, so two requests must not append into a page they share: give one of
+ * them a copy first (kvq_copy_pages).
+ */
+KVQ_API kvq_status kvq_append_blocks(const kvq_cache_desc *desc, const void *k_new, const void *v_new,
+                                     int32_t num_tokens, const int32_t *token_offsets,
+                                     const int32_t *block_table, int32_t max_pages_per_seq,
+                                     const int32_t *seq_lens, int32_t batch,
+                                     const uint8_t *abort_flags, void *k_cache, void *v_cache,
+                                     int8_t *k_exp, int8_t *v_exp, kvq_stream_t stream);
+
+/*
+ * kvq_decode_plan_blocks / kvq_decode_attn_blocks -- kvq_decode_attn_window over
+ * a block-scaled cache:
+ *   s_j = softmax_scale * <q, c^K_j> 2^ek(j),   out = sum_j p_j c^V_j 2^ev(j) / sum_j p_j,
+ *   p_j = exp(s_j - max s),
+ * over the positions j that the query sees, ek(j) and ev(j) the exponents of
+ * position j's block.
+ *   k_exp, v_exp   int8 [num_pages][Hkv][page_size / 16].  Exponents of
+ *                  [-48, 48] (what kvq_append_blocks makes) keep the stated
+ *                  accuracy; others are read as they are, down to -126.
+ *   Every other argument, the window, the sinks and the plan as in
+ *   kvq_decode_attn_window, with KVQ_CACHE_FP8_E4M3 only.
+ */
+KVQ_API kvq_status kvq_decode_plan_blocks(const kvq_cache_desc *desc, int32_t batch,
+                                          int32_t num_query_tokens, int32_t num_q_heads,
+                                          int32_t max_pages_per_seq, int32_t window,
+                                          int32_t num_sinks, int32_t num_splits,
+                                          int32_t *split_tokens, int32_t *max_splits,
+                                          size_t *workspace_bytes);
+KVQ_API kvq_status kvq_decode_attn_blocks(const kvq_cache_desc *desc, const void *q, int32_t batch,
+                                          int32_t num_query_tokens, int32_t num_q_heads,
+                                          const void *k_cache, const void *v_cache,
+                                          const int8_t *k_exp, const int8_t *v_exp,
+                                          const int32_t *block_table, int32_t max_pages_per_seq,
+                                          const int32_t *seq_lens, float softmax_scale,
+                                          int32_t window, int32_t num_sinks,
+                                          const uint8_t *abort_flags, void *out, int32_t out_dtype,
+                                          void *workspace, size_t workspace_bytes,
+                                          int32_t num_splits, kvq_stream_t stream);
+
+/*
+ * kvq_copy_pages -- page src_pages[i] of every listed cache becomes page
+ * dst_pages[i] of the same cache: a fork's own copy of a last page that it
+ * will append to, or pages moved to close gaps.
+ *
+ *   desc           shape and type that all the caches share.
+ *   caches         HOST array of num_caches device pointers (16-byte aligned):
+ *                  K and V caches, of any number of layers.
+ *   exps           HOST array of num_exps device pointers, the exponent arrays
+ *                  of block-scaled caches (num_exps 0 and NULL if there are
+ *                  none; KVQ_ERR_INVALID_ARG with a bf16 descriptor).
+ *   src_pages, dst_pages   int32 [num_listed].  A pair with an id outside
+ *                  [0, num_pages) is skipped; a pair with equal ids changes
+ *                  nothing.
+ * A source may be listed more than once.  A destination listed twice, or a
+ * page that is a destination of one pair and a source of another, races: the
+ * caller must not do that.  Both host arrays are read before the call
+ * returns.
+ */
+KVQ_API kvq_status kvq_copy_pages(const kvq_cache_desc *desc, void *const *caches, int32_t num_caches,
+                                  void *const *exps, int32_t num_exps, const int32_t *src_pages,
+                                  const int32_t *dst_pages, int32_t num_listed, kvq_stream_t stream);
 
 /*
  * kvq_decode_attn_append -- kvq_append of each request's new token followed
