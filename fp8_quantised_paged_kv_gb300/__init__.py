@@ -1,6 +1,7 @@
 """Python binding of the FP8 paged-KV decode path (libkvq.so, sm_103a).
 
-Argument marshalling only: every step runs in the CUDA kernels behind the C
+Argument marshalling only (through ctypes; for the block-scaled, windowed and
+page-copy calls in a small native extension, csrc/kvq_binding.cpp): every step runs in the CUDA kernels behind the C
 ABI declared in ``include/kvq.h``.  Functions carry the C names and take
 torch CUDA tensors (device memory, PyTorch's streams); nothing here computes
 on the host, and there is no CPU fallback -- if the library or a GPU is
@@ -25,13 +26,12 @@ import ctypes
 import dataclasses
 import os
 
-from .build import LIB, build
+from .build import LIB, NATIVE, build
 
 KVQ_CACHE_FP8_E4M3 = 0
 KVQ_CACHE_BF16 = 1
 KVQ_OUT_BF16 = 0
 KVQ_OUT_FP32 = 1
-BLOCK_TOKENS = 16        # tokens of one KV head that share an exponent in a block-scaled cache
 
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "workspace too small",
            4: "CUDA error"}
@@ -323,37 +323,6 @@ def kvq_decode_attn_mt(desc, q, k_cache, v_cache, k_scale, v_scale, block_table,
     _check("kvq_decode_attn_mt", st)
 
 
-def _on_device(fn, stream, *tensors):
-    """The device that holds every tensor (None entries aside), as a context to
-    launch in: ValueError if they are on different devices, or on another one
-    than the given stream."""
-    import torch
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{fn}: expected a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{fn}: tensors on {dev} and {t.device}")
-    if getattr(stream, "device", dev) != dev:
-        raise ValueError(f"{fn}: a stream of {stream.device} for tensors on {dev}")
-    return torch.cuda.device(dev)
-
-
-def _expect_cache(desc: CacheDesc, t, name):
-    import torch
-    _expect(t, torch.uint8 if desc.cache_dtype == KVQ_CACHE_FP8_E4M3 else torch.bfloat16,
-            (desc.num_pages, desc.num_kv_heads, desc.page_size, desc.head_dim), name)
-
-
-def _expect_exps(desc: CacheDesc, t, name):
-    import torch
-    _expect(t, torch.int8, (desc.num_pages, desc.num_kv_heads, desc.page_size // BLOCK_TOKENS), name)
-
-
 def _plan_view(fn, desc, batch, num_query_tokens, num_q_heads, max_pages_per_seq, window, num_sinks,
                num_splits):
     a, b, c = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_size_t()
@@ -400,31 +369,26 @@ def workspace_for_blocks(desc: CacheDesc, batch, num_query_tokens, num_q_heads, 
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
 
 
-def _decode_view(fn, desc, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, softmax_scale,
-                 window, num_sinks, abort_flags, out, workspace, num_splits, stream):
-    import torch
-    B, n, Hq, D = q.shape
-    _expect(q, torch.bfloat16, (B, n, Hq, desc.head_dim), "q")
-    _expect_cache(desc, k_cache, "k_cache")
-    _expect_cache(desc, v_cache, "v_cache")
-    maxp = block_table.shape[1]
-    _expect(block_table, torch.int32, (B, maxp), "block_table")
-    _expect(seq_lens, torch.int32, (B,), "seq_lens")
-    if out.dtype not in (torch.bfloat16, torch.float32) or tuple(out.shape) != (B, n, Hq, D):
-        raise ValueError("out: expected bf16 or fp32 [B][n][Hq][D]")
-    if abort_flags is not None:
-        _expect(abort_flags, torch.uint8, (B,), "abort_flags")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _on_device(fn, stream, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
-                    abort_flags, out, workspace):
-        st = getattr(load(), fn)(
-            ctypes.byref(desc.c()), _ptr(q), B, n, Hq, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-            _ptr(v_scale), _ptr(block_table), maxp, _ptr(seq_lens), ctypes.c_float(softmax_scale),
-            window, num_sinks, _ptr(abort_flags), _ptr(out),
-            KVQ_OUT_FP32 if out.dtype == torch.float32 else KVQ_OUT_BF16, _ptr(workspace), ws_bytes,
-            num_splits, _stream(stream))
-    _check(fn, st)
-    return out
+_native = None
+_NATIVE_CALLS = ("kvq_decode_attn_window", "kvq_decode_attn_blocks", "kvq_tag_check_window",
+                 "kvq_append_blocks", "kvq_copy_pages")
+
+
+def _load_native():
+    """The native marshalling (built beside the library), bound to the loaded library."""
+    global _native
+    import importlib.util
+
+    import torch  # noqa: F401  (its libraries, which the extension uses)
+    lib = load()
+    if not os.path.exists(NATIVE):
+        build()
+    spec = importlib.util.spec_from_file_location("_kvq_native", NATIVE)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NATIVE_CALLS])
+    _native = mod
+    return mod
 
 
 def kvq_decode_attn_window(desc: CacheDesc, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
@@ -433,13 +397,12 @@ def kvq_decode_attn_window(desc: CacheDesc, q, k_cache, v_cache, k_scale, v_scal
     """Decode attention of n query tokens per request (q bf16 [B][n][Hq][D]), each
     seeing the last ``window`` positions up to its own (0: all) and the first
     ``num_sinks``, into ``out`` (bf16 or fp32 [B][n][Hq][D])."""
-    import torch
-    if desc.cache_dtype == KVQ_CACHE_FP8_E4M3:
-        _expect(k_scale, torch.float32, (desc.num_kv_heads,), "k_scale")
-        _expect(v_scale, torch.float32, (desc.num_kv_heads,), "v_scale")
-    return _decode_view("kvq_decode_attn_window", desc, q, k_cache, v_cache, k_scale, v_scale, block_table,
-                        seq_lens, softmax_scale, window, num_sinks, abort_flags, out, workspace,
-                        num_splits, stream)
+    st = (_native or _load_native()).decode_attn_window(
+        desc, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, softmax_scale, window, num_sinks,
+        abort_flags, out, workspace, num_splits, stream)
+    if st:
+        _check("kvq_decode_attn_window", st)
+    return out
 
 
 def kvq_decode_attn_blocks(desc: CacheDesc, q, k_cache, v_cache, k_exp, v_exp, block_table, seq_lens,
@@ -447,33 +410,23 @@ def kvq_decode_attn_blocks(desc: CacheDesc, q, k_cache, v_cache, k_exp, v_exp, b
                            num_splits: int = 0, stream=None):
     """kvq_decode_attn_window over a block-scaled cache: uint8 e4m3 codes with
     exponents int8 [num_pages][Hkv][page_size / 16] (window 0: every position)."""
-    _expect_exps(desc, k_exp, "k_exp")
-    _expect_exps(desc, v_exp, "v_exp")
-    return _decode_view("kvq_decode_attn_blocks", desc, q, k_cache, v_cache, k_exp, v_exp, block_table,
-                        seq_lens, softmax_scale, window, num_sinks, abort_flags, out, workspace,
-                        num_splits, stream)
+    st = (_native or _load_native()).decode_attn_blocks(
+        desc, q, k_cache, v_cache, k_exp, v_exp, block_table, seq_lens, softmax_scale, window, num_sinks,
+        abort_flags, out, workspace, num_splits, stream)
+    if st:
+        _check("kvq_decode_attn_blocks", st)
+    return out
 
 
 def kvq_tag_check_window(block_table, expected_tags, seq_lens, page_size: int, page_tags, window: int,
                          num_sinks: int, num_query_tokens: int, abort_flags, stream=None):
     """kvq_tag_check over the entries that a window of ``window`` positions with
     ``num_sinks`` sinks shows a call of ``num_query_tokens`` query tokens."""
-    import torch
-    B, maxp = block_table.shape
-    _expect(block_table, torch.int32, None, "block_table")
-    if expected_tags.element_size() != 4 or tuple(expected_tags.shape) != (B, maxp):
-        raise ValueError("expected_tags: expected 32-bit tags [B][max_pages]")
-    if page_tags.element_size() != 4 or page_tags.dim() != 1:
-        raise ValueError("page_tags: expected 32-bit tags [num_pages]")
-    _expect(seq_lens, torch.int32, (B,), "seq_lens")
-    _expect(abort_flags, torch.uint8, (B,), "abort_flags")
-    fn = "kvq_tag_check_window"
-    with _on_device(fn, stream, block_table, expected_tags, seq_lens, page_tags, abort_flags):
-        st = load().kvq_tag_check_window(_ptr(block_table), _ptr(expected_tags), _ptr(seq_lens), B, maxp,
-                                         page_size, _ptr(page_tags), page_tags.shape[0], window,
-                                         num_sinks, num_query_tokens, _ptr(abort_flags),
-                                         _stream(stream))
-    _check(fn, st)
+    st = (_native or _load_native()).tag_check_window(
+        block_table, expected_tags, seq_lens, page_size, page_tags, window, num_sinks, num_query_tokens,
+        abort_flags, stream)
+    if st:
+        _check("kvq_tag_check_window", st)
 
 
 def kvq_append_blocks(desc: CacheDesc, k_new, v_new, token_offsets, block_table, seq_lens, abort_flags,
@@ -482,50 +435,20 @@ def kvq_append_blocks(desc: CacheDesc, k_new, v_new, token_offsets, block_table,
     rows token_offsets[r] .. token_offsets[r + 1] - 1 of k_new / v_new (bf16
     [T][Hkv][D]; token_offsets int32 [B + 1], or None for T / B tokens each), at
     the request's last positions (seq_lens counts them)."""
-    import torch
-    T = k_new.shape[0]
-    B, maxp = block_table.shape
-    _expect(k_new, torch.bfloat16, (T, desc.num_kv_heads, desc.head_dim), "k_new")
-    _expect(v_new, torch.bfloat16, (T, desc.num_kv_heads, desc.head_dim), "v_new")
-    _expect(block_table, torch.int32, None, "block_table")
-    _expect(seq_lens, torch.int32, (B,), "seq_lens")
-    if token_offsets is not None:
-        _expect(token_offsets, torch.int32, (B + 1,), "token_offsets")
-    if abort_flags is not None:
-        _expect(abort_flags, torch.uint8, (B,), "abort_flags")
-    _expect_cache(desc, k_cache, "k_cache")
-    _expect_cache(desc, v_cache, "v_cache")
-    _expect_exps(desc, k_exp, "k_exp")
-    _expect_exps(desc, v_exp, "v_exp")
-    fn = "kvq_append_blocks"
-    with _on_device(fn, stream, k_new, v_new, token_offsets, block_table, seq_lens, abort_flags, k_cache,
-                    v_cache, k_exp, v_exp):
-        st = load().kvq_append_blocks(ctypes.byref(desc.c()), _ptr(k_new), _ptr(v_new), T,
-                                      _ptr(token_offsets), _ptr(block_table), maxp, _ptr(seq_lens), B,
-                                      _ptr(abort_flags), _ptr(k_cache), _ptr(v_cache), _ptr(k_exp),
-                                      _ptr(v_exp), _stream(stream))
-    _check(fn, st)
+    st = (_native or _load_native()).append_blocks(
+        desc, k_new, v_new, token_offsets, block_table, seq_lens, abort_flags, k_cache, v_cache, k_exp, v_exp,
+        stream)
+    if st:
+        _check("kvq_append_blocks", st)
 
 
 def kvq_copy_pages(desc: CacheDesc, caches, exps, src_pages, dst_pages, stream=None):
     """Page src_pages[i] becomes page dst_pages[i] in every tensor of ``caches``
     (K and V caches of any number of layers, all described by ``desc``) and of
     ``exps`` (their exponents, if the caches are block-scaled; else empty)."""
-    import torch
-    for i, t in enumerate(caches):
-        _expect_cache(desc, t, f"caches[{i}]")
-    for i, t in enumerate(exps):
-        _expect_exps(desc, t, f"exps[{i}]")
-    n = src_pages.numel()
-    _expect(src_pages, torch.int32, (n,), "src_pages")
-    _expect(dst_pages, torch.int32, (n,), "dst_pages")
-    fn = "kvq_copy_pages"
-    with _on_device(fn, stream, src_pages, dst_pages, *caches, *exps):
-        c = (ctypes.c_void_p * max(1, len(caches)))(*[_ptr(t) for t in caches])
-        e = (ctypes.c_void_p * max(1, len(exps)))(*[_ptr(t) for t in exps])
-        st = load().kvq_copy_pages(ctypes.byref(desc.c()), c, len(caches), e, len(exps), _ptr(src_pages),
-                                   _ptr(dst_pages), n, _stream(stream))
-    _check(fn, st)
+    st = (_native or _load_native()).copy_pages(desc, caches, exps, src_pages, dst_pages, stream)
+    if st:
+        _check("kvq_copy_pages", st)
 
 
 def kvq_decode_attn_append(desc, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
