@@ -75,6 +75,8 @@ kvq_status check_desc(const kvq_cache_desc *d)
 struct Plan {
     int32_t split_tokens, max_splits, row_blocks;
     int32_t cluster;              // 0, or the cluster size (= max_splits) of the cluster combine
+    // balanced launch (DecodeArgs); 0 resident CTAs: a grid of splits
+    int32_t resident_ctas, balanced_ctas, unit_shift, min_split_units, pair_cost;
     size_t counter_bytes, lse_bytes, o_bytes;
 };
 
@@ -118,6 +120,12 @@ int64_t auto_splits(int64_t pairs, int64_t max_ctx, int64_t slots)
     return best;
 }
 
+// Resident clusters of n splits, by the build that the call runs.
+int cluster_capacity(int n, bool bf16, bool multi, bool view)
+{
+    return view ? kvq::decode_view_cluster_capacity(n, bf16, multi) : kvq::decode_cluster_capacity(n, bf16, multi);
+}
+
 // Split count for a job that can run in one wave, or 0 if none can.  Among
 // the counts whose CTAs are all resident at once -- every (request, KV
 // head) as one resident cluster of its splits, or as plain CTAs -- it takes
@@ -131,7 +139,7 @@ int64_t auto_splits(int64_t pairs, int64_t max_ctx, int64_t slots)
 // multi-wave rule took 7 through the workspace, 79.6 us; 32 x 4,097: one
 // split, 62.0 us against 73.5 us.)
 int64_t single_wave_splits(int64_t pairs, int64_t max_ctx, int64_t unit, int64_t slots, bool bf16,
-                           bool multi)
+                           bool multi, bool view)
 {
     const double bytes_per_tok = bf16 ? 512.0 : 256.0;       // K + V of one token of one KV head
     const double cta_rate = bf16 ? 40e9 : 20e9;               // bytes per second per CTA
@@ -154,7 +162,7 @@ int64_t single_wave_splits(int64_t pairs, int64_t max_ctx, int64_t unit, int64_t
             continue;                                           // the same plan as a smaller n
         last = splits;
         const bool cluster = splits >= 2 && splits <= kvq::kMaxCluster &&
-                             pairs <= kvq::decode_cluster_capacity(static_cast<int>(splits), bf16, multi);
+                             pairs <= cluster_capacity(static_cast<int>(splits), bf16, multi, view);
         if (!cluster && pairs * splits > slots)
             continue;                                           // more than one wave
         const double split_us = static_cast<double>(split) * bytes_per_tok / cta_rate * 1e6;
@@ -193,6 +201,64 @@ int32_t visible_pages(const View &v, int32_t page_size, int32_t max_pages, int32
     const int64_t span = static_cast<int64_t>(v.window) + n_query - 1;
     const int64_t pages = sinks + (span - 1) / page_size + 2;
     return pages < max_pages ? static_cast<int32_t>(pages) : max_pages;
+}
+
+// Whether a windowed or block-scaled call shares its work out evenly on the
+// device (a balanced launch) instead of running a grid of equal splits of the
+// longest context its table allows.  The balanced launch costs 2 to 3 us more
+// before its first copy (the lengths come before the table) and merges through
+// the workspace, 4 us on 134 MB of equal lengths (8 requests x 8 KV heads x
+// 8,193 tokens: 30.2 us against the grid's 25.8); a grid that waits for its
+// longest split loses more as the batch grows (64 x 8 x 2,049 equal tokens:
+// 48.2 us against 58.3; 16 x 8 x 1,024..16,384 tokens, 4 query tokens: 73.4
+// against 105).  The border is put at 256 MB of cache that the tables allow.
+constexpr int64_t kBalancedMinBytes = 256 << 20;
+bool balanced_pays(int64_t pairs, int64_t max_ctx, bool bf16)
+{
+    return pairs * max_ctx * (bf16 ? 512 : 256) >= kBalancedMinBytes;
+}
+
+// Units that a border between two (request, KV head) pairs costs a CTA of a
+// balanced launch, in tokens: measured flat from 256 to 512, 5 to 10 % slower
+// without any.
+constexpr int64_t kPairCostTokens = 384;
+
+// A balanced launch: shares of at most 8,192 tokens, as many resident CTAs as
+// the GPU holds, and a workspace slot for every (CTA, pair) that can meet.
+// False where its numbering or the combine's limits do not fit.
+bool plan_balanced(int64_t pairs, int64_t max_ctx, int32_t page_size, bool bf16, bool multi, Plan *p)
+{
+    const int64_t unit = page_size > 64 ? page_size : 64;
+    const int64_t max_units = (max_ctx + unit - 1) / unit;
+    const int64_t most_splits = multi ? kvq::kMultiMaxSplitsPerRequest : kvq::kMaxSplitsTotal;
+    // at least one 32-token chunk per warp, and no more splits of one pair than the combine takes
+    const int64_t shortest = kMinAutoSplitTokens / unit > 0 ? kMinAutoSplitTokens / unit : 1;
+    const int64_t fewest = (max_units + most_splits - 3) / (most_splits - 2);
+    const int64_t min_units = shortest > fewest ? shortest : fewest;
+    if (min_units * unit > kMaxSplitTokens)
+        return false;
+    const int64_t ctas = static_cast<int64_t>(kvq::device_sm_count()) * kvq::decode_view_ctas_per_sm(bf16, multi);
+    const int64_t wave = ctas * (kMaxSplitTokens / unit);
+    const int64_t cost = kPairCostTokens / unit;
+    const int64_t most = pairs * (max_units + cost);       // the longest line there can be
+    if (most > 0x7FFFFFFF - wave)
+        return false;
+    const int64_t waves = (most + wave - 1) / wave;
+    const int64_t grid = ctas * (waves > 0 ? waves : 1);
+    p->resident_ctas = static_cast<int32_t>(ctas);
+    p->balanced_ctas = static_cast<int32_t>(grid);
+    p->unit_shift = unit == 64 ? 6 : 7;
+    p->min_split_units = static_cast<int32_t>(min_units);
+    p->pair_cost = static_cast<int32_t>(cost);
+    p->split_tokens = kMaxSplitTokens;
+    const int64_t splits = (max_units + min_units - 1) / min_units + 1;
+    p->max_splits = static_cast<int32_t>(splits < grid ? splits : grid);
+    p->cluster = 0;
+    p->counter_bytes = (static_cast<size_t>(pairs) * 4 + 255) / 256 * 256;
+    const size_t rows = static_cast<size_t>(grid + pairs) * (multi ? kvq::kMultiRowsPerCta : kvq::kMaxGroup);
+    p->lse_bytes = (rows * sizeof(float) + 255) / 256 * 256;
+    p->o_bytes = rows * kHeadDim * sizeof(float);
+    return true;
 }
 
 // view: null for the calls that read every token with per-head scales.
@@ -238,8 +304,12 @@ kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads
                                    : 1;
     const int64_t pairs = static_cast<int64_t>(batch) * d->num_kv_heads * row_blocks;
     p->row_blocks = static_cast<int32_t>(row_blocks);
+    p->resident_ctas = p->balanced_ctas = p->unit_shift = p->min_split_units = p->pair_cost = 0;
     if (static_cast<int64_t>(d->num_kv_heads) * row_blocks > 65535)
         return KVQ_ERR_UNSUPPORTED;                  // the grid's second dimension
+    if (view != nullptr && num_splits == 0 && batch > 0 && balanced_pays(pairs, max_ctx, bf16) &&
+        plan_balanced(pairs, max_ctx, d->page_size, bf16, multi, p))
+        return KVQ_OK;
     int64_t want;
     bool single_wave = false;
     if (num_splits > 0) {
@@ -264,10 +334,11 @@ kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads
         single_wave = true;                          // no cluster form
     } else {
         const int64_t slots =
-            static_cast<int64_t>(kvq::device_sm_count()) * kvq::decode_ctas_per_sm(bf16, multi);
+            static_cast<int64_t>(kvq::device_sm_count()) *
+            (view ? kvq::decode_view_ctas_per_sm(bf16, multi) : kvq::decode_ctas_per_sm(bf16, multi));
         const int64_t jobs = static_cast<int64_t>(batch > 0 ? batch : 1) * d->num_kv_heads * row_blocks;
         const int64_t big = (max_ctx + kMaxSplitTokens - 1) / kMaxSplitTokens;
-        want = jobs * big < 4 * slots ? single_wave_splits(jobs, max_ctx, unit, slots, bf16, multi) : 0;
+        want = jobs * big < 4 * slots ? single_wave_splits(jobs, max_ctx, unit, slots, bf16, multi, view != nullptr) : 0;
         single_wave = want > 0;
         if (!single_wave)
             want = auto_splits(jobs, max_ctx, slots);
@@ -279,7 +350,7 @@ kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads
         // through distributed shared memory, a much shorter tail than the
         // workspace combine; that is worth giving up up to half the splits.
         int64_t c = want < kvq::kMaxCluster ? want : kvq::kMaxCluster;
-        while (c >= 2 && pairs > kvq::decode_cluster_capacity(static_cast<int>(c), bf16, multi))
+        while (c >= 2 && pairs > cluster_capacity(static_cast<int>(c), bf16, multi, view != nullptr))
             --c;
         if (c >= 2 && 2 * c >= want)
             want = c;
@@ -298,7 +369,7 @@ kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads
     // the workspace.
     p->cluster = 0;
     if (!umma && splits >= 2 && batch > 0 &&
-        pairs <= kvq::decode_cluster_capacity(static_cast<int>(splits), bf16, multi))
+        pairs <= cluster_capacity(static_cast<int>(splits), bf16, multi, view != nullptr))
         p->cluster = static_cast<int32_t>(splits);
     p->counter_bytes = (static_cast<size_t>(pairs) * 4 + 255) / 256 * 256;
     if (p->counter_bytes == 0)
@@ -421,6 +492,11 @@ kvq_status prepare_decode(const kvq_cache_desc *desc, const void *q, int32_t bat
     a.split_tokens = call->plan.split_tokens;
     a.max_splits = call->plan.max_splits;
     a.cluster = call->plan.cluster;
+    a.resident_ctas = call->plan.resident_ctas;
+    a.balanced_ctas = call->plan.balanced_ctas;
+    a.unit_shift = call->plan.unit_shift;
+    a.min_split_units = call->plan.min_split_units;
+    a.pair_cost = call->plan.pair_cost;
     a.n_query = n_query;
     a.row_blocks = call->plan.row_blocks;
     a.window = view ? view->window : 0;

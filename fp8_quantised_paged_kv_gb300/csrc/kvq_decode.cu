@@ -1,36 +1,8 @@
 // kvq_decode.cu -- the decode kernel's build for caches with one scale per KV
-// head (or BF16), every token visible, and the occupancy queries the planner
-// uses for every build of that kernel (they share its shared memory and
-// launch bounds).
+// head (or BF16), every token visible, and the planner's occupancy queries.
 #include "kvq_decode_split.cuh"
 
 namespace kvq {
-namespace {
-
-template <bool kBf16, bool kMulti>
-int cluster_capacity_query(int n)
-{
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || configure<kBf16, false, true, kMulti>(dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    DecodeArgs a = {};
-    a.max_splits = n;
-    cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg =
-        launch_config<kBf16, false, true>(a, dim3(static_cast<unsigned>(n), 1, 1), nullptr, attr);
-    int clusters = 0;
-    if (cudaOccupancyMaxActiveClusters(&clusters, decode_split_kernel<kBf16, false, true, kMulti, false, false>, &cfg) !=
-        cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return clusters;
-}
-
-} // namespace
-
 cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                           cudaStream_t stream)
 {
@@ -39,25 +11,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &k_map, const C
 
 int decode_cluster_capacity(int n, bool bf16_cache, bool multi)
 {
-    if (n < 2 || n > kMaxCluster)
-        return 0;
-    static std::mutex mu;
-    static std::map<std::tuple<int, int, bool, bool>, int> cache;
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    std::lock_guard<std::mutex> lock(mu);
-    const auto key = std::make_tuple(dev, n, bf16_cache, multi);
-    auto it = cache.find(key);
-    if (it != cache.end())
-        return it->second;
-    const int c = multi ? (bf16_cache ? cluster_capacity_query<true, true>(n) : cluster_capacity_query<false, true>(n))
-                        : (bf16_cache ? cluster_capacity_query<true, false>(n)
-                                      : cluster_capacity_query<false, false>(n));
-    cache[key] = c;
-    return c;
+    return cluster_capacity<false>(n, bf16_cache, multi);
 }
 
 int decode_ctas_per_sm(bool bf16_cache, bool multi)

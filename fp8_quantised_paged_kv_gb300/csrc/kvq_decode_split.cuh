@@ -101,6 +101,7 @@ constexpr int kWarps = 4;
 constexpr int kCtasPerSm = 3;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxPageList = 8192 / 16 + 8;       // page ids of one split (<= 8192 tokens)
+constexpr int kMaxShareTokens = 8192;             // of a balanced launch's CTA
 // Published lse of a split that has no result: both are NaN, so the combine
 // zeroes the request either way; the payload tells a failed tag check (the
 // request is aborted and its new token not written) from a copy timeout.
@@ -119,6 +120,28 @@ struct Tile {
                                       2 * kMaxPageList * 4 /* tags of the split's pages */ +
                                       512 /* the new token's K and V row */ + 16;
 };
+
+// Windowed builds hold no tags and no new token; the block-scaled ones keep
+// the exponents of a split's blocks there (ek in the low byte, ev in the high
+// one), the multi-token FP8 ones the query fragments (smem_q).
+constexpr int kExpBytes = 2 * (8192 / kBlockTokens) + 16;
+__host__ __device__ constexpr bool smem_q(bool bf16, bool multi, bool window) { return window && multi && !bf16; }
+constexpr int kQFragBytes = 8 * 2 * 32 * 8;       // [k-step][n-tile][lane] two words
+template <bool kBf16, bool kMulti, bool kWindow>
+constexpr int smem_bytes()
+{
+    if (!kWindow)
+        return Tile<kBf16>::kSmemBytes;
+    return 1024 + Tile<kBf16>::kRingBytes + kWarps * Tile<kBf16>::kStages * 8 + kMaxPageList * 4 + kExpBytes +
+           (smem_q(kBf16, kMulti, kWindow) ? kQFragBytes : 0);
+}
+// Resident CTAs per SM that the registers are compiled for.  Multi-token
+// builds: 2, with both n-tiles' query fragments in registers; the windowed FP8
+// ones read them from shared memory, which leaves registers for 3.
+__host__ __device__ constexpr int min_ctas(bool bf16, bool multi, bool window)
+{
+    return multi && !smem_q(bf16, multi, window) ? 2 : kCtasPerSm;
+}
 
 // Byte offset of 16-byte chunk `c` of 128-byte line `line` in a tile written
 // by a 128-byte-swizzled tensor copy into a 1024-byte-aligned buffer.
@@ -173,6 +196,10 @@ __device__ __forceinline__ void store_out(void *out, int64_t idx, float v, bool 
 }
 
 
+// Query rows of one CTA: one mma n-tile (8) for a single query token, two
+// (16) for the multi-token kernel.
+__host__ __device__ constexpr int rows_per_cta(bool multi) { return multi ? 2 * kMaxGroup : kMaxGroup; }
+
 // The query rows one CTA serves.  The rows of (request b, KV head kvh) are
 // (token i, head h) for the request's n_query new tokens and the g query
 // heads of the group, row i * g + h; a CTA takes rows row0 .. row0 + nrows - 1
@@ -180,10 +207,12 @@ __device__ __forceinline__ void store_out(void *out, int64_t idx, float v, bool 
 // kernel compiled for that case) the rows are the group's heads, one mma
 // n-tile of 8, and one CTA takes them all; the multi-token kernel gives each
 // warp two n-tiles (16 rows), so every chunk's conversions serve 16 rows.
-template <bool kMulti>
+template <bool kMulti, bool kSlots>
 struct Rows {
     int b, kvh, row0, nrows;
     int64_t slot;                            // this (request, KV head, row block)'s arrival counter
+    int64_t base;                            // kSlots: workspace slot of its first split, or -1
+    const int64_t *ids;                      // kSlots: id of every row, in shared memory
 
     // Row of q and out ([B][n_query][Hq][D], in units of head_dim) of local row r.
     __device__ __forceinline__ int64_t id(const DecodeArgs &a, int r) const
@@ -194,7 +223,36 @@ struct Rows {
         return (static_cast<int64_t>(b) * a.n_query + rr / a.group) * a.num_q_heads + kvh * a.group +
                rr % a.group;
     }
+
+    // Place of local row r of split s among the workspace's partials (an lse
+    // each, and head_dim floats of output).  A balanced launch gives every
+    // split of the launch a slot of rows_per_cta rows of its own.
+    __device__ __forceinline__ int64_t part(const DecodeArgs &a, int r, int s) const
+    {
+        if constexpr (kSlots)
+            return base >= 0 ? (base + s) * rows_per_cta(kMulti) + r : ids[r] * a.max_splits + s;
+        return id(a, r) * a.max_splits + s;
+    }
+
+    // Distance of a row's partials of consecutive splits (kSlots).
+    __device__ __forceinline__ int64_t part_step() const { return base >= 0 ? rows_per_cta(kMulti) : 1; }
+
+    __device__ __forceinline__ int64_t out_row(const DecodeArgs &a, int r) const
+    {
+        if constexpr (kSlots)
+            return ids[r];
+        return id(a, r);
+    }
 };
+
+__device__ __forceinline__ void store_out4(void *out, int64_t idx, float4 v, bool fp32)
+{
+    if (fp32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(out) + idx) = v;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(out) + idx) =
+            make_uint2(f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w));
+}
 
 // The warps' merge area holds one row of 128 floats per (warp, head).  Row
 // stride and a skew of 2 words per 32 dims make the fragment stores (a lane
@@ -202,12 +260,6 @@ struct Rows {
 // bank pairs per half-warp, and keep the row reads (thread d) conflict-free.
 constexpr int kMergeStride = 146;                 // >= 128 + 6, == 2 (mod 16)
 __device__ __forceinline__ int merge_col(int d) { return d + 2 * (d >> 5); }
-
-// Shared-memory offset (in floats) of the combine scratch: just past the
-// warps' merge area, inside the ring (idle by then).
-// Query rows of one CTA: one mma n-tile (8) for a single query token, two
-// (16) for the multi-token kernel.
-__host__ __device__ constexpr int rows_per_cta(bool multi) { return multi ? 2 * kMaxGroup : kMaxGroup; }
 
 
 // Shared-memory offset (in floats) of the cluster partial: just past the
@@ -269,7 +321,7 @@ __device__ void finish_step(const DecodeArgs &a, int b, int kvh, bool stale)
 // visible token reaches its row's output whatever the splits are; such a split
 // publishes lse = +inf, which makes the weights and their sum NaN here.
 template <bool kMulti, bool kNanFlows>
-__device__ void publish_and_combine(const DecodeArgs &a, const Rows<kMulti> &R, int nsplit, float *scratch)
+__device__ void publish_and_combine(const DecodeArgs &a, const Rows<kMulti, kNanFlows> &R, int nsplit, float *scratch)
 {
     __shared__ int s_last;
     // The block barrier orders every thread's partial before thread 0's
@@ -286,10 +338,56 @@ __device__ void publish_and_combine(const DecodeArgs &a, const Rows<kMulti> &R, 
         return;
     constexpr int kRowsT = rows_per_cta(kMulti);
     const int g = R.nrows, n = nsplit;
+    if constexpr (kNanFlows) {
+        // Few splits: every lse and partial in one trip to L2, each thread
+        // working out its row's weights itself (no barrier in the tail).
+        constexpr int kFew = 8;
+        if (n <= kFew) {
+            const int d = 4 * (threadIdx.x % 32);
+            const int64_t step = R.part_step();
+            for (int h = threadIdx.x / 32; h < g; h += kWarps) {
+                const int64_t at = R.part(a, h, 0);
+                float lse[kFew];
+                float4 v[kFew];
+#pragma unroll
+                for (int s = 0; s < kFew; ++s) {
+                    lse[s] = s < n ? __ldcg(a.ws_lse + at + s * step) : -INFINITY;
+                    v[s] = s < n ? __ldcg(reinterpret_cast<const float4 *>(a.ws_o + (at + s * step) * kHeadDim + d))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                float m = -INFINITY, sum = 0.f;
+                bool bad = false;
+#pragma unroll
+                for (int s = 0; s < kFew; ++s) {
+                    bad |= lse[s] != lse[s];
+                    m = fmaxf(m, lse[s]);
+                }
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int s = 0; s < kFew; ++s)
+                    if (lse[s] != -INFINITY) {
+                        const float w = fast_exp2(lse[s] - m);
+                        sum += w;
+                        acc.x += w * v[s].x;
+                        acc.y += w * v[s].y;
+                        acc.z += w * v[s].z;
+                        acc.w += w * v[s].w;
+                    }
+                const bool zero = bad || sum == 0.f;
+                store_out4(a.out, R.ids[h] * kHeadDim + d,
+                           zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                : make_float4(acc.x / sum, acc.y / sum, acc.z / sum, acc.w / sum),
+                           a.out_fp32);
+            }
+            if (threadIdx.x == 0)
+                *counter = 0;                // ready for the next call
+            return;
+        }
+    }
     float *s_tot = scratch;                  // [kRowsT] sum of weights (0: drop the row)
     float *s_w = scratch + kRowsT;           // [g][n]: lse, then weights
     for (int i = threadIdx.x; i < g * n; i += kThreads)
-        s_w[i] = __ldcg(a.ws_lse + R.id(a, i / n) * a.max_splits + i % n);
+        s_w[i] = __ldcg(a.ws_lse + R.part(a, i / n, i % n));
     __syncthreads();
     // one warp per head: max, validity, weights, their sum
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -331,16 +429,28 @@ __device__ void publish_and_combine(const DecodeArgs &a, const Rows<kMulti> &R, 
 #pragma unroll
     for (int q = 0; q < kPairs; ++q)
         acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    [[maybe_unused]] const float *from[kPairs];
+    [[maybe_unused]] int64_t step = 0;
+    if constexpr (kNanFlows) {
+        step = R.part_step() * kHeadDim;
+#pragma unroll
+        for (int q = 0; q < kPairs; ++q)
+            from[q] = a.ws_o + R.part(a, min(hp[q], g - 1), 0) * kHeadDim + cp;
+    }
     for (int s0 = 0; s0 < n; s0 += kRound) {
         float4 v[kPairs][kRound];
 #pragma unroll
         for (int q = 0; q < kPairs; ++q)
 #pragma unroll
-            for (int j = 0; j < kRound; ++j)
-                v[q][j] = (hp[q] < g && s0 + j < n)
-                              ? __ldcg(reinterpret_cast<const float4 *>(
-                                    a.ws_o + (R.id(a, hp[q]) * a.max_splits + s0 + j) * kHeadDim + cp))
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j = 0; j < kRound; ++j) {
+                const float *p;
+                if constexpr (kNanFlows)
+                    p = from[q] + (s0 + j) * step;
+                else
+                    p = a.ws_o + R.part(a, hp[q], s0 + j) * kHeadDim + cp;
+                v[q][j] = (hp[q] < g && s0 + j < n) ? __ldcg(reinterpret_cast<const float4 *>(p))
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
 #pragma unroll
         for (int q = 0; q < kPairs; ++q)
 #pragma unroll
@@ -356,8 +466,16 @@ __device__ void publish_and_combine(const DecodeArgs &a, const Rows<kMulti> &R, 
 #pragma unroll
     for (int q = 0; q < kPairs; ++q)
         if (hp[q] < g) {
-            const int64_t o0 = R.id(a, hp[q]) * kHeadDim + cp;
-            const bool some = kNanFlows ? s_tot[hp[q]] != 0.f : s_tot[hp[q]] > 0.f;
+            const int64_t o0 = R.out_row(a, hp[q]) * kHeadDim + cp;
+            if constexpr (kNanFlows) {
+                const float t = s_tot[hp[q]];
+                store_out4(a.out, o0,
+                           t != 0.f ? make_float4(acc[q].x / t, acc[q].y / t, acc[q].z / t, acc[q].w / t)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f),
+                           a.out_fp32);
+                continue;
+            }
+            const bool some = s_tot[hp[q]] > 0.f;
             store_out(a.out, o0, some ? acc[q].x / s_tot[hp[q]] : 0.f, a.out_fp32);
             store_out(a.out, o0 + 1, some ? acc[q].y / s_tot[hp[q]] : 0.f, a.out_fp32);
             store_out(a.out, o0 + 2, some ? acc[q].z / s_tot[hp[q]] : 0.f, a.out_fp32);
@@ -368,7 +486,7 @@ __device__ void publish_and_combine(const DecodeArgs &a, const Rows<kMulti> &R, 
         if (threadIdx.x == 0) {
             int any = 0;
             for (int sp = 0; sp < n; ++sp)
-                any |= __float_as_uint(__ldcg(a.ws_lse + R.id(a, 0) * a.max_splits + sp)) == kLseStale;
+                any |= __float_as_uint(__ldcg(a.ws_lse + R.part(a, 0, sp))) == kLseStale;
             s_stale_any = any;
         }
         __syncthreads();
@@ -382,18 +500,18 @@ __device__ void publish_and_combine(const DecodeArgs &a, const Rows<kMulti> &R, 
 // timed out): a single-split request gets zeros; otherwise the split
 // publishes an invalid (NaN) lse so the combine zeroes the request.
 template <bool kMulti, bool kNanFlows>
-__device__ void drop_split(const DecodeArgs &a, const Rows<kMulti> &R, int split, int nsplit, float *smem,
+__device__ void drop_split(const DecodeArgs &a, const Rows<kMulti, kNanFlows> &R, int split, int nsplit, float *smem,
                            uint32_t lse_bits = kLseInvalid)
 {
     if (nsplit == 1) {
         for (int i = threadIdx.x; i < R.nrows * kHeadDim; i += kThreads)
-            store_out(a.out, R.id(a, i / kHeadDim) * kHeadDim + i % kHeadDim, 0.f, a.out_fp32);
+            store_out(a.out, R.out_row(a, i / kHeadDim) * kHeadDim + i % kHeadDim, 0.f, a.out_fp32);
         if (a.expected_tags != nullptr)
             finish_step(a, R.b, R.kvh, lse_bits == kLseStale);
         return;
     }
     if (threadIdx.x < R.nrows)
-        a.ws_lse[R.id(a, threadIdx.x) * a.max_splits + split] = __uint_as_float(lse_bits);
+        a.ws_lse[R.part(a, threadIdx.x, split)] = __uint_as_float(lse_bits);
     publish_and_combine<kMulti, kNanFlows>(a, R, nsplit, kMulti ? smem : smem + kScratchOffset);
 }
 
@@ -427,7 +545,7 @@ enum PartialStatus { kPartialOk = 0, kPartialEmpty = 1, kPartialInvalid = 2, kPa
 // else -1.  Returns, on the finisher, whether any split of the
 // request failed its tag check (false elsewhere).
 template <bool kMulti, bool kNanFlows>
-__device__ bool cluster_finish(const DecodeArgs &a, const Rows<kMulti> &R, PartialStatus status, float *part,
+__device__ bool cluster_finish(const DecodeArgs &a, const Rows<kMulti, kNanFlows> &R, PartialStatus status, float *part,
                                int finisher)
 {
     __shared__ int s_any_stale;
@@ -487,7 +605,14 @@ __device__ bool cluster_finish(const DecodeArgs &a, const Rows<kMulti> &R, Parti
             }
         }
         const bool zero = bad || (kNanFlows ? sum == 0.f : !(sum > 0.f));
-        const int64_t o0 = R.id(a, h) * kHeadDim + d;
+        const int64_t o0 = R.out_row(a, h) * kHeadDim + d;
+        if constexpr (kNanFlows) {
+            store_out4(a.out, o0,
+                       zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                            : make_float4(acc.x / sum, acc.y / sum, acc.z / sum, acc.w / sum),
+                       a.out_fp32);
+            continue;
+        }
         store_out(a.out, o0, zero ? 0.f : acc.x / sum, a.out_fp32);
         store_out(a.out, o0 + 1, zero ? 0.f : acc.y / sum, a.out_fp32);
         store_out(a.out, o0 + 2, zero ? 0.f : acc.z / sum, a.out_fp32);
@@ -498,14 +623,41 @@ __device__ bool cluster_finish(const DecodeArgs &a, const Rows<kMulti> &R, Parti
     return rank == finisher && s_any_stale != 0;
 }
 
+// One split: tokens t0 .. t0 + span - 1 (span at most 8,192, t0 a multiple of
+// the page size) of the context that (request b, KV head kvh, row block rb)
+// shows, the split-th of nsplit (0: as many as split_tokens gives the
+// request); base as in Rows.
+struct Job {
+    int b, kvh, rb, split, nsplit, span;
+    int64_t t0, base, real;                  // real: the request's tokens, or -1 (read them)
+};
+
+// The context a windowed call shows of a request of `real` tokens, without
+// the hole between the sinks' pages and the page where the first query's
+// window starts: its length, the sinks' pages, the hole's pages, and the
+// window's start, which like every position counts the shortened context.
+struct Shown {
+    int64_t len, sink_pages, hole, win0;
+};
+__device__ __forceinline__ Shown shown_context(const DecodeArgs &a, int64_t real, int ps_shift)
+{
+    Shown v = {real, 0, 0, 0};
+    if (a.window > 0) {
+        const int64_t start = real - a.n_query + 1 - a.window;
+        const int64_t ps = static_cast<int64_t>(1) << ps_shift;
+        v.sink_pages = (min(real, static_cast<int64_t>(a.num_sinks)) + ps - 1) >> ps_shift;
+        v.hole = max((max(start, static_cast<int64_t>(0)) >> ps_shift) - v.sink_pages, static_cast<int64_t>(0));
+        v.len = real - (v.hole << ps_shift);
+        v.win0 = start - (v.hole << ps_shift);
+    }
+    return v;
+}
+
 template <bool kBf16Cache, bool kPreciseP, bool kCluster, bool kMulti, bool kWindow, bool kBlocks>
-__global__ void __launch_bounds__(kThreads, kMulti ? 2 : kCtasPerSm)
-decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
-                    const __grid_constant__ CUtensorMap v_map, const DecodeArgs a)
+__device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtensorMap &v_map, const DecodeArgs &a,
+                                          const Job &job, bool first)
 {
     using T = Tile<kBf16Cache>;
-    static_assert(!kBlocks || (kWindow && !kBf16Cache), "the block-scaled build is an FP8 build with a window");
-    KVQ_STAMP(0);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -514,47 +666,73 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
     uint32_t *tag_live = reinterpret_cast<uint32_t *>(page_list + kMaxPageList);   // kvq_decode_step:
     uint32_t *tag_want = tag_live + kMaxPageList;                                  // the split's tags
     uint8_t *new_tok = reinterpret_cast<uint8_t *>(tag_want + kMaxPageList);       // [K row][V row]
-    // block-scaled build, in the place of the tags: 2^ek and ev of the split's blocks
-    [[maybe_unused]] float *blk_k = reinterpret_cast<float *>(tag_live);
-    [[maybe_unused]] float *blk_v = reinterpret_cast<float *>(tag_want);
-    static_assert(kMaxPageList >= 8192 / kBlockTokens, "a split's blocks fit in the tag lists");
+    // windowed builds, in the place of the tags (kExpBytes, kQFragBytes)
+    [[maybe_unused]] uint16_t *blk_exp = reinterpret_cast<uint16_t *>(page_list + kMaxPageList);
+    [[maybe_unused]] uint2 *q_frag =
+        reinterpret_cast<uint2 *>(reinterpret_cast<uint8_t *>(page_list + kMaxPageList) + kExpBytes);
+    constexpr bool kSmemQ = smem_q(kBf16Cache, kMulti, kWindow);
     __shared__ int s_failed;
     __shared__ int s_stale;                                // kvq_decode_step: a page of this split failed
 
-    const int split = blockIdx.x, b = blockIdx.z;
-    // with several query tokens, blockIdx.y = KV head x row blocks of 8 rows
-    const int kvh = kMulti ? static_cast<int>(blockIdx.y) / a.row_blocks : static_cast<int>(blockIdx.y);
-    const int rb = kMulti ? static_cast<int>(blockIdx.y) % a.row_blocks : 0;
+    // The builds without a window always run the split that their place in
+    // the grid names.
+    const int split = kWindow ? job.split : static_cast<int>(blockIdx.x);
+    const int b = kWindow ? job.b : static_cast<int>(blockIdx.z);
+    // with several query tokens, blockIdx.y = KV head x row blocks
+    const int line = static_cast<int>(blockIdx.y);
+    const int kvh = kWindow ? job.kvh : kMulti ? line / a.row_blocks : line;
+    const int rb = kWindow ? job.rb : kMulti ? line % a.row_blocks : 0;
+    const int split_tokens = kWindow ? job.span : a.split_tokens;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int gq = lane >> 2, tq = lane & 3;
     const int g = a.group, ps = a.page_size;
     const int ps_shift = __ffs(ps) - 1;                  // ps is 16, 32, 64 or 128
-    Rows<kMulti> R;
+    Rows<kMulti, kWindow> R;
     R.b = b;
     R.kvh = kvh;
     R.row0 = rb * rows_per_cta(kMulti);
     R.nrows = kMulti ? min(rows_per_cta(true), a.n_query * g - R.row0) : g;
-    R.slot = static_cast<int64_t>(b) * gridDim.y + blockIdx.y;
+    R.slot = kWindow ? (static_cast<int64_t>(b) * a.num_kv_heads + kvh) * (kMulti ? a.row_blocks : 1) + rb
+                     : static_cast<int64_t>(b) * gridDim.y + line;
+    R.base = job.base;
+    if constexpr (kWindow) {
+        __shared__ int64_t s_ids[rows_per_cta(kMulti)];
+        if (threadIdx.x < R.nrows)
+            s_ids[threadIdx.x] = R.id(a, threadIdx.x);
+        R.ids = s_ids;
+    }
 
-    const int first_page = static_cast<int>(static_cast<int64_t>(split) * a.split_tokens / ps);
+    const int first_page = kWindow ? static_cast<int>(job.t0 >> ps_shift)
+                                   : static_cast<int>(static_cast<int64_t>(split) * a.split_tokens / ps);
     const int span_left = a.max_pages_per_seq - first_page;
-    const int span = a.split_tokens / ps < span_left ? a.split_tokens / ps : span_left;
+    const int span = split_tokens / ps < span_left ? split_tokens / ps : span_left;
     const int32_t *bt = a.block_table + static_cast<int64_t>(b) * a.max_pages_per_seq + first_page;
     const int lines_per_tok = kBf16Cache ? 2 : 1;
 
-    // Launched as a programmatic dependent of the previous kernel on the
-    // stream (in a decode step: the tag check): the CTA can be resident and
-    // have its tensor maps fetched while that kernel runs, and it reads no
-    // global memory until the wait has returned, that is until the previous
-    // kernel has completed and its writes are visible.  (Asking L2 for the
-    // split's first pages before the wait made the step slower: those
-    // requests compete with the check for the memory system.)
-    if (threadIdx.x == 0) {
-        prefetch_tensor_map(&k_map);
-        prefetch_tensor_map(&v_map);
-    }
-    grid_dependency_wait();
-    KVQ_STAMP(1);
+    // A lane's part of query row nt * 8 + gq: dims 32 tq .. 32 tq + 31.  The
+    // single-token windowed builds fetch it here, beside the first table
+    // entries (0.3 us sooner under way); only what follows the first copies
+    // uses it.
+    constexpr bool kEarlyQ = kWindow && !kMulti;
+    constexpr int kNT = rows_per_cta(kMulti) / kMaxGroup;   // mma n-tiles of query rows per warp
+    constexpr int kRowsT = rows_per_cta(kMulti);
+    uint32_t q_raw[kNT][16];
+    auto load_q = [&](int nt) {
+        uint32_t (&w)[16] = q_raw[nt];
+        if (nt * kMaxGroup + gq < R.nrows) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                static_cast<const uint16_t *>(a.q) + (R.id(a, nt * kMaxGroup + gq) * kHeadDim + 32 * tq));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 v = __ldg(src + i);
+                w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                w[i] = 0;
+        }
+    };
 
     // The block-table entries this split can use depend only on the split
     // index, so they are loaded together with the request's length.
@@ -567,44 +745,45 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
             ids[k] = i < span ? __ldg(bt + i) : -1;
         }
     }
-    const int64_t real_len = a.seq_lens[b];
+    const int64_t real_len = kWindow && job.real >= 0 ? job.real : a.seq_lens[b];
+    if constexpr (kEarlyQ)
+        load_q(0);
     // kvq_decode_step: each split checks the tags of its own pages (together
     // the request's used entries) while it streams them, and publishes a
     // failure with its partial; the CTA that sees every split's partial
     // writes the flag and, if the request passed, its new token
     // (finish_here, or finish_step in the workspace form).  A request
     // without tokens to check is decided here.
-    const bool step_check = a.expected_tags != nullptr;
+    const bool step_check = !kWindow && a.expected_tags != nullptr;
     const bool reporter = step_check && split == 0 && kvh == 0 && threadIdx.x == 0;
     const bool aborted = !step_check && a.abort_flags != nullptr && a.abort_flags[b] != 0;
     const int64_t cap = static_cast<int64_t>(a.max_pages_per_seq) * ps;
     const bool zero_request = aborted || real_len <= 0 || real_len > cap;
     // Window: from here on `len` and every position count the shortened
-    // context, without the hole of `hole` pages behind the sinks' pages.
+    // context (shown_context).
     int64_t len = real_len;
     [[maybe_unused]] int64_t win0 = 0;                     // where the first query's window starts
     if constexpr (kWindow) {
         if (a.window > 0) {
-            const int64_t w0 = max(real_len - a.n_query + 1 - a.window, static_cast<int64_t>(0));
-            const int64_t sink_pages = (min(real_len, static_cast<int64_t>(a.num_sinks)) + ps - 1) >> ps_shift;
-            const int64_t hole = max((w0 >> ps_shift) - sink_pages, static_cast<int64_t>(0));
-            len = real_len - (hole << ps_shift);
-            win0 = real_len - a.n_query + 1 - a.window - (hole << ps_shift);
+            const Shown shown = shown_context(a, real_len, ps_shift);
+            len = shown.len;
+            win0 = shown.win0;
             // only entries of pages with a token of the shortened context are read
 #pragma unroll
             for (int k = 0; k < kIdsPerThread; ++k) {
                 const int i = threadIdx.x + k * kThreads;
                 const int64_t v = static_cast<int64_t>(first_page) + i;
-                const bool held = !zero_request && i < a.split_tokens / ps && (v << ps_shift) < len;
-                ids[k] = held ? __ldg(a.block_table + static_cast<int64_t>(b) * a.max_pages_per_seq +
-                                      (v < sink_pages ? v : v + hole))
-                              : -1;
+                const bool held = !zero_request && i < split_tokens / ps && (v << ps_shift) < len;
+                ids[k] = held ? __ldg(bt + i + (v < shown.sink_pages ? 0 : shown.hole)) : -1;
             }
         }
     }
     if (reporter && zero_request)                          // the check's verdict without a look:
         a.abort_out[b] = real_len > cap ? 1 : 0;                // too long fails, empty passes
-    const int nsplit = zero_request ? 1 : static_cast<int>((len + a.split_tokens - 1) / a.split_tokens);
+    const int nsplit = zero_request ? 1
+                       : kWindow && job.nsplit > 0
+                           ? job.nsplit
+                           : static_cast<int>((len + a.split_tokens - 1) / a.split_tokens);
     float *part = reinterpret_cast<float *>(smem) + scratch_offset(kMulti);   // cluster partial
     // kvq_decode_step: the split that finishes the step of a request with
     // tokens in the cluster form and when there is one split -- the last
@@ -626,8 +805,8 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
         return;
     }
 
-    const int64_t t0 = static_cast<int64_t>(split) * a.split_tokens;
-    const int64_t t1 = min(len, t0 + a.split_tokens);
+    const int64_t t0 = kWindow ? job.t0 : static_cast<int64_t>(split) * a.split_tokens;
+    const int64_t t1 = min(len, t0 + split_tokens);
     // page ids of this split (t0 is a multiple of the page size)
     const int n_pages = static_cast<int>((t1 - 1) / ps) - first_page + 1;
     bool bad = false;
@@ -642,8 +821,11 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
     if (threadIdx.x == 0) {
         s_failed = 0;
         s_stale = 0;
-        for (int i = 0; i < kWarps * T::kStages; ++i)
+        for (int i = 0; i < kWarps * T::kStages; ++i) {
+            if (kWindow && !first)
+                mbar_inval(&full[i]);
             mbar_init(&full[i], 1);
+        }
         fence_mbar_init();
     }
     bad = __syncthreads_or(bad);
@@ -657,7 +839,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
     using NewRow = std::conditional_t<kBf16Cache, uint2, uint32_t>;   // a lane's part of the row
     NewRow new_k{}, new_v{};
     int64_t new_row = -1;                                  // cache row of the new token
-    if (a.k_new != nullptr && split == nsplit - 1) {
+    if (!kWindow && a.k_new != nullptr && split == nsplit - 1) {
         const int64_t tpos = len - 1;
         const int c_last = static_cast<int>((tpos - t0) / kChunkTokens);
         const int32_t page = page_list[static_cast<int>(tpos / ps) - first_page];
@@ -785,16 +967,14 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
         const int bpp_shift = ps_shift - 4;                // blocks per page: ps / 16
         for (int i = threadIdx.x; i < 2 * n_chunks; i += kThreads) {
             if (i >= n_blocks) {                           // the last chunk's second m-tile holds no token
-                blk_k[i] = 1.f;
-                blk_v[i] = 0.f;
+                blk_exp[i] = 0;
                 continue;
             }
             const int64_t at = ((static_cast<int64_t>(page_list[i >> bpp_shift]) * a.num_kv_heads + kvh) << bpp_shift) +
                                (i & ((1 << bpp_shift) - 1));
             const int ek = max(static_cast<int>(__ldg(a.k_exp + at)), -126);
             const int ev = max(static_cast<int>(__ldg(a.v_exp + at)), -126);
-            blk_k[i] = __int_as_float((127 + ek) << 23);
-            blk_v[i] = static_cast<float>(min(ev, 126));
+            blk_exp[i] = static_cast<uint16_t>((ek & 0xFF) | (min(ev, 126) << 8));
         }
     }
 
@@ -809,27 +989,14 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
     // changes), so no element overflows and every element within 2^28 of the
     // row's largest keeps all its bits; the score multiplier of head h then
     // carries 2^-e_h.
-    constexpr int kNT = rows_per_cta(kMulti) / kMaxGroup;   // mma n-tiles of query rows per warp
-    constexpr int kRowsT = rows_per_cta(kMulti);
     uint32_t qf[kNT][8][2];
     int q_exp[kNT];                                        // e of row nt * 8 + gq
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
         q_exp[nt] = 0;
-        uint32_t w[16];
-        if (nt * kMaxGroup + gq < R.nrows) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                static_cast<const uint16_t *>(a.q) + (R.id(a, nt * kMaxGroup + gq) * kHeadDim + 32 * tq));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 v = __ldg(src + i);
-                w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                w[i] = 0;
-        }
+        uint32_t (&w)[16] = q_raw[nt];
+        if constexpr (!kEarlyQ)
+            load_q(nt);
         float q_mul = 1.f;
         if constexpr (!kBf16Cache) {
             uint32_t mx = 0;                               // largest |q| of the row, as bf16 bits
@@ -882,7 +1049,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
             for (int j = 0; j < 2; ++j) {
                 const int64_t v = vis0 + (R.row0 + nt * kMaxGroup + 2 * tq + j) / g - t0;
                 vis_col[nt][j] = static_cast<int>(
-                    v < -1 ? -1 : (v > a.split_tokens + kChunkTokens ? a.split_tokens + kChunkTokens : v));
+                    v < -1 ? -1 : (v > split_tokens + kChunkTokens ? split_tokens + kChunkTokens : v));
             }
         full_end = min(t1, vis0 + R.row0 / g);
     }
@@ -898,7 +1065,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
         if (a.window > 0) {
             auto rel = [&](int64_t v) {
                 v -= t0;
-                const int64_t most = a.split_tokens + kChunkTokens;
+                const int64_t most = split_tokens + kChunkTokens;
                 return static_cast<int>(v < -1 ? -1 : (v > most ? most : v));
             };
 #pragma unroll
@@ -912,8 +1079,16 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
             mask_hi = kMulti ? win0 + (R.row0 + R.nrows - 1) / g : win0;
         }
     }
-    if constexpr (kBlocks)
-        __syncthreads();                                   // the blocks' exponents are in place
+    if constexpr (kSmemQ) {                                // each warp stores a quarter of the fragments
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+            if (kk / 2 == warp)
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+                    q_frag[(kk * kNT + nt) * 32 + lane] = make_uint2(qf[nt][kk][0], qf[nt][kk][1]);
+    }
+    if constexpr (kBlocks || kSmemQ)
+        __syncthreads();                                   // the exponents and fragments are in place
 
     // The windowed and block-scaled builds keep weights, sums and accumulators
     // 2^15 times larger (the quotient is the same, and f16 ends at 65504): an
@@ -984,8 +1159,9 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
         if constexpr (kBlocks) {
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
-                blk_mul[mt] = blk_k[2 * c + mt];
-                blk_add[mt] = blk_v[2 * c + mt];
+                const int e = static_cast<int16_t>(blk_exp[2 * c + mt]);
+                blk_mul[mt] = __int_as_float((127 + static_cast<int8_t>(e & 0xFF)) << 23);
+                blk_add[mt] = static_cast<float>(e >> 8);
             }
         }
 
@@ -996,6 +1172,40 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
             // ---- S^T = K Q^T for the two 16-token m-tiles; each K fragment,
             // converted once, feeds every n-tile of query rows
             float sc[kNT][2][4];
+            if constexpr (kSmemQ) {
+                // both m-tiles together: a fragment of Q is read once for four products
+                uint32_t kw[2][2][8];
+    #pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+    #pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int r = mt * 16 + half * 8 + gq;
+                        const uint4 xa = lds128(ks, swz(r, 2 * tq)), xb = lds128(ks, swz(r, 2 * tq + 1));
+                        uint32_t(&w)[8] = kw[mt][half];
+                        w[0] = xa.x; w[1] = xa.y; w[2] = xa.z; w[3] = xa.w;
+                        w[4] = xb.x; w[5] = xb.y; w[6] = xb.z; w[7] = xb.w;
+                    }
+    #pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+    #pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+                        sc[nt][mt][0] = sc[nt][mt][1] = sc[nt][mt][2] = sc[nt][mt][3] = 0.f;
+    #pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    uint2 qv[kNT];
+    #pragma unroll
+                    for (int nt = 0; nt < kNT; ++nt)
+                        qv[nt] = q_frag[(kk * kNT + nt) * 32 + lane];
+    #pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+                        const uint32_t k0 = lo16_e4m3x2_to_f16x2(kw[mt][0][kk]), k1 = lo16_e4m3x2_to_f16x2(kw[mt][1][kk]);
+                        const uint32_t k2 = hi16_e4m3x2_to_f16x2(kw[mt][0][kk]), k3 = hi16_e4m3x2_to_f16x2(kw[mt][1][kk]);
+    #pragma unroll
+                        for (int nt = 0; nt < kNT; ++nt)
+                            mma_f16(sc[nt][mt], k0, k1, k2, k3, qv[nt].x, qv[nt].y);
+                    }
+                }
+            } else {
     #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
     #pragma unroll
@@ -1032,6 +1242,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
                             mma_f16(sc[nt][mt], k0, k1, k2, k3, qf[nt][kk][0], qf[nt][kk][1]);
                     }
                 }
+            }
             }
 
             // ---- online softmax (log2 domain); lane holds rows nt*8 + 2tq, +1
@@ -1304,6 +1515,41 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
         }
     }
     __syncthreads();
+    if constexpr (kWindow) {
+        // warp w takes rows w, w + 4, ..; a lane four dims of each
+        const int d = 4 * lane, c = merge_col(d);
+#pragma unroll
+        for (int q = 0; q < kRowsT / kWarps; ++q) {
+            const int h = warp + q * kWarps;
+            if (h >= R.nrows)
+                break;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float *row = sm_o + (w * kRowsT + h) * kMergeStride + c;
+                const float2 lo = *reinterpret_cast<const float2 *>(row), hi = *reinterpret_cast<const float2 *>(row + 2);
+                const float f = sm_f[h * kWarps + w];
+                acc.x += lo.x * f;
+                acc.y += lo.y * f;
+                acc.z += hi.x * f;
+                acc.w += hi.y * f;
+            }
+            const float t = sm_t[h];
+            acc = make_float4(acc.x * t, acc.y * t, acc.z * t, acc.w * t);
+            if constexpr (kCluster) {
+                *reinterpret_cast<float4 *>(part + kRowsT + h * kHeadDim + d) = acc;
+                if (lane == 0)
+                    part[h] = sm_t[kRowsT + h];
+            } else if (nsplit == 1) {
+                store_out4(a.out, R.ids[h] * kHeadDim + d, acc, a.out_fp32);
+            } else {
+                const int64_t at = R.part(a, h, split);
+                *reinterpret_cast<float4 *>(a.ws_o + at * kHeadDim + d) = acc;
+                if (lane == 0)
+                    a.ws_lse[at] = sm_t[kRowsT + h];
+            }
+        }
+    } else
     for (int d = threadIdx.x; d < kHeadDim; d += kThreads)
 #pragma unroll
     for (int h = 0; h < kRowsT; ++h) {
@@ -1340,6 +1586,213 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
     KVQ_STAMP(6);
 }
 
+// Units (of 1 << unit_shift tokens) that a call shows of a request of `real`
+// tokens; 0 if its outputs are zeros.
+__device__ __forceinline__ int shown_units(const DecodeArgs &a, int64_t real, bool aborted, int ps_shift)
+{
+    if (aborted || real <= 0 || real > static_cast<int64_t>(a.max_pages_per_seq) << ps_shift)
+        return 0;
+    return static_cast<int>((shown_context(a, real, ps_shift).len + (1 << a.unit_shift) - 1) >> a.unit_shift);
+}
+
+// A balanced launch.  The host knows neither the lengths nor, with a table
+// padded for growth, how far they are from the row's capacity; a grid of equal
+// splits of the longest possible request leaves most of the GPU idle behind
+// the longest real one.  Here the whole batch is one line of units, request
+// after request, KV head after KV head, row block after row block, and CTA c
+// takes places [c S, (c + 1) S) of it: S is the line's length divided by the
+// resident CTAs (or by a whole number of waves of them, where a share would
+// pass 8,192 tokens).  A share that crosses (request, KV head) borders is
+// worked off border by border, one split each.  Such a border costs the CTA a
+// drained and refilled pipeline, a merge and a publication, about as long as
+// it streams pair_cost units, so every pair has that many empty places in
+// front of its units: a CTA with a border gets less to stream and ends with
+// the others.  Every CTA finds its share alone, from a block-wide scan of the
+// lengths.  A pair's splits are consecutive CTAs, so (CTA + pair) numbers the
+// launch's splits without collisions: the workspace slot.  S depends on
+// nothing but the lengths, so results repeat.  (The host keeps the line's
+// length within 31 bits.)
+//
+// Share finds CTA c's places and walks them.  It lies in shared memory, and
+// thread 0 moves it on, so that a split's arithmetic keeps its registers.
+template <bool kMulti>
+struct Share {
+    int lines;                               // pairs (KV head x row block) per request
+    int share, x, end;                       // S, the next place, the end of the CTA's places
+    int acc, u;                              // places before request r, places of each of its pairs
+    int r;
+    int64_t real;                            // tokens of request r
+    Job job;                                 // the split at x
+
+    // Places of each pair of request r.
+    __device__ __forceinline__ int places(const DecodeArgs &a, int r, int ps_shift, int64_t &real) const
+    {
+        real = __ldg(a.seq_lens + r);
+        const bool aborted = a.abort_flags != nullptr && __ldg(a.abort_flags + r) != 0;
+        const int n = shown_units(a, real, aborted, ps_shift);
+        return n > 0 ? n + a.pair_cost : 0;
+    }
+
+    // False if the CTA has none.  Also writes the zeros of the requests that
+    // show nothing, one CTA each.  Called by the whole block.
+    __device__ __forceinline__ bool find(const DecodeArgs &a, int ps_shift)
+    {
+        __shared__ int s_sum[kWarps];
+        __shared__ bool s_some;
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+        const int lines = a.num_kv_heads * (kMulti ? a.row_blocks : 1);
+        // thread t sums requests [t m, (t + 1) m)
+        const int m = (a.batch + kThreads - 1) / kThreads;
+        const int r0 = min(a.batch, static_cast<int>(threadIdx.x) * m), r1 = min(a.batch, r0 + m);
+        int64_t real = 0;
+        int mine = 0, first = 0;
+        for (int i = r0; i < r1; ++i) {
+            const int n = places(a, i, ps_shift, real);
+            first = i == r0 ? n : first;
+            mine += n;
+        }
+        int upto = mine;                                   // inclusive scan over the warp
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+            upto += lane >= off ? o : 0;
+        }
+        if (lane == 31)
+            s_sum[warp] = upto;
+        if (threadIdx.x == 0)
+            s_some = false;
+        __syncthreads();
+        int before = upto - mine, total = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            before += w < warp ? s_sum[w] : 0;
+            total += s_sum[w];
+        }
+        for (int64_t i = blockIdx.x; i < a.batch; i += gridDim.x) {
+            int64_t unused;
+            if (places(a, static_cast<int>(i), ps_shift, unused) == 0) {
+                const int64_t n = static_cast<int64_t>(a.n_query) * a.num_q_heads * kHeadDim;
+                for (int64_t j = threadIdx.x; j < n; j += kThreads)
+                    store_out(a.out, i * n + j, 0.f, a.out_fp32);
+            }
+        }
+        const int all = total * lines;
+        const int wave = a.resident_ctas * (kMaxShareTokens >> a.unit_shift);
+        const int parts = a.resident_ctas * max((all + wave - 1) / wave, 1);
+        const int share = max(a.min_split_units, (all + parts - 1) / parts);
+        const int x = static_cast<int>(blockIdx.x) * share, end = min(all, x + share);
+        // the one thread whose requests hold place x
+        if (static_cast<int64_t>(blockIdx.x) * share < all && x >= before * lines && x < (before + mine) * lines) {
+            int sum = before, n = first, i = r0;
+            if (m > 1)
+                for (n = places(a, i, ps_shift, real); x >= (sum + n) * lines; n = places(a, ++i, ps_shift, real))
+                    sum += n;
+            *this = {lines, share, x, end, sum, n, i, real, {}};
+            s_some = set_job(a);
+        }
+        __syncthreads();
+        return s_some;
+    }
+
+    // The split at x; moves x to the share's next pair.  False if the share
+    // ends in the empty places in front of the pair's units.
+    __device__ __forceinline__ bool set_job(const DecodeArgs &a)
+    {
+        const int line = (x - acc * lines) / u, start = acc * lines + line * u + a.pair_cost;
+        const int from = max(x, start), to = min(end, start - a.pair_cost + u);
+        const int c0 = start / share;
+        x = to;
+        if (from >= to)
+            return false;
+        job.b = r;
+        job.kvh = kMulti ? line / a.row_blocks : line;
+        job.rb = kMulti ? line % a.row_blocks : 0;
+        job.split = static_cast<int>(blockIdx.x) - c0;
+        job.nsplit = (start - a.pair_cost + u - 1) / share - c0 + 1;
+        job.t0 = static_cast<int64_t>(from - start) << a.unit_shift;
+        job.span = (to - from) << a.unit_shift;
+        job.base = c0 + static_cast<int64_t>(r) * lines + line;
+        job.real = real;
+        return true;
+    }
+
+    // On to the next job, by the whole block; false at the end of the share.
+    __device__ __forceinline__ bool next(const DecodeArgs &a, int ps_shift)
+    {
+        __shared__ bool s_more;
+        // the next split's copies overwrite what this one's merge read
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (threadIdx.x == 0)
+            s_more = advance(a, ps_shift);
+        __syncthreads();
+        return s_more;
+    }
+
+    __device__ __forceinline__ bool advance(const DecodeArgs &a, int ps_shift)
+    {
+        if (x >= end)
+            return false;
+        if (x == (acc + u) * lines) {                      // the next request that shows something
+            acc += u;
+            do {
+                if (++r >= a.batch)
+                    return false;                          // only if the lengths changed meanwhile
+                u = places(a, r, ps_shift, real);
+            } while (u == 0);
+        }
+        return set_job(a);
+    }
+};
+
+template <bool kBf16Cache, bool kPreciseP, bool kCluster, bool kMulti, bool kWindow, bool kBlocks>
+__global__ void __launch_bounds__(kThreads, min_ctas(kBf16Cache, kMulti, kWindow))
+decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
+                    const __grid_constant__ CUtensorMap v_map, const DecodeArgs a)
+{
+    static_assert(!kBlocks || (kWindow && !kBf16Cache), "the block-scaled build is an FP8 build with a window");
+    KVQ_STAMP(0);
+    // Launched as a programmatic dependent of the previous kernel on the
+    // stream (in a decode step: the tag check): the CTA can be resident and
+    // have its tensor maps fetched while that kernel runs, and it reads no
+    // global memory until the wait has returned, that is until the previous
+    // kernel has completed and its writes are visible.  (Asking L2 for the
+    // split's first pages before the wait made the step slower: those
+    // requests compete with the check for the memory system.)
+    if (threadIdx.x == 0) {
+        prefetch_tensor_map(&k_map);
+        prefetch_tensor_map(&v_map);
+    }
+    grid_dependency_wait();
+    KVQ_STAMP(1);
+
+    Job job;                                               // unused without a window
+    job.split = blockIdx.x;
+    job.b = blockIdx.z;
+    job.kvh = kMulti ? static_cast<int>(blockIdx.y) / a.row_blocks : static_cast<int>(blockIdx.y);
+    job.rb = kMulti ? static_cast<int>(blockIdx.y) % a.row_blocks : 0;
+    job.nsplit = 0;
+    job.span = a.split_tokens;
+    job.t0 = static_cast<int64_t>(job.split) * a.split_tokens;
+    job.base = job.real = -1;
+    if constexpr (kWindow && !kCluster) {
+        const bool balanced = a.resident_ctas > 0;
+        const int ps_shift = __ffs(a.page_size) - 1;
+        __shared__ Share<kMulti> share;
+        if (balanced && !share.find(a, ps_shift))
+            return;
+        for (bool first = true;; first = false) {
+            if (balanced)
+                job = share.job;
+            run_split<kBf16Cache, kPreciseP, kCluster, kMulti, kWindow, kBlocks>(k_map, v_map, a, job, first);
+            if (!balanced || !share.next(a, ps_shift))
+                return;
+        }
+    } else {
+        run_split<kBf16Cache, kPreciseP, kCluster, kMulti, kWindow, kBlocks>(k_map, v_map, a, job, true);
+    }
+}
+
 template <bool kBf16, bool kPrecise, bool kCluster, bool kMulti = false, bool kWindow = false, bool kBlocks = false>
 cudaError_t configure(int dev)
 {
@@ -1348,20 +1801,20 @@ cudaError_t configure(int dev)
         return cudaSuccess;
     cudaError_t e = cudaFuncSetAttribute(decode_split_kernel<kBf16, kPrecise, kCluster, kMulti, kWindow, kBlocks>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Tile<kBf16>::kSmemBytes);
+                                         smem_bytes<kBf16, kMulti, kWindow>());
     if (e == cudaSuccess && dev >= 0 && dev < 64)
         configured[dev] = 1;
     return e;
 }
 
-template <bool kBf16, bool kPrecise, bool kCluster>
+template <bool kBf16, bool kCluster, bool kMulti, bool kWindow>
 cudaLaunchConfig_t launch_config(const DecodeArgs &a, dim3 grid, cudaStream_t stream,
                                  cudaLaunchAttribute (&attr)[2])
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Tile<kBf16>::kSmemBytes;
+    cfg.dynamicSmemBytes = smem_bytes<kBf16, kMulti, kWindow>();
     cfg.stream = stream;
     // programmatic dependent launch: the grid may start while the previous
     // kernel on the stream finishes; the kernel waits before its first read
@@ -1390,10 +1843,13 @@ cudaError_t launch_split(const DecodeArgs &a, const CUtensorMap &k_map, const CU
     e = configure<kBf16, kPrecise, kCluster, kMulti, kWindow, kBlocks>(dev);
     if (e != cudaSuccess)
         return e;
-    const dim3 grid(static_cast<unsigned>(a.max_splits),
-                    static_cast<unsigned>(a.num_kv_heads * a.row_blocks), static_cast<unsigned>(a.batch));
+    const dim3 grid = kWindow && !kCluster && a.resident_ctas > 0
+                          ? dim3(static_cast<unsigned>(a.balanced_ctas))
+                          : dim3(static_cast<unsigned>(a.max_splits),
+                                 static_cast<unsigned>(a.num_kv_heads * a.row_blocks),
+                                 static_cast<unsigned>(a.batch));
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = launch_config<kBf16, kPrecise, kCluster>(a, grid, stream, attr);
+    const cudaLaunchConfig_t cfg = launch_config<kBf16, kCluster, kMulti, kWindow>(a, grid, stream, attr);
     e = cudaLaunchKernelEx(&cfg, decode_split_kernel<kBf16, kPrecise, kCluster, kMulti, kWindow, kBlocks>, k_map,
                            v_map, a);
     if (e != cudaSuccess)
@@ -1425,6 +1881,56 @@ cudaError_t launch_build(const DecodeArgs &a, const CUtensorMap &k_map, const CU
                          : launch_variant<kWindow, kBlocks, false, true>(a, k_map, v_map, stream);
     return a.cluster ? launch_variant<kWindow, kBlocks, true, false>(a, k_map, v_map, stream)
                      : launch_variant<kWindow, kBlocks, false, false>(a, k_map, v_map, stream);
+}
+
+// How many clusters of n split CTAs can be resident at once on the current
+// device (0 if clusters of n cannot be used).
+template <bool kBf16, bool kMulti, bool kWindow>
+int cluster_capacity_query(int n)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || configure<kBf16, false, true, kMulti, kWindow>(dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    DecodeArgs a = {};
+    a.max_splits = n;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg =
+        launch_config<kBf16, true, kMulti, kWindow>(a, dim3(static_cast<unsigned>(n), 1, 1), nullptr, attr);
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, decode_split_kernel<kBf16, false, true, kMulti, kWindow, false>,
+                                       &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return clusters;
+}
+
+// The same, asked once per device, n and build.
+template <bool kWindow>
+int cluster_capacity(int n, bool bf16_cache, bool multi)
+{
+    if (n < 2 || n > kMaxCluster)
+        return 0;
+    static std::mutex mu;
+    static std::map<std::tuple<int, int, bool, bool>, int> cache;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    std::lock_guard<std::mutex> lock(mu);
+    const auto key = std::make_tuple(dev, n, bf16_cache, multi);
+    auto it = cache.find(key);
+    if (it != cache.end())
+        return it->second;
+    const int c = multi ? (bf16_cache ? cluster_capacity_query<true, true, kWindow>(n)
+                                      : cluster_capacity_query<false, true, kWindow>(n))
+                        : (bf16_cache ? cluster_capacity_query<true, false, kWindow>(n)
+                                      : cluster_capacity_query<false, false, kWindow>(n));
+    cache[key] = c;
+    return c;
 }
 
 // Read (and, if asked, reset) this build's error word.

@@ -140,6 +140,12 @@ struct DecodeArgs {
     int32_t row_blocks;              // CTAs per (split, request, KV head): ceil(n_query * g / 8)
     int32_t window, num_sinks;       // windowed builds: last positions a query sees (0: all) and
                                      // first positions that stay visible
+    int32_t resident_ctas;           // balanced launch: CTAs that share the batch's units evenly; 0:
+                                     // a grid of splits of split_tokens
+    int32_t balanced_ctas;           // its grid: resident_ctas times the most waves there can be
+    int32_t unit_shift;              // log2 of a unit's tokens (a multiple of the page size)
+    int32_t min_split_units;
+    int32_t pair_cost;               // units' worth of time that a border between two pairs costs
     const int8_t *k_exp, *v_exp;     // block-scaled cache: [num_pages][Hkv][page_size / 16]
     float qk_scale_log2;             // softmax_scale * log2(e)
     uint64_t copy_wait_ns;           // a consumer's limit on one copy wait (0: give up at once)
@@ -167,6 +173,10 @@ cudaError_t launch_decode_blocks(const DecodeArgs &a, const CUtensorMap &k_map, 
                                  cudaStream_t stream);
 cudaError_t read_window_error(uint32_t *bits, bool clear);
 cudaError_t read_blocks_error(uint32_t *bits, bool clear);
+// The planner's queries for these builds (as decode_ctas_per_sm and
+// decode_cluster_capacity below).
+int decode_view_ctas_per_sm(bool bf16_cache, bool multi);
+int decode_view_cluster_capacity(int n, bool bf16_cache, bool multi);
 // Resident decode CTAs per SM for the cache type (occupancy of the kernel;
 // multi: the multi-token build, 16 query rows per CTA).
 int decode_ctas_per_sm(bool bf16_cache, bool multi = false);

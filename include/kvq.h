@@ -335,10 +335,16 @@ KVQ_API kvq_status kvq_decode_attn_mt(const kvq_cache_desc *desc, const void *q,
  *                  pages that were given back), and a row needs them only as
  *                  places: entry j / page_size is still position j's.
  *   seq_lens       the whole context, tokens outside the window included.
+ *   num_splits     as in kvq_decode_plan, over the tokens that a request can
+ *                  show.  0 (automatic): a small call runs a grid of equal
+ *                  splits; a call whose tables allow 256 MB or more of cache
+ *                  shares what its requests really show evenly among the
+ *                  GPU's resident CTAs, on the device, so that neither
+ *                  unequal lengths nor tables padded for growth leave SMs
+ *                  idle.  *split_tokens and *max_splits are then upper bounds.
  *   Every other argument as in kvq_decode_attn_mt, with either cache type; the
  *   workspace size comes from kvq_decode_plan_window with the same window,
- *   num_sinks and n.  The plan's max_splits and splits count the tokens that
- *   a request can show, not its whole context.
+ *   num_sinks and n.
  * A query that sees no position gets zeros, as does every query of a request
  * that is aborted, empty, longer than its table row or that names a page
  * outside [0, num_pages) in an entry the call reads.  What positions outside

@@ -29,13 +29,15 @@ def _no_device_errors():
 class Case:
     """Caches of random values, shuffled pages, everything unseen poisoned."""
 
-    def __init__(self, kind, lens, g, ps, n, window, sinks, hkv=2, seed=0, ev=(-10, 3), spare_pages=0):
+    def __init__(self, kind, lens, g, ps, n, window, sinks, hkv=2, seed=0, ev=(-10, 3), padded=False):
         rng = np.random.default_rng([seed, n, g, ps, window, sinks])
         self.kind, self.n, self.window, self.sinks, self.ps = kind, n, window, sinks, ps
         self.lens = np.asarray(lens, np.int32)
         B = len(lens)
         counts = [max(1, -(-int(x) // ps)) for x in lens]
-        maxp = max(counts) + spare_pages
+        maxp = max(counts)
+        if padded:                                          # a table padded until the work is shared on the device
+            maxp += -(-(256 << 20) // (256 * B * hkv * ps))
         N = sum(counts) + 3
         perm = rng.permutation(N).astype(np.int32)
         self.bt = np.full((B, maxp), -1, np.int32)
@@ -131,6 +133,36 @@ def test_long_contexts_and_many_splits(kind):
     Case(kind, [70001, 9000, 33], 4, 16, 3, 0, 0, hkv=1).check(splits=(0, 100), kinds=(True,))
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("ps,g,n", [(16, 8, 1), (128, 3, 1), (32, 5, 3), (64, 8, 16), (16, 7, 7)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (40, 20), (1000, 65), (2**30, 0)])
+def test_work_shared_on_the_device(kind, ps, g, n, window, sinks):
+    """Tables padded to 256 MB of cache and more: requests of every length in one
+    call, empty ones between (a window far larger than any context does not
+    shorten the tables' reach, one of 1,000 does, and such a call runs a grid)."""
+    c = Case(kind, LENS + (0, 0, 513, 0), g, ps, n, window, sinks, padded=True)
+    shared = window == 0 or window == 2**30
+    make = kvq.kvq_decode_plan_blocks if kind == "blocks" else kvq.kvq_decode_plan_window
+    plan = make(c.desc, len(c.lens), n, 2 * g, c.bt.shape[1], window, sinks)
+    assert (plan[0] == 8192) == shared
+    abort = (np.arange(len(c.lens)) % 5 == 3).astype(np.uint8)
+    c.check(splits=(0,), abort=abort)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_shared_work_of_many_or_few_requests(kind):
+    rng = np.random.default_rng(11)
+    lens = rng.integers(0, 200, 700)                        # more requests than threads in a block
+    lens[100:300] = 0
+    Case(kind, lens, 4, 16, 1, 0, 0, hkv=1, padded=True).check(splits=(0,), kinds=(True,))
+    Case(kind, [5], 4, 16, 1, 0, 0, hkv=1, padded=True).check(splits=(0,))
+    Case(kind, [0, 0], 4, 16, 2, 0, 0, hkv=1, padded=True).check(splits=(0,))
+    # more than one wave of 8,192-token shares would need gigabytes; shares
+    # that cross no border, one, and many
+    Case(kind, [60000, 1, 1, 30000], 2, 64, 1, 0, 0, hkv=2, padded=True).check(splits=(0,), kinds=(True,))
+    Case(kind, [33] * 40 + [20000], 2, 16, 4, 0, 0, hkv=3, padded=True).check(splits=(0,), kinds=(True,))
+
+
 def test_exponents_far_apart():
     """V exponents over the whole range the append makes, K's chosen so that
     every block keeps some weight: the running maximum of score + exponent, the
@@ -142,9 +174,9 @@ def test_exponents_far_apart():
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("n", [1, 4])
-def test_requests_that_get_zeros(kind, n):
-    c = Case(kind, [300, 0, 77, 500, 40, -5], 4, 16, n, 64, 3)
+@pytest.mark.parametrize("n,padded", [(1, False), (4, False), (1, True), (4, True)])
+def test_requests_that_get_zeros(kind, n, padded):
+    c = Case(kind, [300, 0, 77, 500, 40, -5], 4, 16, n, 64 if not padded else 0, 3, padded=padded)
     c.bt[2, 0] = c.desc.num_pages + 3                       # a sink's page out of range
     c.lens[3] = c.bt.shape[1] * 16 + 1                      # longer than its row
     abort = np.array([0, 0, 0, 0, 1, 0], np.uint8)
@@ -155,10 +187,10 @@ def test_requests_that_get_zeros(kind, n):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("splits", [1, 3, 12])
+@pytest.mark.parametrize("splits", [1, 3, 12, 0])
 def test_a_nan_that_a_query_sees_reaches_its_output_only(kind, splits):
     """One request with a NaN in K, one with a NaN in one dim of V, one clean."""
-    c = Case(kind, [200, 200, 200], 2, 16, 1, 100, 3)
+    c = Case(kind, [200, 200, 200], 2, 16, 1, 0 if splits == 0 else 100, 3, padded=splits == 0)
     nan = 0x7FC0 if kind == "bf16" else R.NAN_CODE
     for r, name in ((0, "k"), (1, "v")):
         cache = getattr(c, name)
@@ -187,23 +219,25 @@ def test_no_window_agrees_with_the_plain_entry_points():
 
 
 @pytest.mark.parametrize("kind", KINDS)
-def test_captured_replayed_and_on_another_stream(kind):
+@pytest.mark.parametrize("splits", [12, 0])
+def test_captured_replayed_and_on_another_stream(kind, splits):
     """One workspace, a captured graph replayed over new lengths and queries,
-    eager calls between; then a stream of its own."""
-    c = Case(kind, [500, 33, 1200], 4, 32, 2, 300, 4)
-    ws, out = c.workspace(12), c.out(True)
-    c.call(out, ws, 12)
+    eager calls between; then a stream of its own.  (0: shared on the device,
+    where the lengths of the replay count.)"""
+    c = Case(kind, [500, 33, 1200], 4, 32, 2, 0 if splits == 0 else 300, 4, padded=splits == 0)
+    ws, out = c.workspace(splits), c.out(True)
+    c.call(out, ws, splits)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        c.call(out, ws, 12)
+        c.call(out, ws, splits)
     first, bound = c.ref(True)
     for _ in range(3):
         out.fill_(3.0)
         graph.replay()
         torch.cuda.synchronize()
         R.assert_within(out.cpu().numpy().astype(np.float64), first, bound, "replay")
-        eager = c.call(c.out(True), ws, 12)
+        eager = c.call(c.out(True), ws, splits)
         torch.cuda.synchronize()
         assert torch.equal(eager, out)
     c.d["seq"].copy_(torch.tensor([0, 33, 900], dtype=torch.int32))
@@ -212,7 +246,7 @@ def test_captured_replayed_and_on_another_stream(kind):
     assert torch.all(out[0] == 0)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    got = c.call(c.out(True), c.workspace(12), 12, stream=side)
+    got = c.call(c.out(True), c.workspace(splits), splits, stream=side)
     side.synchronize()
     assert torch.equal(got, out)
 
@@ -220,17 +254,18 @@ def test_captured_replayed_and_on_another_stream(kind):
 def test_wait_limit_of_the_new_builds():
     """A copy wait that gives up at once: the bit, zeros, and the next call is right."""
     for kind in KINDS:
-        c = Case(kind, [4096, 300], 4, 16, 1, 3000, 4)
-        ref, bound = c.ref(True)
-        try:
-            kvq.kvq_diag_set_copy_wait_ns(0)
-            got = c.run(True, 4)
-        finally:
-            kvq.kvq_diag_set_copy_wait_ns(-1)
-        bits = kvq.kvq_device_error(clear=True)
-        assert bits & 1 and not bits & 2
-        assert np.all(got == 0.0)
-        R.assert_within(c.run(True, 4), ref, bound, kind)
+        for splits in (4, 0):
+            c = Case(kind, [4096, 300], 4, 16, 1, 0 if splits == 0 else 3000, 4, padded=splits == 0)
+            ref, bound = c.ref(True)
+            try:
+                kvq.kvq_diag_set_copy_wait_ns(0)
+                got = c.run(True, splits)
+            finally:
+                kvq.kvq_diag_set_copy_wait_ns(-1)
+            bits = kvq.kvq_device_error(clear=True)
+            assert bits & 1 and not bits & 2
+            assert np.all(got == 0.0)
+            R.assert_within(c.run(True, splits), ref, bound, kind)
 
 
 # ------------------------------------------------------------- tag check

@@ -34,6 +34,30 @@ def test_plans_count_what_a_request_can_show(plan):
     assert plan(desc(64), 4, 1, 16, 16384, 4096, 4)[0] < 8192
 
 
+def test_plans_of_large_tables_share_on_the_device():
+    """From 256 MB of cache that the tables allow: a workspace slot (8 query rows,
+    16 with several query tokens) for every (CTA, pair) that can meet, the
+    grid in whole waves of the resident CTAs (152 SMs x 3 on a host without a
+    GPU), and no more splits of a pair than the combine takes."""
+    below = kvq.kvq_decode_plan_blocks(desc(64), 16, 1, 32, 127)
+    at = kvq.kvq_decode_plan_blocks(desc(64), 16, 1, 32, 128)
+    assert below[0] < 8192 and at[0] == 8192
+    pairs = 16 * 8
+    slots = 152 * 3 + pairs
+    counters = (pairs * 4 + 255) // 256 * 256
+    assert at[2] == counters + (slots * 8 * 4 + 255) // 256 * 256 + slots * 8 * 512
+    mt = kvq.kvq_decode_plan_window(desc(64), 16, 5, 32, 128, 0, 0)          # 20 rows: two row blocks
+    slots = 152 * 3 + 2 * pairs
+    assert mt[2] == (2 * pairs * 4 + 255) // 256 * 256 + (slots * 16 * 4 + 255) // 256 * 256 + slots * 16 * 512
+    # a window that shows little of a large table
+    assert kvq.kvq_decode_plan_window(desc(64), 16, 1, 32, 4096, 500, 4)[0] < 8192
+    # 64 x 8 pairs of 1M tokens: several waves, at most 1,024 splits a pair
+    st, ms, _ = kvq.kvq_decode_plan_blocks(desc(64), 64, 1, 32, 16384)
+    assert st == 8192 and 900 < ms <= 1024
+    # an explicit split count keeps the grid
+    assert kvq.kvq_decode_plan_blocks(desc(64), 16, 1, 32, 128, 0, 0, 4)[:2] == (2048, 4)
+
+
 @pytest.mark.parametrize("plan", [kvq.kvq_decode_plan_window, kvq.kvq_decode_plan_blocks])
 def test_plans_refuse(plan):
     for args, status in [((desc(), 8, 0, 64, 513, 0, 0), 1), ((desc(), 8, 17, 64, 513, 0, 0), 2),
