@@ -17,12 +17,21 @@
 // lanes x 16 bytes, so the block's 16 new rows are eight 16-byte loads per
 // lane, all issued before the first is used, the maximum stays in registers
 // and every row is read once.  Rows leave as 8 codes per lane.  The old rows
-// are read only where the exponent grew.
+// are read only where the exponent grew.  Bound: HBM once there are some
+// thousand tokens (58,637 tokens x 8 heads, 360 MB: 53.3 us, the measured copy
+// rate), three rounds of dependent loads below (64 requests x 1 token: 2.5
+// us).  What counts is how many rows are under way: the maximum goes over
+// bf16 pairs, so that no fp32 copy of a row lives beside it, and 64 registers
+// let four CTAs fit on an SM (fp32 maxima, 128 registers and two CTAs: 81 us).
+// Variants that gave each warp several blocks, with and without the next
+// block's loads issued early, took 56.6 to 60.6 us.
 //
-// Work items are numbered by offset / 16 + 2 * request, which leaves each
-// request room for the blocks that its new tokens can touch (n new tokens
-// touch at most (n + 14) / 16 + 1) without a prefix sum; a CTA finds its
-// request by testing 256 requests at a time.
+// Work items are numbered by offset / (16 x blocks per item) + 2 * request,
+// which leaves each request room for the blocks that its new tokens can touch
+// (n new tokens touch at most (n + 14) / 16 + 1) without a prefix sum; a CTA
+// finds its request by testing 256 requests at a time.  An item is one block,
+// or with one or two KV heads as many as fill the CTA's eight warps (64,390
+// tokens of one head: 11.0 us against 16.2).
 #include "kvq_rowops.cuh"
 
 namespace kvq {
@@ -40,20 +49,28 @@ __device__ __forceinline__ int64_t request_offset(const AppendBlocksArgs &a, int
 }
 
 // First work item of request r; also the item count's bound for r = batch.
-__device__ __forceinline__ int64_t first_item(const AppendBlocksArgs &a, int64_t r)
+// (n tokens of which n / (16 G) = q remainder b touch at most G q + G + 1
+// blocks: q + 2 items of G blocks.)
+__device__ __forceinline__ int64_t first_item(const AppendBlocksArgs &a, int64_t r, int shift)
 {
-    return request_offset(a, r) / kBlockTokens + 2 * r;
+    return (request_offset(a, r) >> (4 + shift)) + 2 * r;
+}
+
+// Items of a request with n new tokens, wherever they start.
+__host__ __device__ inline int64_t items_per_request(int64_t n, int shift)
+{
+    return (((n + kBlockTokens - 2) / kBlockTokens) >> shift) + 1;
 }
 
 // The last request whose first item is not past `item` (0 if none is), by the
 // whole block: one round of tests per 256-fold of the batch.
-__device__ int64_t find_request(const AppendBlocksArgs &a, int64_t item)
+__device__ int64_t find_request(const AppendBlocksArgs &a, int64_t item, int shift)
 {
     int64_t lo = 0, count = a.batch;                       // the answer lies in [lo, lo + count)
     while (count > 1) {
         const int64_t step = (count + kThreads - 1) / kThreads;
         const int64_t at = lo + threadIdx.x * step;
-        const bool reached = threadIdx.x * step < count && first_item(a, at) <= item;
+        const bool reached = threadIdx.x * step < count && first_item(a, at, shift) <= item;
         const int passed = __syncthreads_count(reached);
         const int64_t skip = passed > 0 ? (passed - 1) * step : 0;
         lo += skip;
@@ -62,11 +79,13 @@ __device__ int64_t find_request(const AppendBlocksArgs &a, int64_t item)
     return lo;
 }
 
-// Largest magnitude (bf16 bits) of a word's two elements, NaN as 0.
-__device__ __forceinline__ uint32_t amax2(uint32_t w)
+// The larger of m's and |w|'s bf16 elements, pair by pair (m holds no NaN and
+// no sign; a NaN in w is passed over).
+__device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t w)
 {
-    const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
-    return max(lo > 0x7F80u ? 0u : lo, hi > 0x7F80u ? 0u : hi);
+    uint32_t r;
+    asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %2;\n\tmax.bf16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(m), "r"(w));
+    return r;
 }
 
 // Least e in range with m <= 448 * 2^e, for the bf16 bits of m >= 0:
@@ -91,21 +110,26 @@ __device__ __forceinline__ uint32_t rescale4_e4m3(uint32_t codes, float mul)
            (static_cast<uint32_t>(f32x2_to_e4m3x2(p1.x * mul, p1.y * mul)) << 16);
 }
 
-__global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendBlocksArgs a)
+// kShift: log2 of the blocks per work item.
+template <int kShift>
+__global__ void __launch_bounds__(kThreads, 4) append_blocks_kernel(const AppendBlocksArgs a)
 {
     grid_launch_dependents();              // a dependent decode launch may begin now
     const int64_t item = blockIdx.x;
-    int64_t r, local;
+    int64_t r, local;                      // the request, and the warp's block among those it writes
     if (a.token_offsets == nullptr) {      // equal counts: the same number of items each
-        const int64_t n = a.num_tokens / a.batch, per = (n + kBlockTokens - 2) / kBlockTokens + 1;
+        const int64_t per = items_per_request(a.num_tokens / a.batch, kShift);
         r = item / per;
-        local = item % per;
+        local = (item % per) << kShift;
     } else {
-        r = find_request(a, item);
-        local = item - first_item(a, r);
+        r = find_request(a, item, kShift);
+        local = (item - first_item(a, r, kShift)) << kShift;
     }
-    const int unit = blockIdx.y * kWarps + threadIdx.x / 32;
-    if (unit >= 2 * a.num_kv_heads)
+    const int units = 2 * a.num_kv_heads, warp = threadIdx.x / 32;
+    const int unit = kShift > 0 ? warp % units : static_cast<int>(blockIdx.y) * kWarps + warp;
+    if (kShift > 0)
+        local += warp / units;
+    if (unit >= units)
         return;
     const bool is_v = unit >= a.num_kv_heads;
     const int h = is_v ? unit - a.num_kv_heads : unit;
@@ -116,56 +140,64 @@ __global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendBlo
     const int64_t len = __ldg(a.seq_lens + r), start = len - n;
     const bool aborted = a.abort_flags != nullptr && __ldg(a.abort_flags + r) != 0;
     if (aborted || n <= 0 || off < 0 || off + n > a.num_tokens || start < 0 ||
-        len > static_cast<int64_t>(a.max_pages_per_seq) * a.page_size)
+        len > static_cast<int64_t>(a.max_pages_per_seq) * a.page_size || local < 0)
         return;
     const int64_t block = start / kBlockTokens + local, pos0 = block * kBlockTokens;
-    if (local < 0 || pos0 >= len)
+    if (pos0 >= len)
         return;
     const int lo = static_cast<int>(max(start - pos0, static_cast<int64_t>(0)));     // new rows of the block
     const int hi = static_cast<int>(min(len - pos0, static_cast<int64_t>(kBlockTokens)));
-    const int32_t page = __ldg(a.block_table + r * a.max_pages_per_seq + pos0 / a.page_size);
+    const int ps_shift = __ffs(a.page_size) - 1, bpp_shift = ps_shift - 4;           // blocks per page: page_size / 16
+    const int32_t page = __ldg(a.block_table + r * a.max_pages_per_seq + (block >> bpp_shift));
 
-    const uint16_t *src = static_cast<const uint16_t *>(is_v ? a.v_new : a.k_new) + h * kHeadDim + part * 8;
+    // bytes from one token's row to the next, and this lane's part of row `half`
+    const uint32_t row_step = static_cast<uint32_t>(a.num_kv_heads) * kHeadDim * 2;
+    const uint8_t *src = static_cast<const uint8_t *>(is_v ? a.v_new : a.k_new) +
+                         (off - start + pos0 + half) * row_step + h * kHeadDim * 2 + part * 16;
     uint4 x[kLoads];
-    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
         const int row = i * kRowsPerLoad + half;
         x[i] = make_uint4(0, 0, 0, 0);
         if (row >= lo && row < hi)
-            x[i] = __ldg(reinterpret_cast<const uint4 *>(src + (off + pos0 + row - start) * a.num_kv_heads * kHeadDim));
+            x[i] = __ldg(reinterpret_cast<const uint4 *>(src));
+        src += kRowsPerLoad * row_step;
     }
     if (page < 0 || page >= a.num_pages)
         return;
-    const int sub = static_cast<int>(pos0 % a.page_size) / kBlockTokens, per_page = a.page_size / kBlockTokens;
-    int8_t *exp = (is_v ? a.v_exp : a.k_exp) + (static_cast<int64_t>(page) * a.num_kv_heads + h) * per_page + sub;
+    const int sub = static_cast<int>(block & ((1 << bpp_shift) - 1));
+    const int64_t tile = static_cast<int64_t>(page) * a.num_kv_heads + h;
+    int8_t *exp = (is_v ? a.v_exp : a.k_exp) + (tile << bpp_shift) + sub;
     const int e_old = lo > 0 ? *exp : kBlockExpMin;
+    uint32_t m2 = 0;                                       // largest magnitudes of even and odd dims
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-        m = max(max(m, max(amax2(x[i].x), amax2(x[i].y))), max(amax2(x[i].z), amax2(x[i].w)));
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
-    const int need = block_exponent(m);
+        m2 = amax2(amax2(amax2(amax2(m2, x[i].x), x[i].y), x[i].z), x[i].w);
+    const int need = block_exponent(__reduce_max_sync(0xFFFFFFFFu, max(m2 & 0xFFFFu, m2 >> 16)));
     const int e = lo > 0 ? max(e_old, need) : need;
 
     uint8_t *dst = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) +
-                   ((static_cast<int64_t>(page) * a.num_kv_heads + h) * a.page_size + sub * kBlockTokens) * kHeadDim +
-                   part * 8;
+                   ((tile << ps_shift) + sub * kBlockTokens) * kHeadDim + part * 8;
     if (lo > 0 && e > e_old) {                             // the earlier rows move to the new exponent
         const int d = e - e_old;
         const float mul = d > 126 ? 0.f : __int_as_float((127 - d) << 23);
-        uint2 c[kLoads];
+        constexpr int kOld = 4;                            // rows per lane and trip
+#pragma unroll 1
+        for (int i0 = 0; i0 < kLoads; i0 += kOld) {
+            uint2 c[kOld];
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int row = i * kRowsPerLoad + half;
-            if (row < lo)
-                c[i] = *reinterpret_cast<const uint2 *>(dst + row * kHeadDim);
-        }
+            for (int i = 0; i < kOld; ++i) {
+                const int row = (i0 + i) * kRowsPerLoad + half;
+                if (row < lo)
+                    c[i] = *reinterpret_cast<const uint2 *>(dst + row * kHeadDim);
+            }
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int row = i * kRowsPerLoad + half;
-            if (row < lo)
-                *reinterpret_cast<uint2 *>(dst + row * kHeadDim) =
-                    make_uint2(rescale4_e4m3(c[i].x, mul), rescale4_e4m3(c[i].y, mul));
+            for (int i = 0; i < kOld; ++i) {
+                const int row = (i0 + i) * kRowsPerLoad + half;
+                if (row < lo)
+                    *reinterpret_cast<uint2 *>(dst + row * kHeadDim) =
+                        make_uint2(rescale4_e4m3(c[i].x, mul), rescale4_e4m3(c[i].y, mul));
+            }
         }
     }
     // 2^-e: e can be a stored exponent of up to 127, and 2^-127 is subnormal
@@ -181,24 +213,27 @@ __global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendBlo
         *exp = static_cast<int8_t>(e);
 }
 
+template <int kShift>
+cudaError_t launch(const AppendBlocksArgs &a, cudaStream_t stream)
+{
+    const int64_t items = a.token_offsets == nullptr
+                              ? a.batch * items_per_request(a.num_tokens / a.batch, kShift)
+                              : (a.num_tokens >> (4 + kShift)) + 2 * static_cast<int64_t>(a.batch);
+    if (items > 0x7FFFFFFF)
+        return cudaErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(items),
+                    kShift > 0 ? 1u : static_cast<unsigned>((2 * a.num_kv_heads + kWarps - 1) / kWarps));
+    append_blocks_kernel<kShift><<<grid, kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
 } // namespace
 
 cudaError_t launch_append_blocks(const AppendBlocksArgs &a, cudaStream_t stream)
 {
     if (a.batch == 0 || a.num_tokens == 0)
         return cudaSuccess;
-    int64_t items;
-    if (a.token_offsets == nullptr) {
-        const int64_t n = a.num_tokens / a.batch;
-        items = a.batch * ((n + kBlockTokens - 2) / kBlockTokens + 1);
-    } else {
-        items = a.num_tokens / kBlockTokens + 2 * static_cast<int64_t>(a.batch);
-    }
-    if (items > 0x7FFFFFFF)
-        return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>((2 * a.num_kv_heads + kWarps - 1) / kWarps));
-    append_blocks_kernel<<<grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return a.num_kv_heads == 1 ? launch<2>(a, stream) : a.num_kv_heads == 2 ? launch<1>(a, stream) : launch<0>(a, stream);
 }
 
 } // namespace kvq
