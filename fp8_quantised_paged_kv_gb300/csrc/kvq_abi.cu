@@ -293,7 +293,7 @@ kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads
     // Many query rows over an FP8 cache: the tensor-memory kernel, one CTA
     // per (split, request, KV head) for all n g rows, splits in whole
     // 64-token tiles, combined through the workspace.
-    const bool umma = view == nullptr && kvq::use_umma(bf16, n_query, g);
+    const bool umma = view == nullptr ? kvq::use_umma(bf16, n_query, g) : kvq::use_umma_view(bf16, n_query, g);
     const int64_t min_unit = umma ? kvq::kUmmaTileTokens : kChunkTokens;
     const int64_t unit = d->page_size > min_unit ? d->page_size : min_unit;
     // CTAs per split: one per (request, KV head), or in the BF16 multi-token
@@ -307,7 +307,7 @@ kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads
     p->resident_ctas = p->balanced_ctas = p->unit_shift = p->min_split_units = p->pair_cost = 0;
     if (static_cast<int64_t>(d->num_kv_heads) * row_blocks > 65535)
         return KVQ_ERR_UNSUPPORTED;                  // the grid's second dimension
-    if (view != nullptr && num_splits == 0 && batch > 0 && balanced_pays(pairs, max_ctx, bf16) &&
+    if (view != nullptr && !umma && num_splits == 0 && batch > 0 && balanced_pays(pairs, max_ctx, bf16) &&
         plan_balanced(pairs, max_ctx, d->page_size, bf16, multi, p))
         return KVQ_OK;
     int64_t want;
@@ -841,6 +841,9 @@ kvq_status kvq_decode_attn_window(const kvq_cache_desc *desc, const void *q, int
     CUtensorMap km, vm;
     if (!make_cache_map(&km, desc, k_cache) || !make_cache_map(&vm, desc, v_cache))
         return KVQ_ERR_CUDA;
+    if (kvq::use_umma_view(desc->cache_dtype == KVQ_CACHE_BF16, num_query_tokens, call.args.group))
+        return to_status(
+            kvq::launch_decode_umma_view(call.args, km, vm, reinterpret_cast<cudaStream_t>(stream)));
     return to_status(kvq::launch_decode_window(call.args, km, vm, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -864,6 +867,9 @@ kvq_status kvq_decode_attn_blocks(const kvq_cache_desc *desc, const void *q, int
     CUtensorMap km, vm;
     if (!make_cache_map(&km, desc, k_cache) || !make_cache_map(&vm, desc, v_cache))
         return KVQ_ERR_CUDA;
+    if (kvq::use_umma_view(false, num_query_tokens, call.args.group))
+        return to_status(
+            kvq::launch_decode_umma_view(call.args, km, vm, reinterpret_cast<cudaStream_t>(stream)));
     return to_status(kvq::launch_decode_blocks(call.args, km, vm, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1074,7 +1080,7 @@ KVQ_API kvq_status kvq_phase_stamps(int32_t which, unsigned long long *host, siz
 
 kvq_status kvq_device_error(uint32_t *bits, int32_t clear)
 {
-    uint32_t a = 0, b = 0, c = 0, d = 0, f = 0;
+    uint32_t a = 0, b = 0, c = 0, d = 0, f = 0, g = 0;
     cudaError_t e = kvq::read_device_error(&a, clear != 0);
     if (e == cudaSuccess)
         e = kvq::read_w4_error(&b, clear != 0);
@@ -1084,8 +1090,10 @@ kvq_status kvq_device_error(uint32_t *bits, int32_t clear)
         e = kvq::read_window_error(&d, clear != 0);
     if (e == cudaSuccess)
         e = kvq::read_blocks_error(&f, clear != 0);
+    if (e == cudaSuccess)
+        e = kvq::read_umma_view_error(&g, clear != 0);
     if (bits)
-        *bits = a | b | c | d | f;
+        *bits = a | b | c | d | f | g;
     return to_status(e);
 }
 

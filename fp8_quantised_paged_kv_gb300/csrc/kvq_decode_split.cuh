@@ -61,6 +61,7 @@
 #include "kvq_internal.h"
 #include "kvq_ptx.cuh"
 #include "kvq_rowops.cuh"
+#include "kvq_view.cuh"
 
 namespace kvq {
 
@@ -631,27 +632,6 @@ struct Job {
     int b, kvh, rb, split, nsplit, span;
     int64_t t0, base, real;                  // real: the request's tokens, or -1 (read them)
 };
-
-// The context a windowed call shows of a request of `real` tokens, without
-// the hole between the sinks' pages and the page where the first query's
-// window starts: its length, the sinks' pages, the hole's pages, and the
-// window's start, which like every position counts the shortened context.
-struct Shown {
-    int64_t len, sink_pages, hole, win0;
-};
-__device__ __forceinline__ Shown shown_context(const DecodeArgs &a, int64_t real, int ps_shift)
-{
-    Shown v = {real, 0, 0, 0};
-    if (a.window > 0) {
-        const int64_t start = real - a.n_query + 1 - a.window;
-        const int64_t ps = static_cast<int64_t>(1) << ps_shift;
-        v.sink_pages = (min(real, static_cast<int64_t>(a.num_sinks)) + ps - 1) >> ps_shift;
-        v.hole = max((max(start, static_cast<int64_t>(0)) >> ps_shift) - v.sink_pages, static_cast<int64_t>(0));
-        v.len = real - (v.hole << ps_shift);
-        v.win0 = start - (v.hole << ps_shift);
-    }
-    return v;
-}
 
 template <bool kBf16Cache, bool kPreciseP, bool kCluster, bool kMulti, bool kWindow, bool kBlocks>
 __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtensorMap &v_map, const DecodeArgs &a,

@@ -207,6 +207,17 @@ cudaError_t launch_decode_umma(const DecodeArgs &a, const CUtensorMap &k_map, co
 // Resident CTAs per SM of that kernel (bf16 output; at most 2: tensor memory).
 int decode_umma_ctas_per_sm();
 cudaError_t read_umma_error(uint32_t *bits, bool clear);
+// Its builds with a window, and for the block-scaled cache (a.k_exp set).
+cudaError_t launch_decode_umma_view(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                                    cudaStream_t stream);
+cudaError_t read_umma_view_error(uint32_t *bits, bool clear);
+// Query rows per KV head from which a windowed or block-scaled multi-token
+// call over an FP8 cache takes it.
+constexpr int kUmmaViewMinRows = 33;
+inline bool use_umma_view(bool bf16_cache, int n_query, int group)
+{
+    return !bf16_cache && n_query > 1 && n_query * group >= kUmmaViewMinRows;
+}
 
 // Box height (in 128-byte rows) of one bulk copy for a page size.
 inline int tma_box_rows(int page_size, bool bf16_cache)

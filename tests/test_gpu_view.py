@@ -101,8 +101,11 @@ class Case:
         return out.float().cpu().numpy().astype(np.float64)
 
     def ref(self, fp32, abort=None):
+        # 33 and more query rows per KV head of an FP8 cache: the tensor-memory kernel
+        rows = self.n * self.q_bits.shape[2] // self.k.shape[1]
+        cut = 2.0 ** -32 if self.kind != "bf16" and self.n > 1 and rows >= 33 else 2.0 ** -40
         return R.attention(self.q_bits, self.k, self.v, self.bt, self.lens, SCALE, self.window, self.sinks,
-                           ks=self.ks, vs=self.vs, ke=self.ke, ve=self.ve, abort=abort, fp32=fp32)
+                           ks=self.ks, vs=self.vs, ke=self.ke, ve=self.ve, abort=abort, fp32=fp32, cut=cut)
 
     def check(self, splits=(0, 1, 5, 12), kinds=(False, True), abort=None, what=""):
         t = None if abort is None else torch.from_numpy(abort).to(DEV)
@@ -144,7 +147,8 @@ def test_work_shared_on_the_device(kind, ps, g, n, window, sinks):
     shared = window == 0 or window == 2**30
     make = kvq.kvq_decode_plan_blocks if kind == "blocks" else kvq.kvq_decode_plan_window
     plan = make(c.desc, len(c.lens), n, 2 * g, c.bt.shape[1], window, sinks)
-    assert (plan[0] == 8192) == shared
+    tensor_memory = kind != "bf16" and n > 1 and n * g >= 33   # grids of its own
+    assert (plan[0] == 8192) == (shared and not tensor_memory)
     abort = (np.arange(len(c.lens)) % 5 == 3).astype(np.uint8)
     c.check(splits=(0,), abort=abort)
 

@@ -30,7 +30,7 @@ def positions(cache, bt_row, ps, h, pos):
 
 
 def attention(q_bits, k, v, bt, lens, scale, window, sinks, *, ks=None, vs=None, ke=None, ve=None,
-              abort=None, fp32=False):
+              abort=None, fp32=False, cut=2.0 ** -40):
     """(out, bound) in fp64, [B][n][Hq][D].
 
     q_bits bf16 bits; k, v caches: uint8 codes (scales ks, vs per head, or
@@ -45,7 +45,8 @@ def attention(q_bits, k, v, bt, lens, scale, window, sinks, *, ks=None, vs=None,
       - a weight is rounded to 16 bits (f16 2^-11, for a bf16 cache 2^-8; with
         fp32 output a second term carries the rest: 2^-22, bf16 2^-16); f16
         terms, which hold 2^15 times the weight relative to the largest, are
-        cut at multiples of 2^-24, so by at most 2^-40 of the largest;
+        cut at multiples of 2^-24, so by at most 2^-40 of the largest
+        (``cut``; the tensor-memory kernel holds 2^7 times: 2^-32);
       - sums in fp32 of up to L / 32 terms per warp and a merge of at most
         1024 partials: (L / 32 + 64) * 2^-23;
       - the output's own rounding, 2^-8 or 2^-24 of it.
@@ -106,7 +107,7 @@ def attention(q_bits, k, v, bt, lens, scale, window, sinks, *, ks=None, vs=None,
                 rel = rel + (2.0 ** -8 if is_bf16 else 2.0 ** -11)
             lost = 0.0
             if not is_bf16:
-                lost = 2.0 ** -40 * top * (seen @ (np.abs(kv[1]) / unit[:, None])) / safe
+                lost = cut * top * (seen @ (np.abs(kv[1]) / unit[:, None])) / safe
             bnd = scores + rel * mean + lost
             bnd = bnd + (2.0 ** -24 if fp32 else 2.0 ** -8) * (np.abs(o) + bnd) + 1e-37
             out[b, :, h * g:(h + 1) * g] = np.where(some, o, 0).reshape(n, g, D)
