@@ -74,6 +74,7 @@ kvq_status check_desc(const kvq_cache_desc *d)
 
 struct Plan {
     int32_t split_tokens, max_splits, row_blocks;
+    bool umma;                    // the tensor-memory kernel
     int32_t cluster;              // 0, or the cluster size (= max_splits) of the cluster combine
     // balanced launch (DecodeArgs); 0 resident CTAs: a grid of splits
     int32_t resident_ctas, balanced_ctas, unit_shift, min_split_units, pair_cost;
@@ -167,7 +168,12 @@ int64_t single_wave_splits(int64_t pairs, int64_t max_ctx, int64_t unit, int64_t
             continue;                                           // more than one wave
         const double split_us = static_cast<double>(split) * bytes_per_tok / cta_rate * 1e6;
         const double stream_us = std::pow(std::pow(total_us, 4.0) + std::pow(split_us, 4.0), 0.25);
-        const double combine_us = splits == 1 ? 0.0 : cluster ? 2.5 : 9.0;
+        // a workspace combine is one CTA's work: it grows with the splits that
+        // it reads (counted for the windowed and block-scaled builds: one pair
+        // of 60,000 tokens takes 24 us in 48 splits, 65 us in 313)
+        const double per_split_us = !view ? 0.0 : multi ? 0.38 : 0.16;
+        const double combine_us =
+            splits == 1 ? 0.0 : cluster ? 2.5 : 9.0 + per_split_us * static_cast<double>(splits);
         const double est = 11.0 + stream_us + combine_us;
         if (est < best_us - 1e-9) {
             best_us = est;
@@ -213,9 +219,9 @@ int32_t visible_pages(const View &v, int32_t page_size, int32_t max_pages, int32
 // 48.2 us against 58.3; 16 x 8 x 1,024..16,384 tokens, 4 query tokens: 73.4
 // against 105).  The border is put at 256 MB of cache that the tables allow.
 constexpr int64_t kBalancedMinBytes = 256 << 20;
-bool balanced_pays(int64_t pairs, int64_t max_ctx, bool bf16)
+bool balanced_pays(int64_t jobs, int64_t max_ctx, bool bf16)
 {
-    return pairs * max_ctx * (bf16 ? 512 : 256) >= kBalancedMinBytes;
+    return jobs * max_ctx * (bf16 ? 512 : 256) >= kBalancedMinBytes;
 }
 
 // Units that a border between two (request, KV head) pairs costs a CTA of a
@@ -293,7 +299,9 @@ kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads
     // Many query rows over an FP8 cache: the tensor-memory kernel, one CTA
     // per (split, request, KV head) for all n g rows, splits in whole
     // 64-token tiles, combined through the workspace.
-    const bool umma = view == nullptr ? kvq::use_umma(bf16, n_query, g) : kvq::use_umma_view(bf16, n_query, g);
+    const bool umma = view == nullptr ? kvq::use_umma(bf16, n_query, g)
+                                      : kvq::use_umma_view(bf16, n_query, g, batch, d->num_kv_heads, max_ctx);
+    p->umma = umma;
     const int64_t min_unit = umma ? kvq::kUmmaTileTokens : kChunkTokens;
     const int64_t unit = d->page_size > min_unit ? d->page_size : min_unit;
     // CTAs per split: one per (request, KV head), or in the BF16 multi-token
@@ -307,7 +315,8 @@ kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads
     p->resident_ctas = p->balanced_ctas = p->unit_shift = p->min_split_units = p->pair_cost = 0;
     if (static_cast<int64_t>(d->num_kv_heads) * row_blocks > 65535)
         return KVQ_ERR_UNSUPPORTED;                  // the grid's second dimension
-    if (view != nullptr && !umma && num_splits == 0 && batch > 0 && balanced_pays(pairs, max_ctx, bf16) &&
+    if (view != nullptr && !umma && num_splits == 0 && batch > 0 &&
+        balanced_pays(static_cast<int64_t>(batch) * d->num_kv_heads, max_ctx, bf16) &&
         plan_balanced(pairs, max_ctx, d->page_size, bf16, multi, p))
         return KVQ_OK;
     int64_t want;
@@ -323,6 +332,13 @@ kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads
         const int64_t big = (max_ctx + kMaxSplitTokens - 1) / kMaxSplitTokens;
         if (jobs * big >= slots) {
             want = big;
+            // windowed and block-scaled calls that split: at least 2.5 waves, so that
+            // requests shorter than the table allows leave no long last wave
+            // (16 x 8 x 1,000..16,000 tokens, 64 rows: 123 us in 3 splits, 136
+            // in 2)
+            const int64_t waves = (5 * slots + 2 * jobs - 1) / (2 * jobs);
+            if (view != nullptr && big > 1 && want < waves)
+                want = waves;
         } else {
             want = slots / jobs;
             const int64_t most = max_ctx / kMinAutoSplitTokens;
@@ -841,7 +857,7 @@ kvq_status kvq_decode_attn_window(const kvq_cache_desc *desc, const void *q, int
     CUtensorMap km, vm;
     if (!make_cache_map(&km, desc, k_cache) || !make_cache_map(&vm, desc, v_cache))
         return KVQ_ERR_CUDA;
-    if (kvq::use_umma_view(desc->cache_dtype == KVQ_CACHE_BF16, num_query_tokens, call.args.group))
+    if (call.plan.umma)
         return to_status(
             kvq::launch_decode_umma_view(call.args, km, vm, reinterpret_cast<cudaStream_t>(stream)));
     return to_status(kvq::launch_decode_window(call.args, km, vm, reinterpret_cast<cudaStream_t>(stream)));
@@ -867,7 +883,7 @@ kvq_status kvq_decode_attn_blocks(const kvq_cache_desc *desc, const void *q, int
     CUtensorMap km, vm;
     if (!make_cache_map(&km, desc, k_cache) || !make_cache_map(&vm, desc, v_cache))
         return KVQ_ERR_CUDA;
-    if (kvq::use_umma_view(false, num_query_tokens, call.args.group))
+    if (call.plan.umma)
         return to_status(
             kvq::launch_decode_umma_view(call.args, km, vm, reinterpret_cast<cudaStream_t>(stream)));
     return to_status(kvq::launch_decode_blocks(call.args, km, vm, reinterpret_cast<cudaStream_t>(stream)));

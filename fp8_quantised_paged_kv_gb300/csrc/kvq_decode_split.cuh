@@ -1020,8 +1020,8 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
     // count from the split's start, at most one chunk past its end.  Below
     // full_end every row of the CTA sees every token.
     [[maybe_unused]] int vis_col[kNT][2] = {};
-    int64_t full_end = t1;
-    if constexpr (kMulti) {
+    [[maybe_unused]] int64_t full_end = t1;
+    if constexpr (kMulti && !kWindow) {
         const int64_t vis0 = len - a.n_query + 1;
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
@@ -1033,30 +1033,37 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
             }
         full_end = min(t1, vis0 + R.row0 / g);
     }
-    // Window: per row the first position of its window, as a count from the
-    // split's start (clamped as above), and likewise the end of the sinks;
-    // the tokens between are masked.  V rows that no row of the CTA sees (up
-    // to the first row's window) are zeroed, so what they hold cannot reach
-    // the product.  Outside [mask_lo, mask_hi) no token is masked.
-    [[maybe_unused]] int win_col[kNT][2] = {};
-    [[maybe_unused]] int sink_end = 0, win_first = 0;
-    [[maybe_unused]] int64_t mask_lo = 0, mask_hi = 0;
+    // Windowed builds keep less in registers, counts from the split's start
+    // (t0) all: query token i of the call sees the positions below vis0 + i
+    // but for those from sink_end to win + i; the tokens i of this lane's score
+    // columns lie in a nibble each of tok_col.  V rows that no row of the CTA
+    // sees (sink_end up to win_first) are zeroed, so what they hold cannot
+    // reach the product.  Below full_to and outside [sink_end, mask_hi) no
+    // token is masked.
+    [[maybe_unused]] uint32_t tok_col = 0;
+    [[maybe_unused]] int vis0 = 0, sink_end = 0, full_to = 0;
+    [[maybe_unused]] int win = -2 * kChunkTokens, win_first = win, mask_hi = win;      // window 0: before everything
     if constexpr (kWindow) {
-        if (a.window > 0) {
-            auto rel = [&](int64_t v) {
-                v -= t0;
-                const int64_t most = split_tokens + kChunkTokens;
-                return static_cast<int>(v < -1 ? -1 : (v > most ? most : v));
-            };
+        auto rel = [&](int64_t v) {                        // query tokens are at most 15 further on
+            v -= t0;
+            const int64_t most = split_tokens + 2 * kChunkTokens;
+            return static_cast<int>(v < -2 * kChunkTokens ? -2 * kChunkTokens : (v > most ? most : v));
+        };
+        const int first = kMulti ? R.row0 / g : 0, last = kMulti ? (R.row0 + R.nrows - 1) / g : 0;
+        vis0 = rel(len - a.n_query + 1);
+        full_to = rel(min(t1, len - a.n_query + 1 + first));
+        if constexpr (kMulti)
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    win_col[nt][j] = rel(kMulti ? win0 + (R.row0 + nt * kMaxGroup + 2 * tq + j) / g : win0);
+                    tok_col |= static_cast<uint32_t>(min((R.row0 + nt * kMaxGroup + 2 * tq + j) / g, 15))
+                               << (4 * (2 * nt + j));
+        if (a.window > 0) {
+            win = rel(win0);
             sink_end = rel(a.num_sinks);
-            win_first = rel(kMulti ? win0 + R.row0 / g : win0);
-            mask_lo = a.num_sinks;
-            mask_hi = kMulti ? win0 + (R.row0 + R.nrows - 1) / g : win0;
+            win_first = rel(win0 + first);
+            mask_hi = rel(win0 + last);
         }
     }
     if constexpr (kSmemQ) {                                // each warp stores a quarter of the fragments
@@ -1118,23 +1125,13 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
         }
         const int64_t left = t1 - tok;
         const int n_valid = left < kChunkTokens ? static_cast<int>(left) : kChunkTokens;   // V rows
-        int s_valid[kNT][2];                             // tokens of the chunk each score column sees
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                s_valid[nt][j] = kMulti ? min(n_valid, vis_col[nt][j] - c * kChunkTokens) : n_valid;
-        // window: rows [hole_lo, hole_hi) of the chunk are masked
-        [[maybe_unused]] const int hole_lo = sink_end - c * kChunkTokens;
-        [[maybe_unused]] int hole_hi[kNT][2];
-        [[maybe_unused]] const int hole_v = win_first - c * kChunkTokens;
-        if constexpr (kWindow) {
+        [[maybe_unused]] int s_valid[kNT][2];            // tokens of the chunk each score column sees
+        if constexpr (!kWindow)
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    hole_hi[nt][j] = win_col[nt][j] - c * kChunkTokens;
-        }
+                    s_valid[nt][j] = kMulti ? min(n_valid, vis_col[nt][j] - c * kChunkTokens) : n_valid;
         [[maybe_unused]] float blk_mul[2], blk_add[2];     // 2^ek and ev of the two 16-token m-tiles
         if constexpr (kBlocks) {
 #pragma unroll
@@ -1245,9 +1242,13 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
                             x = fmaf(sc[nt][mt][i], mul[i & 1], blk_add[mt]);
                         else
                             x = sc[nt][mt][i] * qk_col[nt][i & 1];
-                        bool keep = kFull || row < s_valid[nt][i & 1];
-                        if constexpr (kWindow && !kFull)
-                            keep = keep && !(row >= hole_lo && row < hole_hi[nt][i & 1]);
+                        bool keep = true;
+                        if constexpr (kWindow && !kFull) {
+                            const int at = c * kChunkTokens + row, ti = (tok_col >> (4 * (2 * nt + (i & 1)))) & 15;
+                            keep = row < n_valid && at < vis0 + ti && !(at >= sink_end && at < win + ti);
+                        } else if constexpr (!kFull) {
+                            keep = row < s_valid[nt][i & 1];
+                        }
                         x = keep ? x : -INFINITY;
                         sc[nt][mt][i] = x;
                         mx[i & 1] = fmaxf(mx[i & 1], x);
@@ -1336,7 +1337,7 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
                         const uint4 hi = lds128(vs, swz(line, (gq & 3) * 2 + 1));
                         bool keep = kFull || rows[q] < n_valid;
                         if constexpr (kWindow && !kFull)
-                            keep = keep && !(rows[q] >= hole_lo && rows[q] < hole_v);
+                            keep = keep && !(c * kChunkTokens + rows[q] >= sink_end && c * kChunkTokens + rows[q] < win_first);
                         R[q][0] = keep ? lo.x : 0u; R[q][1] = keep ? lo.y : 0u;
                         R[q][2] = keep ? lo.z : 0u; R[q][3] = keep ? lo.w : 0u;
                         R[q][4] = keep ? hi.x : 0u; R[q][5] = keep ? hi.y : 0u;
@@ -1362,7 +1363,7 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
                         const uint4 v = lds128(vs, swz(rows[q], gq));
                         bool keep = kFull || rows[q] < n_valid;
                         if constexpr (kWindow && !kFull)
-                            keep = keep && !(rows[q] >= hole_lo && rows[q] < hole_v);
+                            keep = keep && !(c * kChunkTokens + rows[q] >= sink_end && c * kChunkTokens + rows[q] < win_first);
                         R[q][0] = keep ? v.x : 0u; R[q][1] = keep ? v.y : 0u;
                         R[q][2] = keep ? v.z : 0u; R[q][3] = keep ? v.w : 0u;
                     }
@@ -1383,7 +1384,9 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
                 }
             }
         };
-        if (tok + kChunkTokens <= full_end && (!kWindow || tok + kChunkTokens <= mask_lo || tok >= mask_hi))
+        const int chunk_end = (c + 1) * kChunkTokens;
+        if (kWindow ? chunk_end <= full_to && (chunk_end <= sink_end || chunk_end - kChunkTokens >= mask_hi)
+                    : tok + kChunkTokens <= full_end)
             chunk(std::true_type{});
         else
             chunk(std::false_type{});

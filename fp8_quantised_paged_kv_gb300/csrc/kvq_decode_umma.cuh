@@ -175,6 +175,98 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, ui
     return false;
 }
 
+// The combine of the builds with a window or block exponents, by the whole
+// CTA.  Every (row, split) lse is fetched at once into a table, a warp per row
+// turns them into weights over their sum, and each thread merges 16-byte
+// pieces of the output with a round of kRound splits' loads in flight (the
+// combine below, one thread per row and four warps, took 30 to 100 us on 8 to
+// 19 splits of 40 to 128 rows).  A NaN sum (a split with lse +inf) makes the
+// row NaN.
+__device__ void combine_all(const DecodeArgs &a, int b, int kvh, int nsplit, float *sm)
+{
+    __shared__ int s_last_split;
+    __shared__ int s_row[128];                             // row_id of local row r, relative to the request's first
+    __syncthreads();
+    unsigned int *counter = a.counters + static_cast<int64_t>(b) * gridDim.y + kvh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0)
+        s_last_split = atom_add_acq_rel_gpu(counter, 1u) == static_cast<unsigned int>(nsplit - 1);
+    __syncthreads();
+    if (!s_last_split)
+        return;
+    const int R = a.n_query * a.group;
+    const int64_t first = row_id(a, b, kvh, 0);
+    if (tid < R)
+        s_row[tid] = static_cast<int>(row_id(a, b, kvh, tid) - first);
+    __syncthreads();
+    // rows in groups whose weights fit the table
+    const int per = min(R, max(1, kCombineTable / nsplit));
+    for (int r0 = 0; r0 < R; r0 += per) {
+        const int rows = min(per, R - r0);
+        float *sm_w = sm;                                  // [rows][nsplit]
+        for (int i = tid; i < rows * nsplit; i += kUThreads) {
+            const int r = i / nsplit, s2 = i - r * nsplit;
+            sm_w[i] = __ldcg(a.ws_lse + (first + s_row[r0 + r]) * a.max_splits + s2);
+        }
+        __syncthreads();
+        for (int r = warp; r < rows; r += kUThreads / 32) {
+            float *w = sm_w + r * nsplit;
+            float M = -INFINITY;
+            bool bad = false;
+            for (int s2 = lane; s2 < nsplit; s2 += 32) {
+                bad |= w[s2] != w[s2];
+                M = fmaxf(M, w[s2]);
+            }
+            bad = __any_sync(0xFFFFFFFFu, bad);
+            for (int off = 16; off > 0; off >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+            float S = 0.f;
+            for (int s2 = lane; s2 < nsplit; s2 += 32) {
+                const float e = bad || w[s2] == -INFINITY ? 0.f : fast_exp2(w[s2] - M);
+                w[s2] = e;
+                S += e;
+            }
+            for (int off = 16; off > 0; off >>= 1)
+                S += __shfl_xor_sync(0xFFFFFFFFu, S, off);
+            const float inv = S == 0.f ? 0.f : 1.f / S;    // NaN stays
+            for (int s2 = lane; s2 < nsplit; s2 += 32)
+                w[s2] *= inv;
+        }
+        __syncthreads();
+        constexpr int kRound = 8;
+        for (int it = tid; it < rows * 32; it += kUThreads) {
+            const int r = it >> 5, d4 = 4 * (it & 31);
+            const int64_t id = first + s_row[r0 + r];
+            const float *from = a.ws_o + id * a.max_splits * kHeadDim + d4;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int s0 = 0; s0 < nsplit; s0 += kRound) {
+                float4 v[kRound];
+#pragma unroll
+                for (int k = 0; k < kRound; ++k)
+                    v[k] = s0 + k < nsplit
+                               ? __ldcg(reinterpret_cast<const float4 *>(from + static_cast<int64_t>(s0 + k) * kHeadDim))
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < kRound; ++k)
+                    if (s0 + k < nsplit) {
+                        const float w = sm_w[r * nsplit + s0 + k];
+                        // a split without a result, or without weight, may hold anything
+                        if (w != 0.f) {
+                            acc.x += w * v[k].x;
+                            acc.y += w * v[k].y;
+                            acc.z += w * v[k].z;
+                            acc.w += w * v[k].w;
+                        }
+                    }
+            }
+            store_row_value4(a.out, id * kHeadDim + d4, acc, a.out_fp32);
+        }
+        __syncthreads();
+    }
+    if (tid == 0)
+        *counter = 0;                                      // ready for the next call
+}
+
 // kTpc: tokens of a tile each copy of the rows takes: 32 for up to 64 rows
 // (two copies fill the 128 M slots), 64 for 65 .. 128 rows (one copy).
 template <bool kPrecise, int kTpc, bool kWindow, bool kBlocks>
@@ -846,7 +938,13 @@ decode_mt_umma_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
             tmem_dealloc(tmem, kTmemCols);
         }
     }
-    if (nsplit == 1 || tid >= 128)
+    if (nsplit == 1)
+        return;
+    if constexpr (kWindow) {
+        combine_all(a, b, kvh, nsplit, reinterpret_cast<float *>(sm));
+        return;
+    }
+    if (tid >= 128)
         return;
 
     // ---------------------------------------------- combine of the splits
@@ -882,13 +980,12 @@ decode_mt_umma_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
                 if (v != -INFINITY)
                     S += fast_exp2(v - M);
             }
-        S = bad_row ? 0.f : S;                              // NaN where a split's lse is +inf (kWindow)
+        S = bad_row ? 0.f : S;
         sm_S[tid] = S;
         if (table)
             for (int s2 = 0; s2 < nsplit; ++s2) {
                 const float v = __ldcg(a.ws_lse + base + s2);
-                const bool some = kWindow ? S != 0.f : S > 0.f;
-                sm_w[tid * nsplit + s2] = some && v != -INFINITY ? fast_exp2(v - M) / S : 0.f;
+                sm_w[tid * nsplit + s2] = S > 0.f && v != -INFINITY ? fast_exp2(v - M) / S : 0.f;
             }
         else
             sm_w[tid] = M;                                  // the max, for weights computed on the fly
@@ -899,7 +996,7 @@ decode_mt_umma_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
         const int64_t id = row_id(a, b, kvh, rr);
         const float S = sm_S[rr];
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (kWindow ? S != 0.f : S > 0.f) {
+        if (S > 0.f) {
             const int64_t base = id * a.max_splits;
 #pragma unroll 4
             for (int s2 = 0; s2 < nsplit; ++s2) {

@@ -211,12 +211,21 @@ cudaError_t read_umma_error(uint32_t *bits, bool clear);
 cudaError_t launch_decode_umma_view(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                                     cudaStream_t stream);
 cudaError_t read_umma_view_error(uint32_t *bits, bool clear);
-// Query rows per KV head from which a windowed or block-scaled multi-token
-// call over an FP8 cache takes it.
+// A windowed or block-scaled multi-token call over an FP8 cache takes it from
+// 33 query rows per KV head (three row blocks of the mma.sync build, each of
+// which converts every tile again; up to 64 rows cost the tensor-memory kernel
+// the same) and enough work to fill its pipeline, cache bytes that the tables
+// allow times rows: 8 requests x 8 KV heads x 8,193 tokens, 40, 64 and 128
+// rows: 65, 59 and 83 us against 95, 120 and 222; 2 x 4 x 3,000 tokens: 20, 25
+// and 38 us against 11, 12 and 16; even at 2,000 tokens of 8 x 8 and 40 rows.
 constexpr int kUmmaViewMinRows = 33;
-inline bool use_umma_view(bool bf16_cache, int n_query, int group)
+constexpr double kUmmaViewMinWork = 2e9;
+inline bool use_umma_view(bool bf16_cache, int n_query, int group, int64_t batch, int64_t num_kv_heads,
+                          int64_t max_tokens)
 {
-    return !bf16_cache && n_query > 1 && n_query * group >= kUmmaViewMinRows;
+    const double rows = n_query * group;
+    return !bf16_cache && n_query > 1 && rows >= kUmmaViewMinRows &&
+           256.0 * rows * static_cast<double>(batch * num_kv_heads) * static_cast<double>(max_tokens) >= kUmmaViewMinWork;
 }
 
 // Box height (in 128-byte rows) of one bulk copy for a page size.

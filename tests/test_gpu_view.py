@@ -101,7 +101,7 @@ class Case:
         return out.float().cpu().numpy().astype(np.float64)
 
     def ref(self, fp32, abort=None):
-        # 33 and more query rows per KV head of an FP8 cache: the tensor-memory kernel
+        # 33 and more query rows per KV head of an FP8 cache can take the tensor-memory kernel
         rows = self.n * self.q_bits.shape[2] // self.k.shape[1]
         cut = 2.0 ** -32 if self.kind != "bf16" and self.n > 1 and rows >= 33 else 2.0 ** -40
         return R.attention(self.q_bits, self.k, self.v, self.bt, self.lens, SCALE, self.window, self.sinks,
