@@ -893,7 +893,12 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
     const int parts = kChunkTokens / box_tok;                       // 1 or 2 copies per tensor
     const uint32_t part_bytes = static_cast<uint32_t>(box_tok * T::kRowBytes);
     // evict-first unless other row blocks of the split read the same pages
-    const uint64_t policy = kMulti && a.row_blocks > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+    auto make_policy = [&]() {
+        return kMulti && a.row_blocks > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+    };
+    uint64_t policy = 0;
+    if constexpr (!kWindow)
+        policy = make_policy();
 
 
     // Issue the copies of this warp's local chunk `it`: the whole warp, one
@@ -915,7 +920,7 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
             const int64_t row = (static_cast<int64_t>(page) * a.num_kv_heads + kvh) * ps + (ptok & (ps - 1));
             uint8_t *dst = ring + st * T::kStageBytes + (lane < np ? 0 : T::kBytes) + part * part_bytes;
             tma_load_2d(dst, lane < np ? static_cast<const void *>(&k_map) : static_cast<const void *>(&v_map), 0,
-                        static_cast<int32_t>(row * lines_per_tok), &my_full[st], policy);
+                        static_cast<int32_t>(row * lines_per_tok), &my_full[st], kWindow ? make_policy() : policy);
         }
     };
 

@@ -153,6 +153,71 @@ def test_work_shared_on_the_device(kind, ps, g, n, window, sinks):
     c.check(splits=(0,), abort=abort)
 
 
+# Few requests of many heads: enough work for the tensor-memory kernel (cache
+# bytes x query rows of 2e9 and more, 33 rows and more per KV head)
+TM_LENS = (5000, 0, 40, 4097, 1, 130, 2500, 9000)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "blocks"])
+@pytest.mark.parametrize("n,g,ps", [(5, 8, 16), (8, 8, 64), (11, 6, 32), (16, 8, 128), (16, 3, 16)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (4000, 70), (2**31 - 1, 3)])
+def test_tensor_memory_kernel(kind, n, g, ps, window, sinks):
+    c = Case(kind, TM_LENS, g, ps, n, window, sinks, hkv=8, ev=(-20, 10))
+    assert 256 * n * g * 8 * len(TM_LENS) * min(9000, window or 9000) >= 2e9
+    c.check(splits=(0, 1, 3, 12))
+
+
+@pytest.mark.parametrize("kind", ["fp8", "blocks"])
+def test_tensor_memory_kernel_edges(kind):
+    """Scores that rise along the context (the stale maximum is raised tile after
+    tile), exponents far apart, a NaN in K and in V, requests that get zeros,
+    and a copy wait that gives up."""
+    n, g, ps = 8, 8, 16
+    c = Case(kind, TM_LENS, g, ps, n, 0, 0, hkv=8, ev=(-48, 48), seed=3)
+    big = np.arange(9000)                                   # K of request 7 grows along its positions
+    pages = c.bt[7][big // ps]
+    grow = R.encode((W.bf16_bits_to_f32(c.q_bits[7, 0, 0]).astype(np.float64)[None, :] * np.linspace(-60, 60, 9000)[:, None]))
+    c.k[pages, :, big % ps] = grow[:, None, :]
+    c.d["k"] = torch.from_numpy(c.k).to(DEV)
+    c.check(splits=(0, 1, 5))
+    abort = np.array([0, 0, 0, 1, 0, 0, 0, 0], np.uint8)
+    c.bt[0, 7], c.lens[6] = c.desc.num_pages, c.bt.shape[1] * ps + 1
+    c.d["bt"], c.d["seq"] = torch.from_numpy(c.bt).to(DEV), torch.from_numpy(c.lens).to(DEV)
+    for s in (0, 1, 5):
+        got = c.run(True, s, torch.from_numpy(abort).to(DEV))
+        for r in (0, 1, 3, 6):
+            assert np.all(got[r] == 0.0), (s, r)
+        assert np.any(got[7] != 0)
+    c = Case(kind, TM_LENS, g, ps, n, 4000, 70, hkv=8)
+    c.k[c.bt[0, 4000 // ps], 2, 4000 % ps, 5] = R.NAN_CODE  # seen by every query of request 0
+    c.v[c.bt[3, 4000 // ps], 1, 4000 % ps, 9] = R.NAN_CODE
+    c.d["k"], c.d["v"] = torch.from_numpy(c.k).to(DEV), torch.from_numpy(c.v).to(DEV)
+    for s in (0, 1, 5):
+        got = c.run(True, s)
+        assert np.isnan(got[0, :, 16:24]).all() and np.isnan(got[0]).sum() == n * 8 * D
+        assert np.isnan(got[3, :, 8:16, 9]).all() and np.isnan(got[3]).sum() == n * 8
+        assert not np.isnan(got[[1, 2, 4, 5, 6, 7]]).any()
+    c = Case(kind, TM_LENS, g, ps, n, 4000, 70, hkv=8)
+    ref, bound = c.ref(True)
+    try:
+        kvq.kvq_diag_set_copy_wait_ns(0)
+        got = c.run(True, 3)
+    finally:
+        kvq.kvq_diag_set_copy_wait_ns(-1)
+    bits = kvq.kvq_device_error(clear=True)
+    assert bits & 1 and not bits & 2
+    assert np.all(got == 0.0)
+    R.assert_within(c.run(True, 3), ref, bound, kind)
+
+
+def test_tensor_memory_kernel_many_splits():
+    """More (row, split) weights than the combine's table holds: rows in groups."""
+    c = Case("blocks", [70000, 3000], 8, 16, 16, 0, 0, hkv=1, seed=9)
+    plan = kvq.kvq_decode_plan_blocks(c.desc, 2, 16, 8, c.bt.shape[1], 0, 0, 128)
+    assert plan[1] * 128 > 8192 and 256 * 128 * 2 * 70000 >= 2e9
+    c.check(splits=(128, 0), kinds=(True,))
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_shared_work_of_many_or_few_requests(kind):
     rng = np.random.default_rng(11)
