@@ -1087,6 +1087,12 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
     // f16 weight, and with it the second term of the precise form, is then cut
     // at 2^-39 of the largest weight instead of 2^-24.
     constexpr float kLift = kWindow ? 15.f : 0.f;
+    // 16-bit terms of a weight in the PV product: one for bf16 output (f16
+    // 2^-12, for a bf16 cache bf16 2^-9: an output of many tokens averages
+    // them below its own 2^-9; a second bf16 term cost 2 to 10 %), for fp32
+    // output two f16 terms (2^-24) or two bf16 ones (2^-18), in the windowed
+    // builds three (2^-27).
+    constexpr int kTerms = !kPreciseP ? 1 : kWindow && kBf16Cache ? 3 : 2;
     float m_run[kNT][2], l_run[kNT][2];
     float o[kNT][8][4];
 #pragma unroll
@@ -1303,8 +1309,10 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
             // every n-tile
     #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
+                // a weight as the sum of kTerms 16-bit terms, each carrying
+                // what the rounding of those before it dropped
                 uint32_t pb0[kNT], pb1[kNT];
-                [[maybe_unused]] uint32_t pl0[kNT], pl1[kNT];
+                [[maybe_unused]] uint32_t pl0[kNT], pl1[kNT], pm0[kNT], pm1[kNT];
     #pragma unroll
                 for (int nt = 0; nt < kNT; ++nt) {
                     uint32_t x0, x1;
@@ -1317,8 +1325,7 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
                     }
                     pb0[nt] = movmatrix_trans(x0);
                     pb1[nt] = movmatrix_trans(x1);
-                    if constexpr (kPreciseP) {
-                        // second term carries what the 16-bit rounding of P dropped
+                    if constexpr (kTerms > 1) {
                         const float2 h0 = kBf16Cache ? bf16x2_to_f32x2(x0) : f16x2_to_f32x2(x0);
                         const float2 h1 = kBf16Cache ? bf16x2_to_f32x2(x1) : f16x2_to_f32x2(x1);
                         const float *p = sc[nt][mt];
@@ -1328,6 +1335,11 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
                                                        : f32x2_to_f16x2(p[2] - h1.x, p[3] - h1.y);
                         pl0[nt] = movmatrix_trans(y0);
                         pl1[nt] = movmatrix_trans(y1);
+                        if constexpr (kTerms > 2) {
+                            const float2 l0 = bf16x2_to_f32x2(y0), l1 = bf16x2_to_f32x2(y1);
+                            pm0[nt] = movmatrix_trans(f32x2_to_bf16x2(p[0] - h0.x - l0.x, p[1] - h0.y - l0.y));
+                            pm1[nt] = movmatrix_trans(f32x2_to_bf16x2(p[2] - h1.x - l1.x, p[3] - h1.y - l1.y));
+                        }
                     }
                 }
                 // V rows of token slots 2tq, 2tq+1, 2tq+8, 2tq+9 of this m-tile
@@ -1357,8 +1369,10 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
     #pragma unroll
                         for (int nt = 0; nt < kNT; ++nt) {
                             mma_bf16(o[nt][i], a0, a1, a2, a3, pb0[nt], pb1[nt]);
-                            if constexpr (kPreciseP)
+                            if constexpr (kTerms > 1)
                                 mma_bf16(o[nt][i], a0, a1, a2, a3, pl0[nt], pl1[nt]);
+                            if constexpr (kTerms > 2)
+                                mma_bf16(o[nt][i], a0, a1, a2, a3, pm0[nt], pm1[nt]);
                         }
                     }
                 } else {
@@ -1382,7 +1396,7 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
     #pragma unroll
                         for (int nt = 0; nt < kNT; ++nt) {
                             mma_f16(o[nt][i], a0, a1, a2, a3, pb0[nt], pb1[nt]);
-                            if constexpr (kPreciseP)
+                            if constexpr (kTerms > 1)
                                 mma_f16(o[nt][i], a0, a1, a2, a3, pl0[nt], pl1[nt]);
                         }
                     }

@@ -42,8 +42,9 @@ def attention(q_bits, k, v, bt, lens, scale, window, sinks, *, ks=None, vs=None,
         their size in log2 units; a score error moves its own weight by that
         much relative (the far smaller weights of far smaller scores too), and
         with it the weighted sum and the sum of the weights;
-      - a weight is rounded to 16 bits (f16 2^-11, for a bf16 cache 2^-8; with
-        fp32 output a second term carries the rest: 2^-22, bf16 2^-16); f16
+      - a weight becomes 16-bit terms, each rounding what those before it left
+        (one f16 term for bf16 output, 2^-11, two for fp32, 2^-22; with a bf16
+        cache one bf16 term, 2^-8, and three, 2^-24); f16
         terms, which hold 2^15 times the weight relative to the largest, are
         cut at multiples of 2^-24, so by at most 2^-40 of the largest
         (``cut``; the tensor-memory kernel holds 2^7 times: 2^-32);
@@ -102,9 +103,8 @@ def attention(q_bits, k, v, bt, lens, scale, window, sinks, *, ks=None, vs=None,
             size = np.where(seen, np.abs(s) / np.log(2) + np.abs(np.log2(unit))[None, :] + 32, 0)
             wrong = p * np.expm1(ds + 2.0 ** -22 * size) / safe         # each weight's own share
             scores = wrong @ np.abs(kv[1]) + wrong.sum(axis=1, keepdims=True) * np.abs(o)
-            rel = (2.0 ** -16 if is_bf16 else 2.0 ** -22) + (L / 32 + 64) * 2.0 ** -23
-            if not fp32:
-                rel = rel + (2.0 ** -8 if is_bf16 else 2.0 ** -11)
+            rel = (2.0 ** -24 if fp32 else 2.0 ** -8) if is_bf16 else (2.0 ** -22 if fp32 else 2.0 ** -11)
+            rel = rel + (L / 32 + 64) * 2.0 ** -23
             lost = 0.0
             if not is_bf16:
                 lost = cut * top * (seen @ (np.abs(kv[1]) / unit[:, None])) / safe
