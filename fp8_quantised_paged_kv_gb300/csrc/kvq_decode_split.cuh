@@ -1093,6 +1093,11 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
     // output two f16 terms (2^-24) or two bf16 ones (2^-18), in the windowed
     // builds three (2^-27).
     constexpr int kTerms = !kPreciseP ? 1 : kWindow && kBf16Cache ? 3 : 2;
+    // For fp32 output a tile's products are summed from zero and added to O
+    // by fp32 additions that round: the tensor core cuts what it adds to a
+    // large accumulator, always towards zero (error against fp64, 64 requests
+    // of up to 5,000 tokens: bf16 cache 1.6e-6, 3.9e-7 so; FP8 9.9e-7, 3.7e-7).
+    constexpr bool kSumApart = kWindow && kPreciseP;
     float m_run[kNT][2], l_run[kNT][2];
     float o[kNT][8][4];
 #pragma unroll
@@ -1368,11 +1373,19 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
                         const uint32_t a3 = prmt(R[2][i], R[3][i], 0x7632);
     #pragma unroll
                         for (int nt = 0; nt < kNT; ++nt) {
-                            mma_bf16(o[nt][i], a0, a1, a2, a3, pb0[nt], pb1[nt]);
-                            if constexpr (kTerms > 1)
-                                mma_bf16(o[nt][i], a0, a1, a2, a3, pl0[nt], pl1[nt]);
-                            if constexpr (kTerms > 2)
-                                mma_bf16(o[nt][i], a0, a1, a2, a3, pm0[nt], pm1[nt]);
+                            if constexpr (kSumApart) {
+                                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma_bf16(t, a0, a1, a2, a3, pm0[nt], pm1[nt]);
+                                mma_bf16(t, a0, a1, a2, a3, pl0[nt], pl1[nt]);
+                                mma_bf16(t, a0, a1, a2, a3, pb0[nt], pb1[nt]);
+    #pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    o[nt][i][q] += t[q];
+                            } else {
+                                mma_bf16(o[nt][i], a0, a1, a2, a3, pb0[nt], pb1[nt]);
+                                if constexpr (kTerms > 1)
+                                    mma_bf16(o[nt][i], a0, a1, a2, a3, pl0[nt], pl1[nt]);
+                            }
                         }
                     }
                 } else {
@@ -1395,9 +1408,18 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
                         const uint32_t a2 = lo16_e4m3x2_to_f16x2(p23), a3 = hi16_e4m3x2_to_f16x2(p23);
     #pragma unroll
                         for (int nt = 0; nt < kNT; ++nt) {
-                            mma_f16(o[nt][i], a0, a1, a2, a3, pb0[nt], pb1[nt]);
-                            if constexpr (kTerms > 1)
-                                mma_f16(o[nt][i], a0, a1, a2, a3, pl0[nt], pl1[nt]);
+                            if constexpr (kSumApart) {
+                                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma_f16(t, a0, a1, a2, a3, pl0[nt], pl1[nt]);
+                                mma_f16(t, a0, a1, a2, a3, pb0[nt], pb1[nt]);
+    #pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    o[nt][i][q] += t[q];
+                            } else {
+                                mma_f16(o[nt][i], a0, a1, a2, a3, pb0[nt], pb1[nt]);
+                                if constexpr (kTerms > 1)
+                                    mma_f16(o[nt][i], a0, a1, a2, a3, pl0[nt], pl1[nt]);
+                            }
                         }
                     }
                 }

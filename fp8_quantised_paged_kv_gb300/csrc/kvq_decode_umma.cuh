@@ -84,8 +84,17 @@ constexpr int kStageBytes = 2 * kTile * 128;              // K then V rows of on
 constexpr int kOffRing = 0;
 constexpr int kOffKV = kOffRing + kStages * kStageBytes;  // operand buffers: K f16 [64 tok][64 d] x 2, V alike
 constexpr int kKVBytes = 32768;
-constexpr int kKV = 4;                                    // operand buffers in flight
-constexpr int kDataBytes = kOffKV + kKV * kKVBytes;
+constexpr int kMaxKV = 4;                                 // operand buffers in flight
+constexpr int kDataBytes = kOffKV + kMaxKV * kKVBytes;
+// With fp32 output the builds with a window or block exponents take O out of
+// tensor memory every kFlushTiles tiles into fp32 sums that round, kept where
+// two of the operand buffers would be (128 rows x 512 bytes, 16-byte chunks
+// xor-swizzled by the row): the tensor core cuts what it adds to a large
+// accumulator, always towards zero, which came to 1.4e-6 of the output over 78
+// tiles (8.7e-7 so, 128 rows; 7.2e-7 and 5.0e-7 with 64).
+constexpr int kFlushTiles = 16;
+constexpr int kOffSums = kOffKV + 2 * kKVBytes;
+static_assert(kOffSums + 128 * kHeadDim * 4 <= kDataBytes, "the sums fit in two operand buffers");
 constexpr int kMergeStride = 132;                         // floats per row of the copies' merge buffer
 constexpr int kMaxPageList = 8192 / 16 + 8;
 // tensor-memory columns (lane m = M-row m): Q as f16 pairs, two score
@@ -95,7 +104,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColQ = 0, kColS = 64, kColO = 192, kColP = 320, kColPlo = 384;
 constexpr float kRaiseThreshold = 8.f;
 constexpr int kCombineTable = 8192;                       // (row, split) weights the combine keeps in shared memory
-constexpr int kNumBars = 2 * kStages + 2 * kKV + 3 * 2 + 3;   // see the barrier map in the kernel
+constexpr int kNumBars = 2 * kStages + 2 * kMaxKV + 3 * 2 + 3;   // see the barrier map in the kernel
 
 __host__ __device__ constexpr int smem_bytes()
 {
@@ -274,6 +283,8 @@ __global__ void __launch_bounds__(kUThreads, 1)
 decode_mt_umma_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                       const DecodeArgs a)
 {
+    constexpr bool kFlush = kWindow && kPrecise;           // O summed apart (kFlushTiles)
+    constexpr int kKV = kFlush ? 2 : kMaxKV;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -406,6 +417,9 @@ decode_mt_umma_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
     const int copy = m / Rp, r = m % Rp;
     const bool row_valid = tid < 128 && r < R;
     float m_used = -INFINITY, l_sum = 0.f;
+    // kFlush: this thread's row of the sums, and what they are behind m_used by
+    [[maybe_unused]] float4 *sums = reinterpret_cast<float4 *>(sm + kOffSums) + (tid & 127) * (kHeadDim / 4);
+    [[maybe_unused]] float sums_mul = 1.f;
     int issued = 0;                                        // producer lane 0: tiles whose copies it issued
 
     if (bad) {
@@ -587,7 +601,8 @@ decode_mt_umma_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)         // P: 8 columns (16 tokens) per k step
                         umma_f16_ts(tmem + kColO, tmem + kColP + 32u * pb + 8u * kk,
-                                    dvb + static_cast<uint64_t>(kk * 128), kIdescPV, jp > 0 || kk > 0);
+                                    dvb + static_cast<uint64_t>(kk * 128), kIdescPV,
+                                    (kFlush ? jp % kFlushTiles != 0 : jp > 0) || kk > 0);
                     if constexpr (kPrecise) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
@@ -752,7 +767,34 @@ decode_mt_umma_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
                 // O holds earlier tiles of row m: rescale it once O += P V of
                 // tile j - 1 is done (warp-wide loads and stores: the other
                 // lanes multiply by 1)
-                const bool rescale = raise && m_used != -INFINITY && j > 0;
+                const bool flush = kFlush && j > 0 && j % kFlushTiles == 0;
+                const bool rescale = raise && m_used != -INFINITY && j > 0 && !flush;
+                if constexpr (kFlush) {
+                    if (flush) {                           // O += P V starts from zero with this tile
+                        if (!__all_sync(0xFFFFFFFFu, wait_or_abort(&pv_done[(j - 1) % kKV], ((j - 1) / kKV) & 1,
+                                                                   kCopyWaitLimitNs, abort_flag, 4u)))
+                            break;
+                        tmem_fence_after_sync();
+#pragma unroll 1
+                        for (int cc = 0; cc < 8; ++cc) {
+                            uint32_t o[16];
+                            tmem_ld16(tmem + lane_base + kColO + 16 * cc, o);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float4 &at = sums[(4 * cc + i) ^ (m & 7)];
+                                float4 v = j == kFlushTiles ? make_float4(0.f, 0.f, 0.f, 0.f) : at;
+                                v.x = fmaf(v.x, sums_mul, __uint_as_float(o[4 * i]));
+                                v.y = fmaf(v.y, sums_mul, __uint_as_float(o[4 * i + 1]));
+                                v.z = fmaf(v.z, sums_mul, __uint_as_float(o[4 * i + 2]));
+                                v.w = fmaf(v.w, sums_mul, __uint_as_float(o[4 * i + 3]));
+                                at = v;
+                            }
+                        }
+                        sums_mul = 1.f;
+                    }
+                    if (raise)
+                        sums_mul *= alpha;
+                }
                 if (__any_sync(0xFFFFFFFFu, rescale)) {
                     if (!__all_sync(0xFFFFFFFFu, wait_or_abort(&pv_done[(j - 1) % kKV], ((j - 1) / kKV) & 1,
                                                                kCopyWaitLimitNs, abort_flag, 4u)))
@@ -902,6 +944,18 @@ decode_mt_umma_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
             for (int cc = 0; cc < 8; ++cc) {
                 uint32_t o[16];
                 tmem_ld16(tmem + lane_base + kColO + 16 * cc, o);
+                if constexpr (kFlush) {
+                    if (n_tiles > kFlushTiles) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 v = sums[(4 * cc + i) ^ (m & 7)];
+                            o[4 * i] = __float_as_uint(fmaf(v.x, sums_mul, __uint_as_float(o[4 * i])));
+                            o[4 * i + 1] = __float_as_uint(fmaf(v.y, sums_mul, __uint_as_float(o[4 * i + 1])));
+                            o[4 * i + 2] = __float_as_uint(fmaf(v.z, sums_mul, __uint_as_float(o[4 * i + 2])));
+                            o[4 * i + 3] = __float_as_uint(fmaf(v.w, sums_mul, __uint_as_float(o[4 * i + 3])));
+                        }
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
                     const float4 v = wgt != 0.f
