@@ -44,18 +44,20 @@ __device__ __forceinline__ void copy_small(uint8_t *base, const CopyPagesArgs &a
     }
 }
 
-__global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_constant__ CopyPagesArgs a, int pieces,
-                                                                int small_blocks)
+// Row y of the grid: `extra` of the exponents' blocks (small_blocks for each
+// exponent array; first, so that their dependent loads hide behind the
+// pages'), then the num_listed pages of cache y, `pieces` blocks each.
+__global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_constant__ CopyPagesArgs a,
+                                                                uint32_t pieces, uint32_t small_blocks,
+                                                                uint32_t extra)
 {
     grid_launch_dependents();              // a dependent decode launch may begin now
-    if (static_cast<int>(blockIdx.y) >= a.num_caches) {
-        // rows past the caches: small_blocks blocks for each exponent array in turn
-        const int64_t block = (static_cast<int64_t>(blockIdx.y) - a.num_caches) * gridDim.x + blockIdx.x;
-        const int64_t array = block / small_blocks;
-        if (array >= a.num_exps)
+    if (blockIdx.x < extra) {
+        const uint32_t block = blockIdx.y * extra + blockIdx.x, array = block / small_blocks;
+        if (array >= static_cast<uint32_t>(a.num_exps))
             return;
         uint8_t *base = static_cast<uint8_t *>(a.arrays[a.num_caches + array]);
-        const int64_t worker = (block % small_blocks) * kThreads + threadIdx.x;
+        const int64_t worker = static_cast<int64_t>(block - array * small_blocks) * kThreads + threadIdx.x;
         const int64_t workers = static_cast<int64_t>(small_blocks) * kThreads;
         const uintptr_t unit = reinterpret_cast<uintptr_t>(base) | static_cast<uintptr_t>(a.exp_page_bytes);
         if (unit % 16 == 0)
@@ -67,7 +69,7 @@ __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_const
         return;
     }
     uint8_t *base = static_cast<uint8_t *>(a.arrays[blockIdx.y]);
-    const int pair = blockIdx.x / pieces, piece = blockIdx.x % pieces;
+    const uint32_t pair = (blockIdx.x - extra) / pieces, piece = (blockIdx.x - extra) - pair * pieces;
     const int64_t s = __ldg(a.src_pages + pair), d = __ldg(a.dst_pages + pair);
     if (s < 0 || s >= a.num_pages || d < 0 || d >= a.num_pages || s == d)
         return;
@@ -92,17 +94,16 @@ cudaError_t launch_copy_pages(const CopyPagesArgs &a, cudaStream_t stream)
     if (a.num_listed == 0 || a.num_caches + a.num_exps == 0)
         return cudaSuccess;
     const int64_t pieces = (a.cache_page_bytes + kPiece - 1) / kPiece;
-    if (pieces * a.num_listed > 0x7FFFFFFF)
+    const int64_t per_cache = a.num_caches > 0 ? pieces * a.num_listed : 0;
+    const int64_t small_blocks = (a.exp_page_bytes * a.num_listed + kThreads * kSmallPerThread - 1) /
+                                 (kThreads * kSmallPerThread);
+    const int64_t rows = a.num_caches > 0 ? a.num_caches : 1;
+    const int64_t extra = (small_blocks * a.num_exps + rows - 1) / rows;
+    if (per_cache + extra > 0x7FFFFFFF || extra * rows > 0x7FFFFFFF)
         return cudaErrorInvalidValue;
-    // A row of the grid per cache; the exponents' few blocks share the rows
-    // behind them (a row each cost 25 us of empty blocks on 8,002 pages of 64 KB).
-    const int64_t per_row = pieces * a.num_listed;
-    const int64_t small = (a.exp_page_bytes * a.num_listed + kThreads * kSmallPerThread - 1) /
-                          (kThreads * kSmallPerThread);
-    const int64_t small_blocks = small < per_row ? small : per_row;
-    const int64_t rows = a.num_caches + (small_blocks * a.num_exps + per_row - 1) / per_row;
-    const dim3 grid(static_cast<unsigned>(per_row), static_cast<unsigned>(rows));
-    copy_pages_kernel<<<grid, kThreads, 0, stream>>>(a, static_cast<int>(pieces), static_cast<int>(small_blocks));
+    const dim3 grid(static_cast<unsigned>(per_cache + extra), static_cast<unsigned>(rows));
+    copy_pages_kernel<<<grid, kThreads, 0, stream>>>(a, static_cast<uint32_t>(pieces),
+                                                     static_cast<uint32_t>(small_blocks), static_cast<uint32_t>(extra));
     return cudaGetLastError();
 }
 
