@@ -325,6 +325,9 @@ def kvq_decode_attn_mt(desc, q, k_cache, v_cache, k_scale, v_scale, block_table,
 
 def _plan_view(fn, desc, batch, num_query_tokens, num_q_heads, max_pages_per_seq, window, num_sinks,
                num_splits):
+    for v in (batch, num_query_tokens, num_q_heads, max_pages_per_seq, window, num_sinks, num_splits):
+        if not -2**31 <= v < 2**31:                       # ctypes would wrap it
+            raise OverflowError(f"{fn}: {v} does not fit 32 bits")
     a, b, c = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_size_t()
     st = getattr(load(), fn)(ctypes.byref(desc.c()), batch, num_query_tokens, num_q_heads,
                              max_pages_per_seq, window, num_sinks, num_splits, ctypes.byref(a),

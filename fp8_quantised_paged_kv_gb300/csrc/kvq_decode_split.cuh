@@ -947,7 +947,9 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
     }
 
     if constexpr (kBlocks) {
-        // the exponents of the split's blocks, one byte each, behind the first copies
+        // the exponents of the split's blocks, one byte each, behind the first
+        // copies (through L2: the append that wrote them may have run on this
+        // SM beside this CTA)
         const int n_blocks = static_cast<int>((t1 - t0 + kBlockTokens - 1) / kBlockTokens);
         const int bpp_shift = ps_shift - 4;                // blocks per page: ps / 16
         for (int i = threadIdx.x; i < 2 * n_chunks; i += kThreads) {
@@ -957,8 +959,8 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
             }
             const int64_t at = ((static_cast<int64_t>(page_list[i >> bpp_shift]) * a.num_kv_heads + kvh) << bpp_shift) +
                                (i & ((1 << bpp_shift) - 1));
-            const int ek = max(static_cast<int>(__ldg(a.k_exp + at)), -126);
-            const int ev = max(static_cast<int>(__ldg(a.v_exp + at)), -126);
+            const int ek = max(static_cast<int>(__ldcg(a.k_exp + at)), -126);
+            const int ev = max(static_cast<int>(__ldcg(a.v_exp + at)), -126);
             blk_exp[i] = static_cast<uint16_t>((ek & 0xFF) | (min(ev, 126) << 8));
         }
     }
@@ -1651,8 +1653,8 @@ struct Share {
     // Places of each pair of request r.
     __device__ __forceinline__ int places(const DecodeArgs &a, int r, int ps_shift, int64_t &real) const
     {
-        real = __ldg(a.seq_lens + r);
-        const bool aborted = a.abort_flags != nullptr && __ldg(a.abort_flags + r) != 0;
+        real = __ldcg(a.seq_lens + r);
+        const bool aborted = a.abort_flags != nullptr && __ldcg(a.abort_flags + r) != 0;
         const int n = shown_units(a, real, aborted, ps_shift);
         return n > 0 ? n + a.pair_cost : 0;
     }

@@ -437,8 +437,8 @@ decode_mt_umma_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
                     const int64_t at =
                         ((static_cast<int64_t>(page_list[i >> bpp_shift]) * a.num_kv_heads + kvh) << bpp_shift) +
                         (i & ((1 << bpp_shift) - 1));
-                    const int ek = max(static_cast<int>(__ldg(a.k_exp + at)), -126);
-                    const int ev = max(static_cast<int>(__ldg(a.v_exp + at)), -126);
+                    const int ek = max(static_cast<int>(__ldcg(a.k_exp + at)), -126);
+                    const int ev = max(static_cast<int>(__ldcg(a.v_exp + at)), -126);
                     e = static_cast<uint16_t>((ek & 0xFF) | (min(ev, 126) << 8));
                 }
                 blk_exp[i] = e;

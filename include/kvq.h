@@ -344,7 +344,11 @@ KVQ_API kvq_status kvq_decode_attn_mt(const kvq_cache_desc *desc, const void *q,
  *                  idle.  *split_tokens and *max_splits are then upper bounds.
  *   Every other argument as in kvq_decode_attn_mt, with either cache type; the
  *   workspace size comes from kvq_decode_plan_window with the same window,
- *   num_sinks and n.
+ *   num_sinks and n.  As in every decode call the workspace's first bytes are
+ *   arrival counters that a call finds and leaves at zero; how many there are
+ *   goes by the batch, the heads and n, so a buffer that calls of different
+ *   shapes share is zeroed between them (calls that differ in lengths, window
+ *   or sinks alone need not be).
  * A query that sees no position gets zeros, as does every query of a request
  * that is aborted, empty, longer than its table row or that names a page
  * outside [0, num_pages) in an entry the call reads.  What positions outside

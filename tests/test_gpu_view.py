@@ -320,6 +320,81 @@ def test_captured_replayed_and_on_another_stream(kind, splits):
     assert torch.equal(got, out)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_refusals_with_tensors_on_the_gpu(kind):
+    """Tensors that the library cannot take as they are: not contiguous, off a
+    16-byte border, on the host, of another shape; a workspace that is too
+    small.  Nothing is launched: the output keeps what it held."""
+    c = Case(kind, [40, 20], 2, 16, 2, 16, 3)
+    ws, out = c.workspace(0), c.out(True)
+    q = c.d["q"]
+    wide = torch.zeros((*q.shape[:3], 2 * D), dtype=q.dtype, device=DEV)[..., :D]
+    shifted = torch.zeros(q.numel() + 1, dtype=q.dtype, device=DEV)[1:].view(q.shape)
+    for other, err in ((dict(q=wide), ValueError), (dict(seq=c.d["seq"].cpu()), ValueError),
+                       (dict(bt=c.d["bt"][:1]), ValueError), (dict(k=c.d["k"].cpu()), ValueError),
+                       (dict(seq=c.d["seq"].long()), TypeError), (dict(q=shifted), kvq.KvqError),
+                       (dict(q=None), TypeError), (dict(bt=c.d["bt"][0]), ValueError)):
+        with pytest.raises(err):
+            c.call(out, ws, **other)
+    with pytest.raises(kvq.KvqError) as e:
+        c.call(out, ws[:16])
+    assert e.value.status == 3
+    with pytest.raises(kvq.KvqError):
+        c.call(out, None)
+    with pytest.raises(OverflowError):
+        c.call(out, ws, splits=2**31)
+    torch.cuda.synchronize()
+    assert torch.all(out == 7.0)
+    # a stream given as a handle
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = c.call(c.out(True), ws, stream=side.cuda_stream)
+    side.synchronize()
+    ref, bound = c.ref(True)
+    R.assert_within(got.cpu().numpy().astype(np.float64), ref, bound, "handle")
+
+
+def test_two_calls_at_once_with_workspaces_of_their_own():
+    a = Case("blocks", [3000, 700, 41], 8, 16, 1, 0, 0, hkv=2, padded=True)
+    b = Case("fp8", [9000, 33], 4, 16, 4, 2000, 5)
+    wa, wb = a.workspace(0), b.workspace(12)
+    ra, ba = a.ref(True)
+    rb, bb = b.ref(True)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        oa = a.call(a.out(True), wa, 0, stream=streams[0])
+        ob = b.call(b.out(True), wb, 12, stream=streams[1])
+    torch.cuda.synchronize()
+    R.assert_within(oa.cpu().numpy().astype(np.float64), ra, ba, "first")
+    R.assert_within(ob.cpu().numpy().astype(np.float64), rb, bb, "second")
+
+
+def test_one_workspace_under_changing_lengths_windows_and_graphs():
+    """Two graphs captured over one workspace (as documented: the same batch,
+    heads and query tokens) and replayed in turn with an eager call between."""
+    c = Case("fp8", [5000, 64, 900], 4, 16, 1, 0, 0)
+    ws = torch.zeros(max(c.workspace(0).numel(), 1 << 22), dtype=torch.uint8, device=DEV)
+    outs, graphs, refs = [], [], []
+    for window, splits in ((0, 12), (700, 12), (700, 0), (0, 0)):
+        c.window = window
+        refs.append(R.attention(c.q_bits, c.k, c.v, c.bt, c.lens, SCALE, window, 0, ks=c.ks, vs=c.vs, fp32=True))
+        out = c.call(c.out(True), ws, splits)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.call(out, ws, splits)
+        outs.append(out)
+        graphs.append(g)
+    for order in ((0, 1, 2, 3), (3, 1, 0, 2)):
+        for i in order:
+            outs[i].fill_(5.0)
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            R.assert_within(outs[i].cpu().numpy().astype(np.float64), *refs[i], f"graph {i}")
+
+
 def test_wait_limit_of_the_new_builds():
     """A copy wait that gives up at once: the bit, zeros, and the next call is right."""
     for kind in KINDS:

@@ -70,6 +70,14 @@ def test_plans_refuse(plan):
         assert e.value.status == status, args
 
 
+def test_numbers_past_32_bits_are_refused():
+    for plan in (kvq.kvq_decode_plan_window, kvq.kvq_decode_plan_blocks):
+        with pytest.raises(OverflowError):
+            plan(desc(), 8, 1, 64, 513, 2**32 + 5, 0)
+        with pytest.raises(OverflowError):
+            plan(desc(), 8, 1, 64, 513, 5, 2**31)
+
+
 def test_the_block_scaled_cache_is_an_fp8_cache():
     with pytest.raises(kvq.KvqError) as e:
         kvq.kvq_decode_plan_blocks(desc(dtype=1), 8, 1, 64, 513)
