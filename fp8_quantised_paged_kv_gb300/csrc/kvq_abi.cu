@@ -221,7 +221,7 @@ int32_t visible_pages(const View &v, int32_t page_size, int32_t max_pages, int32
 constexpr int64_t kBalancedMinBytes = 256 << 20;
 bool balanced_pays(int64_t jobs, int64_t max_ctx, bool bf16)
 {
-    return jobs * max_ctx * (bf16 ? 512 : 256) >= kBalancedMinBytes;
+    return static_cast<double>(jobs) * static_cast<double>(max_ctx) * (bf16 ? 512 : 256) >= kBalancedMinBytes;
 }
 
 // Units that a border between two (request, KV head) pairs costs a CTA of a
@@ -246,6 +246,8 @@ bool plan_balanced(int64_t pairs, int64_t max_ctx, int32_t page_size, bool bf16,
     const int64_t ctas = static_cast<int64_t>(kvq::device_sm_count()) * kvq::decode_view_ctas_per_sm(bf16, multi);
     const int64_t wave = ctas * (kMaxSplitTokens / unit);
     const int64_t cost = kPairCostTokens / unit;
+    if (max_units + cost > 0x7FFFFFFF / pairs)
+        return false;
     const int64_t most = pairs * (max_units + cost);       // the longest line there can be
     if (most > 0x7FFFFFFF - wave)
         return false;

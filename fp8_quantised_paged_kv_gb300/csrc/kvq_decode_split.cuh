@@ -946,22 +946,40 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
         cp_async_commit();
     }
 
+    // Behind the first copies, in one trip: the exponents of the split's
+    // blocks, one byte each (through L2: the append that wrote them may have
+    // run on this SM beside this CTA), and in the multi-token windowed builds
+    // the query rows.
+    constexpr int kExpsPerThread = (8192 / kBlockTokens + kThreads - 1) / kThreads;
+    [[maybe_unused]] int exps[kExpsPerThread][2];
     if constexpr (kBlocks) {
-        // the exponents of the split's blocks, one byte each, behind the first
-        // copies (through L2: the append that wrote them may have run on this
-        // SM beside this CTA)
         const int n_blocks = static_cast<int>((t1 - t0 + kBlockTokens - 1) / kBlockTokens);
         const int bpp_shift = ps_shift - 4;                // blocks per page: ps / 16
-        for (int i = threadIdx.x; i < 2 * n_chunks; i += kThreads) {
-            if (i >= n_blocks) {                           // the last chunk's second m-tile holds no token
-                blk_exp[i] = 0;
-                continue;
+#pragma unroll
+        for (int k = 0; k < kExpsPerThread; ++k) {
+            const int i = threadIdx.x + k * kThreads;
+            exps[k][0] = exps[k][1] = 0;                   // the last chunk's second m-tile may hold no token
+            if (i < n_blocks) {
+                const int64_t at =
+                    ((static_cast<int64_t>(page_list[i >> bpp_shift]) * a.num_kv_heads + kvh) << bpp_shift) +
+                    (i & ((1 << bpp_shift) - 1));
+                exps[k][0] = __ldcg(a.k_exp + at);
+                exps[k][1] = __ldcg(a.v_exp + at);
             }
-            const int64_t at = ((static_cast<int64_t>(page_list[i >> bpp_shift]) * a.num_kv_heads + kvh) << bpp_shift) +
-                               (i & ((1 << bpp_shift) - 1));
-            const int ek = max(static_cast<int>(__ldcg(a.k_exp + at)), -126);
-            const int ev = max(static_cast<int>(__ldcg(a.v_exp + at)), -126);
-            blk_exp[i] = static_cast<uint16_t>((ek & 0xFF) | (min(ev, 126) << 8));
+        }
+    }
+    constexpr bool kMidQ = kWindow && kMulti;
+    if constexpr (kMidQ)
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+            load_q(nt);
+    if constexpr (kBlocks) {
+#pragma unroll
+        for (int k = 0; k < kExpsPerThread; ++k) {
+            const int i = threadIdx.x + k * kThreads;
+            if (i < 2 * n_chunks)
+                blk_exp[i] = static_cast<uint16_t>((max(exps[k][0], -126) & 0xFF) |
+                                                   (min(max(exps[k][1], -126), 126) << 8));
         }
     }
 
@@ -982,7 +1000,7 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
     for (int nt = 0; nt < kNT; ++nt) {
         q_exp[nt] = 0;
         uint32_t (&w)[16] = q_raw[nt];
-        if constexpr (!kEarlyQ)
+        if constexpr (!kEarlyQ && !kMidQ)
             load_q(nt);
         float q_mul = 1.f;
         if constexpr (!kBf16Cache) {
