@@ -109,11 +109,11 @@ constexpr int kMaxShareTokens = 8192;             // of a balanced launch's CTA
 constexpr uint32_t kLseInvalid = 0x7FC00000u;
 constexpr uint32_t kLseStale = 0x7FC0A5A5u;
 
-template <bool kBf16Cache>
+template <bool kBf16Cache, int kRingStages = 2>
 struct Tile {
     static constexpr int kRowBytes = kBf16Cache ? 256 : 128;      // one token of one head
     static constexpr int kBytes = kChunkTokens * kRowBytes;       // K (or V) part of a stage
-    static constexpr int kStages = 2;
+    static constexpr int kStages = kRingStages;
     static constexpr int kStageBytes = 2 * kBytes;
     static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
     static constexpr int kSmemBytes = 1024 /* alignment slack */ + kRingBytes +
@@ -124,24 +124,30 @@ struct Tile {
 
 // Windowed builds hold no tags and no new token; the block-scaled ones keep
 // the exponents of a split's blocks there (ek in the low byte, ev in the high
-// one), the multi-token FP8 ones the query fragments (smem_q).
+// one), the multi-token ones the query fragments (smem_q).  A bf16 cache's
+// windowed builds give a warp one stage instead of two: the ring is half as
+// large, three CTAs fit on an SM like the FP8 builds', and what one warp does
+// not overlap its eleven neighbours do.
 constexpr int kExpBytes = 2 * (8192 / kBlockTokens) + 16;
-__host__ __device__ constexpr bool smem_q(bool bf16, bool multi, bool window) { return window && multi && !bf16; }
+__host__ __device__ constexpr bool smem_q(bool multi, bool window) { return window && multi; }
+template <bool kBf16, bool kWindow>
+using BuildTile = Tile<kBf16, kBf16 && kWindow ? 1 : 2>;
 constexpr int kQFragBytes = 8 * 2 * 32 * 8;       // [k-step][n-tile][lane] two words
 template <bool kBf16, bool kMulti, bool kWindow>
 constexpr int smem_bytes()
 {
     if (!kWindow)
         return Tile<kBf16>::kSmemBytes;
-    return 1024 + Tile<kBf16>::kRingBytes + kWarps * Tile<kBf16>::kStages * 8 + kMaxPageList * 4 + kExpBytes +
-           (smem_q(kBf16, kMulti, kWindow) ? kQFragBytes : 0);
+    using T = BuildTile<kBf16, kWindow>;
+    return 1024 + T::kRingBytes + kWarps * T::kStages * 8 + kMaxPageList * 4 + kExpBytes +
+           (smem_q(kMulti, kWindow) ? kQFragBytes : 0);
 }
 // Resident CTAs per SM that the registers are compiled for.  Multi-token
-// builds: 2, with both n-tiles' query fragments in registers; the windowed FP8
+// builds: 2, with both n-tiles' query fragments in registers; the windowed
 // ones read them from shared memory, which leaves registers for 3.
-__host__ __device__ constexpr int min_ctas(bool bf16, bool multi, bool window)
+__host__ __device__ constexpr int min_ctas(bool multi, bool window)
 {
-    return multi && !smem_q(bf16, multi, window) ? 2 : kCtasPerSm;
+    return multi && !smem_q(multi, window) ? 2 : kCtasPerSm;
 }
 
 // Byte offset of 16-byte chunk `c` of 128-byte line `line` in a tile written
@@ -637,7 +643,7 @@ template <bool kBf16Cache, bool kPreciseP, bool kCluster, bool kMulti, bool kWin
 __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtensorMap &v_map, const DecodeArgs &a,
                                           const Job &job, bool first)
 {
-    using T = Tile<kBf16Cache>;
+    using T = BuildTile<kBf16Cache, kWindow>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -650,7 +656,7 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
     [[maybe_unused]] uint16_t *blk_exp = reinterpret_cast<uint16_t *>(page_list + kMaxPageList);
     [[maybe_unused]] uint2 *q_frag =
         reinterpret_cast<uint2 *>(reinterpret_cast<uint8_t *>(page_list + kMaxPageList) + kExpBytes);
-    constexpr bool kSmemQ = smem_q(kBf16Cache, kMulti, kWindow);
+    constexpr bool kSmemQ = smem_q(kMulti, kWindow);
     __shared__ int s_failed;
     __shared__ int s_stale;                                // kvq_decode_step: a page of this split failed
 
@@ -1185,7 +1191,7 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
             // ---- S^T = K Q^T for the two 16-token m-tiles; each K fragment,
             // converted once, feeds every n-tile of query rows
             float sc[kNT][2][4];
-            if constexpr (kSmemQ) {
+            if constexpr (kSmemQ && !kBf16Cache) {
                 // both m-tiles together: a fragment of Q is read once for four products
                 uint32_t kw[2][2][8];
     #pragma unroll
@@ -1238,9 +1244,14 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
     #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
     #pragma unroll
-                        for (int nt = 0; nt < kNT; ++nt)
-                            mma_bf16(sc[nt][mt], w0[2 * kk], w1[2 * kk], w0[2 * kk + 1], w1[2 * kk + 1],
-                                     qf[nt][kk][0], qf[nt][kk][1]);
+                        for (int nt = 0; nt < kNT; ++nt) {
+                            uint2 qv;
+                            if constexpr (kSmemQ)
+                                qv = q_frag[(kk * kNT + nt) * 32 + lane];
+                            else
+                                qv = make_uint2(qf[nt][kk][0], qf[nt][kk][1]);
+                            mma_bf16(sc[nt][mt], w0[2 * kk], w1[2 * kk], w0[2 * kk + 1], w1[2 * kk + 1], qv.x, qv.y);
+                        }
                 } else {
                     const uint4 x0a = lds128(ks, swz(r0, 2 * tq)), x0b = lds128(ks, swz(r0, 2 * tq + 1));
                     const uint4 x1a = lds128(ks, swz(r1, 2 * tq)), x1b = lds128(ks, swz(r1, 2 * tq + 1));
@@ -1790,7 +1801,7 @@ struct Share {
 };
 
 template <bool kBf16Cache, bool kPreciseP, bool kCluster, bool kMulti, bool kWindow, bool kBlocks>
-__global__ void __launch_bounds__(kThreads, min_ctas(kBf16Cache, kMulti, kWindow))
+__global__ void __launch_bounds__(kThreads, min_ctas(kMulti, kWindow))
 decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
                     const __grid_constant__ CUtensorMap v_map, const DecodeArgs a)
 {

@@ -22,7 +22,7 @@ int decode_view_ctas_per_sm(bool bf16_cache, bool multi)
     constexpr int kSm = 233472, kReserved = 1024;
     const int bytes = multi ? (bf16_cache ? smem_bytes<true, true, true>() : smem_bytes<false, true, true>())
                             : (bf16_cache ? smem_bytes<true, false, true>() : smem_bytes<false, false, true>());
-    const int by_smem = kSm / (bytes + kReserved), bound = min_ctas(bf16_cache, multi, true);
+    const int by_smem = kSm / (bytes + kReserved), bound = min_ctas(multi, true);
     return by_smem < bound ? by_smem : bound;
 }
 
