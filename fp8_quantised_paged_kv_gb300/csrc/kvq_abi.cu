@@ -360,6 +360,13 @@ kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads
         single_wave = want > 0;
         if (!single_wave)
             want = auto_splits(jobs, max_ctx, slots);
+        // More pairs than resident CTAs, and short contexts: a split's fixed
+        // cost is more than what a fuller last wave saves (64 x 8 requests of
+        // 100..300 tokens: 13.0 us in one split, 16.1 in two, 200..600 18.1
+        // against 20.1, 333..1,000 23.0 against 23.5, 666..2,000 40.5 against
+        // 37.0; counted for the windowed and block-scaled builds).
+        if (view != nullptr && !single_wave && max_ctx <= 1024)
+            want = 1;
     }
     if (want < 1)
         want = 1;
