@@ -170,8 +170,10 @@ int64_t single_wave_splits(int64_t pairs, int64_t max_ctx, int64_t unit, int64_t
         const double stream_us = std::pow(std::pow(total_us, 4.0) + std::pow(split_us, 4.0), 0.25);
         // a workspace combine is one CTA's work: it grows with the splits that
         // it reads (counted for the windowed and block-scaled builds: one pair
-        // of 60,000 tokens takes 24 us in 48 splits, 65 us in 313)
-        const double per_split_us = !view ? 0.0 : multi ? 0.38 : 0.16;
+        // of 60,000 tokens takes 22 us in 48 splits, 60 us in 384; 0.35 us a
+        // split puts eight of eleven such shapes within 4% of their best
+        // count, the others within 14%)
+        const double per_split_us = view ? 0.35 : 0.0;
         const double combine_us =
             splits == 1 ? 0.0 : cluster ? 2.5 : 9.0 + per_split_us * static_cast<double>(splits);
         const double est = 11.0 + stream_us + combine_us;
