@@ -220,10 +220,9 @@ int32_t visible_pages(const View &v, int32_t page_size, int32_t max_pages, int32
 // longest split loses more as the batch grows (64 x 8 x 2,049 equal tokens:
 // 48.2 us against 58.3; 16 x 8 x 1,024..16,384 tokens, 4 query tokens: 73.4
 // against 105).  The border is put at 256 MB of cache that the tables allow.
-constexpr int64_t kBalancedMinBytes = 256 << 20;
 bool balanced_pays(int64_t jobs, int64_t max_ctx, bool bf16)
 {
-    return static_cast<double>(jobs) * static_cast<double>(max_ctx) * (bf16 ? 512 : 256) >= kBalancedMinBytes;
+    return static_cast<double>(jobs) * static_cast<double>(max_ctx) * (bf16 ? 512 : 256) >= kvq::kBalancedMinBytes;
 }
 
 // Units that a border between two (request, KV head) pairs costs a CTA of a

@@ -211,21 +211,32 @@ cudaError_t read_umma_error(uint32_t *bits, bool clear);
 cudaError_t launch_decode_umma_view(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                                     cudaStream_t stream);
 cudaError_t read_umma_view_error(uint32_t *bits, bool clear);
-// A windowed or block-scaled multi-token call over an FP8 cache takes it from
-// 33 query rows per KV head (three row blocks of the mma.sync build, each of
-// which converts every tile again; up to 64 rows cost the tensor-memory kernel
-// the same) and enough work to fill its pipeline, cache bytes that the tables
-// allow times rows: 8 requests x 8 KV heads x 8,193 tokens, 40, 64 and 128
-// rows: 65, 59 and 83 us against 95, 120 and 222; 2 x 4 x 3,000 tokens: 20, 25
-// and 38 us against 11, 12 and 16; even at 2,000 tokens of 8 x 8 and 40 rows.
-constexpr int kUmmaViewMinRows = 33;
-constexpr double kUmmaViewMinWork = 2e9;
+// Where a windowed or block-scaled multi-token call over an FP8 cache takes it.
+// The mma.sync build converts every tile once per 16 rows and costs what its
+// row blocks cost; up to 64 rows cost the tensor-memory kernel the same, but
+// it has a pipeline to fill.  8 requests x 8 KV heads x 8,193 tokens, 32, 40,
+// 64 and 128 rows: 52, 53, 51 and 58 us against 53, 75, 106 and 191.
+// From 33 rows the cache bytes that the tables allow times rows decide: at
+// 0.94e9 (8 x 8 x 2,000 tokens 40 rows, 4 x 8 x 2,000 64 rows) the two are even,
+// at 0.2e9 to 0.6e9 it is 0 to 3 us behind, at 3e9 22 us against 42.  With 17
+// to 32 rows, two row blocks, it gains later (1 x 8 x 30,000 tokens, 24 rows,
+// 1.5e9: 28 us against 37) and only where the tables allow less cache than the
+// mma.sync build shares out evenly (16 x 8 x 1,000..16,000 tokens: 111 against
+// 92).
+constexpr int kUmmaViewMinRows = 17, kUmmaViewManyRows = 33;
+constexpr double kUmmaViewMinWork = 0.9e9, kUmmaViewMinWorkFew = 1.4e9;
+// (bytes from which the planner shares a call out evenly)
+constexpr int64_t kBalancedMinBytes = 256 << 20;
 inline bool use_umma_view(bool bf16_cache, int n_query, int group, int64_t batch, int64_t num_kv_heads,
                           int64_t max_tokens)
 {
-    const double rows = n_query * group;
-    return !bf16_cache && n_query > 1 && rows >= kUmmaViewMinRows &&
-           256.0 * rows * static_cast<double>(batch * num_kv_heads) * static_cast<double>(max_tokens) >= kUmmaViewMinWork;
+    const int64_t rows = static_cast<int64_t>(n_query) * group;
+    if (bf16_cache || n_query == 1 || rows < kUmmaViewMinRows)
+        return false;
+    const double bytes = 256.0 * static_cast<double>(batch * num_kv_heads) * static_cast<double>(max_tokens);
+    if (rows >= kUmmaViewManyRows)
+        return bytes * static_cast<double>(rows) >= kUmmaViewMinWork;
+    return bytes * static_cast<double>(rows) >= kUmmaViewMinWorkFew && bytes < static_cast<double>(kBalancedMinBytes);
 }
 
 // Box height (in 128-byte rows) of one bulk copy for a page size.
