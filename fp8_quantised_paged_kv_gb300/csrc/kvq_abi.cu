@@ -168,14 +168,10 @@ int64_t single_wave_splits(int64_t pairs, int64_t max_ctx, int64_t unit, int64_t
             continue;                                           // more than one wave
         const double split_us = static_cast<double>(split) * bytes_per_tok / cta_rate * 1e6;
         const double stream_us = std::pow(std::pow(total_us, 4.0) + std::pow(split_us, 4.0), 0.25);
-        // a workspace combine is one CTA's work: it grows with the splits that
-        // it reads (counted for the windowed and block-scaled builds: one pair
-        // of 60,000 tokens takes 22 us in 48 splits, 60 us in 384; 0.35 us a
-        // split puts eight of eleven such shapes within 4% of their best
-        // count, the others within 14%)
-        const double per_split_us = view ? 0.35 : 0.0;
-        const double combine_us =
-            splits == 1 ? 0.0 : cluster ? 2.5 : 9.0 + per_split_us * static_cast<double>(splits);
+        // a workspace combine is one CTA's work; the windowed and block-scaled
+        // builds', a launch of its own, grows a little with the splits
+        const double memory_us = view ? 4.5 + 0.14 * static_cast<double>(splits) : 9.0;
+        const double combine_us = splits == 1 ? 0.0 : cluster ? 2.5 : memory_us;
         const double est = 11.0 + stream_us + combine_us;
         if (est < best_us - 1e-9) {
             best_us = est;
@@ -523,6 +519,7 @@ kvq_status prepare_decode(const kvq_cache_desc *desc, const void *q, int32_t bat
     a.unit_shift = call->plan.unit_shift;
     a.min_split_units = call->plan.min_split_units;
     a.pair_cost = call->plan.pair_cost;
+    a.combine_apart = view && !call->plan.umma && !a.cluster && !a.resident_ctas && a.max_splits > 1;
     a.n_query = n_query;
     a.row_blocks = call->plan.row_blocks;
     a.window = view ? view->window : 0;

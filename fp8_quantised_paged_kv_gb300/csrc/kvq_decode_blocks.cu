@@ -7,7 +7,8 @@ namespace kvq {
 cudaError_t launch_decode_blocks(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                                  cudaStream_t stream)
 {
-    return launch_build<true, true>(a, k_map, v_map, stream);
+    const cudaError_t e = launch_build<true, true>(a, k_map, v_map, stream);
+    return e != cudaSuccess || !a.combine_apart ? e : launch_combine_rows(a, stream);
 }
 
 cudaError_t read_blocks_error(uint32_t *bits, bool clear) { return read_error_word(bits, clear); }

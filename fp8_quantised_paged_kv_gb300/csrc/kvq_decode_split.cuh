@@ -330,6 +330,8 @@ __device__ void finish_step(const DecodeArgs &a, int b, int kvh, bool stale)
 template <bool kMulti, bool kNanFlows>
 __device__ void publish_and_combine(const DecodeArgs &a, const Rows<kMulti, kNanFlows> &R, int nsplit, float *scratch)
 {
+    if (kNanFlows && a.combine_apart)                      // a grid of splits: launch_combine_rows
+        return;
     __shared__ int s_last;
     // The block barrier orders every thread's partial before thread 0's
     // release; the last split's acquire, then its barrier, orders all the

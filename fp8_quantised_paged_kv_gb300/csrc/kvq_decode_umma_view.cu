@@ -77,84 +77,6 @@ static_assert(view_smem_bytes() <= 232448, "one CTA fits an SM");
 constexpr uint32_t kTcQ = 0, kTcS = 64, kTcO = 192, kTcPlo = 320, kTcP = 448;
 constexpr float kLift = 7.f;                               // log2 of what P, the sum and O are larger by
 
-// The combine of the splits, a launch of its own behind the attention: a warp
-// per output row, a lane four dims of it and the lse of one split, a round of
-// kRound splits' partials in flight.  (By the last CTA of each pair to finish,
-// with its atomic, it took 14 us on 128 rows in 9 splits and the other SMs
-// waited.)  A NaN sum (a split with lse +inf) makes the row NaN.
-constexpr int kCombineWarps = 4;
-__global__ void __launch_bounds__(32 * kCombineWarps)
-combine_rows_kernel(const DecodeArgs a)
-{
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kCombineWarps + threadIdx.x / 32;
-    const int lane = threadIdx.x % 32;
-    const int64_t rows_per_request = static_cast<int64_t>(a.n_query) * a.num_q_heads;
-    grid_dependency_wait();
-    if (row >= a.batch * rows_per_request)
-        return;
-    const int b = static_cast<int>(row / rows_per_request);
-    const int64_t real = a.seq_lens[b];
-    const bool aborted = a.abort_flags != nullptr && a.abort_flags[b] != 0;
-    if (aborted || real <= 0 || real > static_cast<int64_t>(a.max_pages_per_seq) * a.page_size) {
-        store_row_value4(a.out, row * kHeadDim + 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f), a.out_fp32);
-        return;
-    }
-    const int64_t len = shown_context(a, real, __ffs(a.page_size) - 1).len;
-    const int nsplit = static_cast<int>((len + a.split_tokens - 1) / a.split_tokens);
-    if (nsplit == 1)
-        return;
-    constexpr int kRound = 8;
-    const float *lse = a.ws_lse + row * a.max_splits;
-    const float *part = a.ws_o + row * a.max_splits * kHeadDim + 4 * lane;
-    float w = lane < nsplit ? __ldcg(lse + lane) : -INFINITY;
-    float M = 0.f, inv = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < nsplit; s0 += kRound) {
-        float4 v[kRound];
-#pragma unroll
-        for (int k = 0; k < kRound; ++k)
-            v[k] = s0 + k < nsplit
-                       ? __ldcg(reinterpret_cast<const float4 *>(part + static_cast<int64_t>(s0 + k) * kHeadDim))
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
-        if (s0 == 0) {                                     // the largest lse, and the weights' sum
-            M = w;
-            bool bad = w != w;
-            for (int c = 32; c < nsplit; c += 32) {
-                const float y = c + lane < nsplit ? __ldcg(lse + c + lane) : -INFINITY;
-                bad |= y != y;
-                M = fmaxf(M, y);
-            }
-            bad = __any_sync(0xFFFFFFFFu, bad);
-            for (int off = 16; off > 0; off >>= 1)
-                M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
-            float sum = 0.f;
-            for (int c = 0; c < nsplit; c += 32) {
-                const float y = c == 0 ? w : c + lane < nsplit ? __ldcg(lse + c + lane) : -INFINITY;
-                sum += y == -INFINITY ? 0.f : fast_exp2(y - M);
-            }
-            for (int off = 16; off > 0; off >>= 1)
-                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-            inv = bad || sum == 0.f ? 0.f : 1.f / sum;     // NaN stays
-        }
-        if (s0 % 32 == 0) {                                // lane s: the weight of split s0 + s
-            if (s0 > 0)
-                w = s0 + lane < nsplit ? __ldcg(lse + s0 + lane) : -INFINITY;
-            w = inv == 0.f || w == -INFINITY ? 0.f : fast_exp2(w - M) * inv;
-        }
-#pragma unroll
-        for (int k = 0; k < kRound; ++k) {
-            const float wk = __shfl_sync(0xFFFFFFFFu, w, (s0 + k) & 31);
-            if (s0 + k < nsplit && wk != 0.f) {            // a split without weight may hold anything
-                acc.x += wk * v[k].x;
-                acc.y += wk * v[k].y;
-                acc.z += wk * v[k].z;
-                acc.w += wk * v[k].w;
-            }
-        }
-    }
-    store_row_value4(a.out, row * kHeadDim + 4 * lane, acc, a.out_fp32);
-}
-
 // kTpc: tokens of a tile each copy of the rows takes: 32 for up to 64 rows
 // (two copies fill the 128 M slots), 64 for 65 .. 128 rows (one copy).
 template <bool kPrecise, int kTpc, bool kBlocks>
@@ -909,22 +831,6 @@ cudaError_t launch_rows(const DecodeArgs &a, const CUtensorMap &k_map, const CUt
     return cudaGetLastError();
 }
 
-cudaError_t launch_combine(const DecodeArgs &a, cudaStream_t stream)
-{
-    const int64_t rows = static_cast<int64_t>(a.batch) * a.n_query * a.num_q_heads;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((rows + kCombineWarps - 1) / kCombineWarps));
-    cfg.blockDim = dim3(32 * kCombineWarps);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, combine_rows_kernel, a);
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 template <bool kBlocks>
 cudaError_t launch_rows_build(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                               cudaStream_t stream)
@@ -938,7 +844,7 @@ cudaError_t launch_rows_build(const DecodeArgs &a, const CUtensorMap &k_map, con
                                                  : launch_rows<false, 64, kBlocks>(a, k_map, v_map, stream)
                           : a.out_fp32 ? launch_rows<true, 32, kBlocks>(a, k_map, v_map, stream)
                                        : launch_rows<false, 32, kBlocks>(a, k_map, v_map, stream);
-    return e != cudaSuccess || a.max_splits == 1 ? e : launch_combine(a, stream);
+    return e != cudaSuccess || a.max_splits == 1 ? e : launch_combine_rows(a, stream);
 }
 
 } // namespace

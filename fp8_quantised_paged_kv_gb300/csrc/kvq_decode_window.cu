@@ -7,7 +7,8 @@ namespace kvq {
 cudaError_t launch_decode_window(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                                  cudaStream_t stream)
 {
-    return launch_build<true, false>(a, k_map, v_map, stream);
+    const cudaError_t e = launch_build<true, false>(a, k_map, v_map, stream);
+    return e != cudaSuccess || !a.combine_apart ? e : launch_combine_rows(a, stream);
 }
 
 int decode_view_cluster_capacity(int n, bool bf16_cache, bool multi)
