@@ -78,7 +78,8 @@ struct Plan {
     int32_t cluster;              // 0, or the cluster size (= max_splits) of the cluster combine
     // balanced launch (DecodeArgs); 0 resident CTAs: a grid of splits
     int32_t resident_ctas, balanced_ctas, unit_shift, min_split_units, pair_cost;
-    size_t counter_bytes, lse_bytes, o_bytes;
+    size_t counter_bytes, lse_bytes, o_bytes, pair_bytes;
+    size_t bytes() const { return counter_bytes + lse_bytes + o_bytes + pair_bytes; }
 };
 
 // Automatic split count per (request, KV head).  Large jobs use the largest
@@ -263,6 +264,7 @@ bool plan_balanced(int64_t pairs, int64_t max_ctx, int32_t page_size, bool bf16,
     const size_t rows = static_cast<size_t>(grid + pairs) * (multi ? kvq::kMultiRowsPerCta : kvq::kMaxGroup);
     p->lse_bytes = (rows * sizeof(float) + 255) / 256 * 256;
     p->o_bytes = rows * kHeadDim * sizeof(float);
+    p->pair_bytes = static_cast<size_t>(pairs) * sizeof(int2);
     return true;
 }
 
@@ -301,6 +303,7 @@ kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads
     const bool umma = view == nullptr ? kvq::use_umma(bf16, n_query, g)
                                       : kvq::use_umma_view(bf16, n_query, g, batch, d->num_kv_heads, max_ctx);
     p->umma = umma;
+    p->pair_bytes = 0;
     const int64_t min_unit = umma ? kvq::kUmmaTileTokens : kChunkTokens;
     const int64_t unit = d->page_size > min_unit ? d->page_size : min_unit;
     // CTAs per split: one per (request, KV head), or in the BF16 multi-token
@@ -484,7 +487,7 @@ kvq_status prepare_decode(const kvq_cache_desc *desc, const void *q, int32_t bat
     }
     if (batch > 65535)
         return KVQ_ERR_UNSUPPORTED;
-    const size_t need = call->plan.counter_bytes + call->plan.lse_bytes + call->plan.o_bytes;
+    const size_t need = call->plan.bytes();
     if (workspace == nullptr || workspace_bytes < need)
         return KVQ_ERR_WORKSPACE;
     if (!aligned16(workspace))
@@ -519,7 +522,14 @@ kvq_status prepare_decode(const kvq_cache_desc *desc, const void *q, int32_t bat
     a.unit_shift = call->plan.unit_shift;
     a.min_split_units = call->plan.min_split_units;
     a.pair_cost = call->plan.pair_cost;
-    a.combine_apart = view && !call->plan.umma && !a.cluster && !a.resident_ctas && a.max_splits > 1;
+    // The splits of a grid are combined by a launch of its own, and those of a
+    // balanced launch where a pair has eight of them and more (8 pairs of
+    // 140,000 tokens, two query tokens: 73 us by the last of a pair, 63 so;
+    // 128 pairs of 10..16,384: 94 against 97).
+    const int64_t apart_pairs = static_cast<int64_t>(batch) * a.num_kv_heads * call->plan.row_blocks;
+    a.combine_apart = view && !call->plan.umma && !call->plan.cluster && call->plan.max_splits > 1 &&
+                      (call->plan.resident_ctas == 0 || call->plan.resident_ctas >= 8 * apart_pairs);
+    a.ws_pairs = call->plan.pair_bytes ? reinterpret_cast<int2 *>(ws + need - call->plan.pair_bytes) : nullptr;
     a.n_query = n_query;
     a.row_blocks = call->plan.row_blocks;
     a.window = view ? view->window : 0;
@@ -738,7 +748,7 @@ kvq_status kvq_decode_plan(const kvq_cache_desc *desc, int32_t batch, int32_t nu
     if (max_splits)
         *max_splits = p.max_splits;
     if (workspace_bytes)
-        *workspace_bytes = p.counter_bytes + p.lse_bytes + p.o_bytes;
+        *workspace_bytes = p.bytes();
     return KVQ_OK;
 }
 
@@ -777,7 +787,7 @@ kvq_status kvq_decode_plan_mt(const kvq_cache_desc *desc, int32_t batch, int32_t
     if (max_splits)
         *max_splits = p.max_splits;
     if (workspace_bytes)
-        *workspace_bytes = p.counter_bytes + p.lse_bytes + p.o_bytes;
+        *workspace_bytes = p.bytes();
     return KVQ_OK;
 }
 
@@ -820,7 +830,7 @@ static kvq_status plan_view(const kvq_cache_desc *desc, int32_t batch, int32_t n
     if (max_splits)
         *max_splits = p.max_splits;
     if (workspace_bytes)
-        *workspace_bytes = p.counter_bytes + p.lse_bytes + p.o_bytes;
+        *workspace_bytes = p.bytes();
     return KVQ_OK;
 }
 

@@ -45,13 +45,25 @@ combine_rows_kernel(const DecodeArgs a)
         return;
     }
     const int64_t len = shown_context(a, real, __ffs(a.page_size) - 1).len;
-    const int nsplit = static_cast<int>((len + a.split_tokens - 1) / a.split_tokens);
-    if (nsplit == 1)
+    int nsplit = static_cast<int>((len + a.split_tokens - 1) / a.split_tokens);
+    // partial of split s: at + s * step
+    int64_t at = row * a.max_splits;
+    int step = 1;
+    if (a.resident_ctas > 0) {
+        const int per = a.n_query > 1 ? kMultiRowsPerCta : kMaxGroup;      // rows of a slot
+        const int i = static_cast<int>(row % rows_per_request) / a.num_q_heads, hq = static_cast<int>(row % a.num_q_heads);
+        const int kvh = hq / a.group, r = i * a.group + hq % a.group;
+        const int2 pair = __ldcg(a.ws_pairs + (static_cast<int64_t>(b) * a.num_kv_heads + kvh) * a.row_blocks + r / per);
+        at = static_cast<int64_t>(pair.x) * per + r % per;
+        step = per;
+        nsplit = pair.y;
+    }
+    if (nsplit == 1)                                       // written already
         return;
     constexpr int kRound = 8;
-    const float *lse = a.ws_lse + row * a.max_splits;
-    const float *part = a.ws_o + row * a.max_splits * kHeadDim + 4 * lane;
-    float w = lane < nsplit ? __ldcg(lse + lane) : -INFINITY;
+    const float *lse = a.ws_lse + at;
+    const float *part = a.ws_o + at * kHeadDim + 4 * lane;
+    float w = lane < nsplit ? __ldcg(lse + static_cast<int64_t>(lane) * step) : -INFINITY;
     float M = 0.f, inv = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s0 = 0; s0 < nsplit; s0 += kRound) {
@@ -59,13 +71,13 @@ combine_rows_kernel(const DecodeArgs a)
 #pragma unroll
         for (int k = 0; k < kRound; ++k)
             v[k] = s0 + k < nsplit
-                       ? __ldcg(reinterpret_cast<const float4 *>(part + static_cast<int64_t>(s0 + k) * kHeadDim))
+                       ? __ldcg(reinterpret_cast<const float4 *>(part + static_cast<int64_t>(s0 + k) * step * kHeadDim))
                        : make_float4(0.f, 0.f, 0.f, 0.f);
         if (s0 == 0) {                                     // the largest lse, and the weights' sum
             M = w;
             bool bad = w != w;
             for (int c = 32; c < nsplit; c += 32) {
-                const float y = c + lane < nsplit ? __ldcg(lse + c + lane) : -INFINITY;
+                const float y = c + lane < nsplit ? __ldcg(lse + static_cast<int64_t>(c + lane) * step) : -INFINITY;
                 bad |= y != y;
                 M = fmaxf(M, y);
             }
@@ -74,7 +86,7 @@ combine_rows_kernel(const DecodeArgs a)
                 M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
             float sum = 0.f;
             for (int c = 0; c < nsplit; c += 32) {
-                const float y = c == 0 ? w : c + lane < nsplit ? __ldcg(lse + c + lane) : -INFINITY;
+                const float y = c == 0 ? w : c + lane < nsplit ? __ldcg(lse + static_cast<int64_t>(c + lane) * step) : -INFINITY;
                 sum += y == -INFINITY ? 0.f : fast_exp2(y - M);
             }
             for (int off = 16; off > 0; off >>= 1)
@@ -83,7 +95,7 @@ combine_rows_kernel(const DecodeArgs a)
         }
         if (s0 % 32 == 0) {                                // lane s: the weight of split s0 + s
             if (s0 > 0)
-                w = s0 + lane < nsplit ? __ldcg(lse + s0 + lane) : -INFINITY;
+                w = s0 + lane < nsplit ? __ldcg(lse + static_cast<int64_t>(s0 + lane) * step) : -INFINITY;
             w = inv == 0.f || w == -INFINITY ? 0.f : fast_exp2(w - M) * inv;
         }
 #pragma unroll

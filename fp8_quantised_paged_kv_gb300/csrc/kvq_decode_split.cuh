@@ -330,7 +330,7 @@ __device__ void finish_step(const DecodeArgs &a, int b, int kvh, bool stale)
 template <bool kMulti, bool kNanFlows>
 __device__ void publish_and_combine(const DecodeArgs &a, const Rows<kMulti, kNanFlows> &R, int nsplit, float *scratch)
 {
-    if (kNanFlows && a.combine_apart)                      // a grid of splits: launch_combine_rows
+    if (kNanFlows && a.combine_apart)                      // launch_combine_rows does it
         return;
     __shared__ int s_last;
     // The block barrier orders every thread's partial before thread 0's
@@ -1774,6 +1774,8 @@ struct Share {
         job.span = (to - from) << a.unit_shift;
         job.base = c0 + static_cast<int64_t>(r) * lines + line;
         job.real = real;
+        if (job.split == 0)                                // for the combine
+            a.ws_pairs[static_cast<int64_t>(r) * lines + line] = make_int2(static_cast<int>(job.base), job.nsplit);
         return true;
     }
 

@@ -149,6 +149,7 @@ struct DecodeArgs {
     const int8_t *k_exp, *v_exp;     // block-scaled cache: [num_pages][Hkv][page_size / 16]
     float qk_scale_log2;             // softmax_scale * log2(e)
     uint64_t copy_wait_ns;           // a consumer's limit on one copy wait (0: give up at once)
+    int2 *ws_pairs;                  // balanced launch: each pair's first workspace slot and splits
     bool combine_apart;              // windowed builds: launch_combine_rows combines the splits
     bool out_fp32, bf16_cache;
 };
@@ -172,8 +173,7 @@ cudaError_t launch_decode_window(const DecodeArgs &a, const CUtensorMap &k_map, 
                                  cudaStream_t stream);
 cudaError_t launch_decode_blocks(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                                  cudaStream_t stream);
-// The combine as a launch of its own, behind a grid of splits whose partials
-// stand at row * max_splits + split.
+// The combine as a launch of its own.
 cudaError_t launch_combine_rows(const DecodeArgs &a, cudaStream_t stream);
 cudaError_t read_window_error(uint32_t *bits, bool clear);
 cudaError_t read_blocks_error(uint32_t *bits, bool clear);
