@@ -264,7 +264,10 @@ bool plan_balanced(int64_t pairs, int64_t max_ctx, int32_t page_size, bool bf16,
     const size_t rows = static_cast<size_t>(grid + pairs) * (multi ? kvq::kMultiRowsPerCta : kvq::kMaxGroup);
     p->lse_bytes = (rows * sizeof(float) + 255) / 256 * 256;
     p->o_bytes = rows * kHeadDim * sizeof(float);
-    p->pair_bytes = static_cast<size_t>(pairs) * sizeof(int2);
+    // Combined by a launch of its own where a pair has eight splits and more (8
+    // pairs of 140,000 tokens, two query tokens: 73 us by the last of a pair,
+    // 63 so; 128 pairs of 10..16,384: 94 against 97).
+    p->pair_bytes = ctas >= 8 * pairs ? static_cast<size_t>(pairs) * sizeof(int2) : 0;
     return true;
 }
 
@@ -522,13 +525,9 @@ kvq_status prepare_decode(const kvq_cache_desc *desc, const void *q, int32_t bat
     a.unit_shift = call->plan.unit_shift;
     a.min_split_units = call->plan.min_split_units;
     a.pair_cost = call->plan.pair_cost;
-    // The splits of a grid are combined by a launch of its own, and those of a
-    // balanced launch where a pair has eight of them and more (8 pairs of
-    // 140,000 tokens, two query tokens: 73 us by the last of a pair, 63 so;
-    // 128 pairs of 10..16,384: 94 against 97).
-    const int64_t apart_pairs = static_cast<int64_t>(batch) * a.num_kv_heads * call->plan.row_blocks;
+    // the splits of a grid are combined by a launch of its own
     a.combine_apart = view && !call->plan.umma && !call->plan.cluster && call->plan.max_splits > 1 &&
-                      (call->plan.resident_ctas == 0 || call->plan.resident_ctas >= 8 * apart_pairs);
+                      (call->plan.resident_ctas == 0 || call->plan.pair_bytes > 0);
     a.ws_pairs = call->plan.pair_bytes ? reinterpret_cast<int2 *>(ws + need - call->plan.pair_bytes) : nullptr;
     a.n_query = n_query;
     a.row_blocks = call->plan.row_blocks;

@@ -1774,7 +1774,7 @@ struct Share {
         job.span = (to - from) << a.unit_shift;
         job.base = c0 + static_cast<int64_t>(r) * lines + line;
         job.real = real;
-        if (job.split == 0)                                // for the combine
+        if (a.ws_pairs != nullptr && job.split == 0)       // for the combine
             a.ws_pairs[static_cast<int64_t>(r) * lines + line] = make_int2(static_cast<int>(job.base), job.nsplit);
         return true;
     }
