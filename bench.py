@@ -50,7 +50,7 @@ L2_FLUSH_BYTES = 512 << 20          # > 129 MB L2: written, then another read, b
 L2_FLUSH_NOTE = ("flushed before every timed step (a 512 MiB write, then a read of another "
                  "512 MiB buffer, so that no dirty line of the flush is written back inside "
                  "the timed region)")
-DECODE_SOURCES = ("kvq_decode.cu", "kvq_ptx.cuh")
+DECODE_SOURCES = ("kvq_decode.cu", "kvq_decode_split.cuh", "kvq_ptx.cuh")
 PROFILE_SUMMARIES = {                # committed ncu summaries of the decode kernel, by workload
     "tiny": os.path.join(ROOT, "profiles", "decode_split_tiny.json"),
     "uniform8": os.path.join(ROOT, "profiles", "decode_split_uniform8.json"),
@@ -62,7 +62,7 @@ W4_PROFILE_SUMMARY = os.path.join(ROOT, "profiles", "w4a16_m1.json")
 MT_PROFILE_SUMMARY = os.path.join(ROOT, "profiles", "decode_mt_uniform8_n4.json")
 # the tensor-memory kernel that takes 64 or more query rows per KV head
 UMMA_PROFILE_SUMMARY = os.path.join(ROOT, "profiles", "decode_mt_umma_uniform8_n8.json")
-UMMA_SOURCES = ("kvq_decode_umma.cu", "kvq_umma.cuh", "kvq_ptx.cuh")
+UMMA_SOURCES = ("kvq_decode_umma.cu", "kvq_decode_umma.cuh", "kvq_umma.cuh", "kvq_ptx.cuh")
 MULTI_TOKEN_CONFIGS = ("uniform8",)
 STEADY_STATE_CONFIGS = ("tiny",)
 W4_SOURCES = ("kvq_w4a16.cu", "kvq_ptx.cuh")

@@ -219,14 +219,14 @@ cudaError_t read_umma_view_error(uint32_t *bits, bool clear);
 // The mma.sync build converts every tile once per 16 rows and costs what its
 // row blocks cost; up to 64 rows cost the tensor-memory kernel the same, but
 // it has a pipeline to fill.  8 requests x 8 KV heads x 8,193 tokens, 32, 40,
-// 64 and 128 rows: 52, 53, 51 and 58 us against 53, 75, 106 and 191.
+// 64 and 128 rows: 50, 50, 52 and 58 us against 53, 75, 106 and 191.
 // From 33 rows the cache bytes that the tables allow times rows decide: at
 // 0.94e9 (8 x 8 x 2,000 tokens 40 rows, 4 x 8 x 2,000 64 rows) the two are even,
 // at 0.2e9 to 0.6e9 it is 0 to 3 us behind, at 3e9 22 us against 42.  With 17
 // to 32 rows, two row blocks, it gains later (1 x 8 x 30,000 tokens, 24 rows,
-// 1.5e9: 28 us against 37) and only where the tables allow less cache than the
-// mma.sync build shares out evenly (16 x 8 x 1,000..16,000 tokens: 111 against
-// 92).
+// 1.5e9: 26 us against 37) and only where the tables allow less cache than the
+// mma.sync build shares out evenly (16 x 8 x 1,000..16,000 tokens: 102 with 40
+// rows here, 94 with 32 there).
 constexpr int kUmmaViewMinRows = 17, kUmmaViewManyRows = 33;
 constexpr double kUmmaViewMinWork = 0.9e9, kUmmaViewMinWorkFew = 1.4e9;
 // (bytes from which the planner shares a call out evenly)

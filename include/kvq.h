@@ -356,7 +356,8 @@ KVQ_API kvq_status kvq_decode_attn_mt(const kvq_cache_desc *desc, const void *q,
  * position that a query sees reaches its output, and one in the V row of a
  * position that only some of a request's queries see may reach the others.
  * Only the visible tokens' pages are read: the time goes with min(context,
- * window + num_sinks), not with the context.
+ * window + num_sinks), not with the context.  One launch, or two where a second
+ * one joins the splits through the workspace.
  */
 KVQ_API kvq_status kvq_decode_plan_window(const kvq_cache_desc *desc, int32_t batch,
                                           int32_t num_query_tokens, int32_t num_q_heads,
