@@ -426,10 +426,10 @@ __device__ void publish_and_combine(const DecodeArgs &a, const Rows<kMulti, kNan
     // thread t: the (row, 4 dims) pairs t, t + 128, ... of the rows x 32;
     // kRound splits per round, every 16-byte load of a round issued before
     // any is used, so a round costs one trip to L2. The windowed and
-    // block-scaled builds take short rounds: this code runs once per pair and
-    // cold, and the unrolled rounds' instruction misses cost more than the
-    // trips saved (1 pair of 60,000 tokens: 4 query tokens 48 -> 33 us, single
-    // 25 -> 23 us; 2 pairs of 20,000 tokens 19.4 -> 15.0 us)
+    // block-scaled builds (balanced launches of few splits per pair) take short
+    // rounds: this code runs once per pair and cold, and the unrolled rounds'
+    // instruction misses cost more than the trips saved (48 splits by one CTA:
+    // 4 query tokens 48 -> 33 us, single 25 -> 23 us)
     constexpr int kPairs = kRowsT * (kHeadDim / 4) / kThreads;          // 2, or 4 with 16 rows
     constexpr int kRound = (kMulti ? 4 : 8) / (kNanFlows ? 4 : 1);
     static_assert(kRowsT * (kHeadDim / 4) == kPairs * kThreads, "whole (row, 4 dims) pairs per thread");

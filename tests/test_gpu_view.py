@@ -167,6 +167,40 @@ def test_tensor_memory_kernel(kind, n, g, ps, window, sinks):
     c.check(splits=(0, 1, 3, 12))
 
 
+class FewRows(Case):
+    """17 to 32 query rows per KV head, enough work and less than 256 MB of cache
+    that the tables allow: the tensor-memory kernel, which holds weights 2^7
+    times and so cuts them at 2^-32 of the largest."""
+
+    def ref(self, fp32, abort=None):
+        return R.attention(self.q_bits, self.k, self.v, self.bt, self.lens, SCALE, self.window, self.sinks,
+                           ks=self.ks, vs=self.vs, ke=self.ke, ve=self.ve, abort=abort, fp32=fp32, cut=2.0 ** -32)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "blocks"])
+@pytest.mark.parametrize("n,g,ps", [(3, 8, 16), (5, 4, 64), (16, 2, 32), (4, 8, 128)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (8000, 70)])
+def test_tensor_memory_kernel_few_rows(kind, n, g, ps, window, sinks):
+    c = FewRows(kind, TM_LENS, g, ps, n, window, sinks, hkv=8, ev=(-20, 10))
+    table = 256 * 8 * len(TM_LENS) * 9000
+    assert table * n * g * min(1, (window or 9000) / 9000) >= 1.4e9 and 1.05 * table < 256 << 20 and 17 <= n * g <= 32
+    abort = (np.arange(len(TM_LENS)) == 5).astype(np.uint8)
+    c.check(splits=(0, 1, 7), abort=abort)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [1, 2])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (2**30, 3)])
+def test_one_long_request_shared_on_the_device(kind, n, window, sinks):
+    """Over a hundred splits of a pair in a launch that shares its work out, joined
+    by a launch behind it; the other requests fit one split, show nothing or
+    name a page that is not there."""
+    c = Case(kind, (70001, 0, 33, 1, 200), 5, 64, n, window, sinks, padded=True, hkv=1)
+    c.bt[4, 1] = c.desc.num_pages
+    c.d["bt"] = torch.from_numpy(c.bt).to(DEV)
+    c.check(splits=(0,))
+
+
 @pytest.mark.parametrize("kind", ["fp8", "blocks"])
 def test_tensor_memory_kernel_edges(kind):
     """Scores that rise along the context (the stale maximum is raised tile after
