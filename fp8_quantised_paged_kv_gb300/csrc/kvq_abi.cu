@@ -228,8 +228,8 @@ bool balanced_pays(int64_t jobs, int64_t max_ctx, bool bf16)
 constexpr int64_t kPairCostTokens = 384;
 
 // A balanced launch: shares of at most 8,192 tokens, as many resident CTAs as
-// the GPU holds, and a workspace slot for every (CTA, pair) that can meet.
-// False where its numbering or the combine's limits do not fit.
+// the GPU holds, and a workspace slot for every (CTA, pair) that can meet
+// behind the counters that make_plan placed.  False where its numbering or the combine's limits do not fit.
 bool plan_balanced(int64_t pairs, int64_t max_ctx, int32_t page_size, bool bf16, bool multi, Plan *p)
 {
     const int64_t unit = page_size > 64 ? page_size : 64;
@@ -260,7 +260,6 @@ bool plan_balanced(int64_t pairs, int64_t max_ctx, int32_t page_size, bool bf16,
     const int64_t splits = (max_units + min_units - 1) / min_units + 1;
     p->max_splits = static_cast<int32_t>(splits < grid ? splits : grid);
     p->cluster = 0;
-    p->counter_bytes = (static_cast<size_t>(pairs) * 4 + 255) / 256 * 256;
     const size_t rows = static_cast<size_t>(grid + pairs) * (multi ? kvq::kMultiRowsPerCta : kvq::kMaxGroup);
     p->lse_bytes = (rows * sizeof(float) + 255) / 256 * 256;
     p->o_bytes = rows * kHeadDim * sizeof(float);
@@ -309,13 +308,21 @@ kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads
     p->pair_bytes = 0;
     const int64_t min_unit = umma ? kvq::kUmmaTileTokens : kChunkTokens;
     const int64_t unit = d->page_size > min_unit ? d->page_size : min_unit;
-    // CTAs per split: one per (request, KV head), or in the BF16 multi-token
-    // build one per (request, KV head, block of 16 query rows)
-    const int64_t row_blocks = multi && !umma
-                                   ? (static_cast<int64_t>(n_query) * g + kvq::kMultiRowsPerCta - 1) /
-                                         kvq::kMultiRowsPerCta
-                                   : 1;
-    const int64_t pairs = static_cast<int64_t>(batch) * d->num_kv_heads * row_blocks;
+    // CTAs per split: one per (request, KV head), or in the mma.sync
+    // multi-token builds one per (request, KV head, block of 16 query rows)
+    const int64_t all_blocks = multi ? (static_cast<int64_t>(n_query) * g + kvq::kMultiRowsPerCta - 1) /
+                                           kvq::kMultiRowsPerCta
+                                     : 1;
+    const int64_t row_blocks = umma ? 1 : all_blocks;
+    const int64_t jobs_of_batch = static_cast<int64_t>(batch) * d->num_kv_heads;
+    const int64_t pairs = jobs_of_batch * row_blocks;
+    // Arrival counters.  Windowed and block-scaled calls that differ in window,
+    // sinks or table width share a workspace without zeroing it in between,
+    // and those decide which kernel runs: so their counters take the same
+    // place whichever it is, one per (request, KV head, block of 16 query rows).
+    p->counter_bytes = (static_cast<size_t>(view ? jobs_of_batch * all_blocks : pairs) * 4 + 255) / 256 * 256;
+    if (p->counter_bytes == 0)
+        p->counter_bytes = 256;
     p->row_blocks = static_cast<int32_t>(row_blocks);
     p->resident_ctas = p->balanced_ctas = p->unit_shift = p->min_split_units = p->pair_cost = 0;
     if (static_cast<int64_t>(d->num_kv_heads) * row_blocks > 65535)
@@ -399,9 +406,6 @@ kvq_status make_plan(const kvq_cache_desc *d, int32_t batch, int32_t num_q_heads
     if (!umma && splits >= 2 && batch > 0 &&
         pairs <= cluster_capacity(static_cast<int>(splits), bf16, multi, view != nullptr))
         p->cluster = static_cast<int32_t>(splits);
-    p->counter_bytes = (static_cast<size_t>(pairs) * 4 + 255) / 256 * 256;
-    if (p->counter_bytes == 0)
-        p->counter_bytes = 256;
     if (splits > 1 && p->cluster == 0) {
         const size_t n = static_cast<size_t>(batch) * n_query * num_q_heads * splits;
         p->lse_bytes = (n * sizeof(float) + 255) / 256 * 256;

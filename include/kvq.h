@@ -218,8 +218,9 @@ KVQ_API kvq_status kvq_quantize_pages(const kvq_cache_desc *src_desc, const void
  *   *max_splits    OUT: splits of the longest possible request,
  *                  ceil(max_pages_per_seq * page_size / *split_tokens).
  *   *workspace_bytes OUT: bytes of workspace kvq_decode_attn needs: the
- *                  arrival counters (4 bytes per request and KV head, padded
- *                  to 256) plus, when a request can span more than one split
+ *                  arrival counters (4 bytes per request and KV head -- with
+ *                  several query tokens per block of 16 query rows of one,
+ *                  see those calls --, padded to 256) plus, when a request can span more than one split
  *                  and the splits merge through the workspace, the per-split
  *                  partial results.
  * Any OUT pointer may be NULL.
@@ -294,7 +295,9 @@ KVQ_API kvq_status kvq_decode_attn(const kvq_cache_desc *desc, const void *q, in
  *   num_query_tokens  n, 1 to 16 (KVQ_ERR_UNSUPPORTED above); n = 1 is
  *                  kvq_decode_attn.
  *   Every other argument as in kvq_decode_plan / kvq_decode_attn; the
- *   workspace size comes from kvq_decode_plan_mt with the same n.
+ *   workspace size comes from kvq_decode_plan_mt with the same n.  The arrival
+ *   counters at its start: one per (request, KV head, block of 16 query rows),
+ *   with an FP8 cache and n * g >= 64 one per (request, KV head).
  * One launch.  With an FP8 cache and n * g >= 64 query rows (token, head) per
  * KV head, one CTA per (split, request, KV head) serves every row on the
  * 5th-generation tensor cores (tcgen05: Q, P and the accumulators in tensor
@@ -345,10 +348,13 @@ KVQ_API kvq_status kvq_decode_attn_mt(const kvq_cache_desc *desc, const void *q,
  *   Every other argument as in kvq_decode_attn_mt, with either cache type; the
  *   workspace size comes from kvq_decode_plan_window with the same window,
  *   num_sinks and n.  As in every decode call the workspace's first bytes are
- *   arrival counters that a call finds and leaves at zero; how many there are
- *   goes by the batch, the heads and n, so a buffer that calls of different
- *   shapes share is zeroed between them (calls that differ in lengths, window
- *   or sinks alone need not be).
+ *   arrival counters that a call finds and leaves at zero: here one uint32 per
+ *   (request, KV head, block of 16 of the n * g query rows; one block if n is
+ *   1), padded to 256 bytes, whatever the window, the sinks, the table's width,
+ *   the lengths and num_splits are.  So calls of kvq_decode_attn_window and
+ *   kvq_decode_attn_blocks that differ in those alone may share a buffer (large
+ *   enough for each) one after another as it is; a buffer that calls of other
+ *   batches, heads or n, or the other decode calls, used is zeroed before.
  * A query that sees no position gets zeros, as does every query of a request
  * that is aborted, empty, longer than its table row or that names a page
  * outside [0, num_pages) in an entry the call reads.  What positions outside
