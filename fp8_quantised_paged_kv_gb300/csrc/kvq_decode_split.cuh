@@ -47,7 +47,8 @@
 // in fp32) is the softmax's denominator in the same unit, so out = O / l and
 // the split's log-sum-exp is M + log2 l: one exponential per score, no pass
 // over the accumulators for the block's scale, and nothing overflows f16
-// whatever the blocks' scales are.
+// whatever the blocks' scales are.  What bounds the exponents that are read as
+// they are is l (kReadValueExpMin).
 #pragma once
 
 #include <cfloat>
@@ -990,8 +991,9 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
         for (int k = 0; k < kExpsPerThread; ++k) {
             const int i = threadIdx.x + k * kThreads;
             if (i < 2 * n_chunks)
-                blk_exp[i] = static_cast<uint16_t>((max(exps[k][0], -126) & 0xFF) |
-                                                   (min(max(exps[k][1], -126), 126) << 8));
+                blk_exp[i] = static_cast<uint16_t>(
+                    (max(exps[k][0], kReadKeyExpMin) & 0xFF) |
+                    (min(max(exps[k][1], kReadValueExpMin), kReadValueExpMax) << 8));
         }
     }
 

@@ -248,9 +248,9 @@ decode_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     const int64_t at =
                         ((static_cast<int64_t>(page_list[i >> bpp_shift]) * a.num_kv_heads + kvh) << bpp_shift) +
                         (i & ((1 << bpp_shift) - 1));
-                    const int ek = max(static_cast<int>(__ldcg(a.k_exp + at)), -126);
-                    const int ev = max(static_cast<int>(__ldcg(a.v_exp + at)), -126);
-                    e = static_cast<uint16_t>((ek & 0xFF) | (min(ev, 126) << 8));
+                    const int ek = max(static_cast<int>(__ldcg(a.k_exp + at)), kReadKeyExpMin);
+                    const int ev = max(static_cast<int>(__ldcg(a.v_exp + at)), kReadValueExpMin);
+                    e = static_cast<uint16_t>((ek & 0xFF) | (min(ev, kReadValueExpMax) << 8));
                 }
                 blk_exp[i] = e;
             }

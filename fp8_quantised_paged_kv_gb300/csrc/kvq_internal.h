@@ -13,6 +13,13 @@ constexpr int kHeadDim = 128;
 constexpr int kChunkTokens = 32;     // tokens one warp consumes per pipeline stage
 constexpr int kBlockTokens = 16;     // tokens of one KV head that share an exponent (block-scaled cache)
 constexpr int kBlockExpMin = -48, kBlockExpMax = 48;   // exponents the append makes
+// Exponents that the attention reads as they are (others as the nearer border).
+// K's: 2^ek is a normal fp32 number.  V's are those that the append makes: the
+// softmax's denominator is the sum of weights w = 2^(s + ev - M), held 2^15 times
+// larger, times 2^-ev.  Exponents more than 96 apart would flush weights of
+// 2^-45 of the largest and more to zero before 2^-ev brought them back, and 8,192
+// of them at 2^-ev = 2^100 would overflow.
+constexpr int kReadKeyExpMin = -126, kReadValueExpMin = kBlockExpMin, kReadValueExpMax = kBlockExpMax;
 constexpr int kMaxGroup = 8;         // query heads per KV head on one mma n-tile
 constexpr int kMaxCluster = 8;       // splits merged inside one thread-block cluster
 constexpr int kMaxSplitsTotal = 1024;  // splits of one (request, KV head)

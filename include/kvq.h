@@ -422,7 +422,9 @@ KVQ_API kvq_status kvq_tag_check_window(const int32_t *block_table, const uint32
  *          max(exp, need) with exp the block's stored exponent;
  *   the rows of the block's earlier positions become e4m3(c * 2^(exp - e))
  *   where e > exp; the new rows are e4m3(x * 2^-e), rounded to nearest even and
- *   saturating at +-448 (a NaN stays NaN); exp becomes e.
+ *   saturating at +-448 (a NaN stays NaN); exp becomes e.  (A stored exponent
+ *   above 48, which no call of this one leaves, stays as large, but the
+ *   attention reads V's as 48: see kvq_decode_attn_blocks.)
  * Rows behind the request's last position are left as they were.  A request
  * is skipped if it is longer than its table row, has fewer positions than new
  * tokens, or has offsets outside [0, num_tokens] or descending; a block is
@@ -444,9 +446,10 @@ KVQ_API kvq_status kvq_append_blocks(const kvq_cache_desc *desc, const void *k_n
  *   p_j = exp(s_j - max s),
  * over the positions j that the query sees, ek(j) and ev(j) the exponents of
  * position j's block.
- *   k_exp, v_exp   int8 [num_pages][Hkv][page_size / 16].  Exponents of
- *                  [-48, 48] (what kvq_append_blocks makes) keep the stated
- *                  accuracy; others are read as they are, down to -126.
+ *   k_exp, v_exp   int8 [num_pages][Hkv][page_size / 16].  V's exponents are read as
+ *                  they are within [-48, 48], which is what kvq_append_blocks
+ *                  makes, others as the nearer of the two; K's from -126 on,
+ *                  lower ones as -126.
  *   Every other argument, the window, the sinks and the plan as in
  *   kvq_decode_attn_window, with KVQ_CACHE_FP8_E4M3 only.
  */
