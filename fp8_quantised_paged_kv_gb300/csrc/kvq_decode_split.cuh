@@ -1116,11 +1116,13 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
     if constexpr (kBlocks || kSmemQ)
         __syncthreads();                                   // the exponents and fragments are in place
 
-    // The windowed and block-scaled builds keep weights, sums and accumulators
-    // 2^15 times larger (the quotient is the same, and f16 ends at 65504): an
-    // f16 weight, and with it the second term of the precise form, is then cut
-    // at 2^-39 of the largest weight instead of 2^-24.
-    constexpr float kLift = kWindow ? 15.f : 0.f;
+    // The windowed and block-scaled builds over FP8 keep weights, sums and
+    // accumulators 2^15 times larger (the quotient is the same, and f16 ends at
+    // 65504): an f16 weight, and with it the second term of the precise form,
+    // is then cut at 2^-39 of the largest weight instead of 2^-24.  A bf16
+    // cache's weights are bf16 terms, whose range needs no lift, and its values
+    // (up to 2^128) leave no room for one.
+    constexpr float kLift = kWindow && !kBf16Cache ? 15.f : 0.f;
     // 16-bit terms of a weight in the PV product: one for bf16 output (f16
     // 2^-12, for a bf16 cache bf16 2^-9: an output of many tokens averages
     // them below its own 2^-9; a second bf16 term cost 2 to 10 %), for fp32
