@@ -26,7 +26,7 @@ import ctypes
 import dataclasses
 import os
 
-from .build import LIB, NATIVE, build
+from .build import LIB, build, build_native, native_path
 
 KVQ_CACHE_FP8_E4M3 = 0
 KVQ_CACHE_BF16 = 1
@@ -108,7 +108,7 @@ def load(path: str | None = None):
         return _lib
     path = path or LIB
     if not os.path.exists(path):
-        build()
+        build(native=False)
     lib = ctypes.CDLL(path)
     T = {"p": ctypes.c_void_p, "i32": ctypes.c_int32, "f32": ctypes.c_float,
          "size": ctypes.c_size_t, "desc": ctypes.POINTER(_Desc), "i64": ctypes.c_int64}
@@ -378,15 +378,17 @@ _NATIVE_CALLS = ("kvq_decode_attn_window", "kvq_decode_attn_blocks", "kvq_tag_ch
 
 
 def _load_native():
-    """The native marshalling (built beside the library), bound to the loaded library."""
+    """The native marshalling (built beside the library for the installed torch),
+    bound to the loaded library."""
     global _native
     import importlib.util
 
     import torch  # noqa: F401  (its libraries, which the extension uses)
     lib = load()
-    if not os.path.exists(NATIVE):
-        build()
-    spec = importlib.util.spec_from_file_location("_kvq_native", NATIVE)
+    native = native_path()
+    if not os.path.exists(native):
+        build_native()
+    spec = importlib.util.spec_from_file_location("_kvq_native", native)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
     mod.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NATIVE_CALLS])
