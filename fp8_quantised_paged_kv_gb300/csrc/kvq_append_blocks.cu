@@ -29,7 +29,9 @@
 // Work items are numbered by offset / (16 x blocks per item) + 2 * request,
 // which leaves each request room for the blocks that its new tokens can touch
 // (n new tokens touch at most (n + 14) / 16 + 1) without a prefix sum; a CTA
-// finds its request by testing 256 requests at a time.  An item is one block,
+// finds its request by testing 256 requests at a time.  (Offsets that descend
+// break the numbering: blocks are then passed over, but each item still works
+// by its request's own offsets.)  An item is one block,
 // or with one or two KV heads as many as fill the CTA's eight warps (64,390
 // tokens of one head: 11.0 us against 16.2).
 #include "kvq_rowops.cuh"

@@ -406,8 +406,9 @@ KVQ_API kvq_status kvq_tag_check_window(const int32_t *block_table, const uint32
  *   k_new, v_new   bf16 [num_tokens][Hkv][D], the requests' tokens one request
  *                  after another.
  *   token_offsets  int32 [batch + 1]: request r's new tokens are rows
- *                  token_offsets[r] .. token_offsets[r + 1] - 1 (ascending;
- *                  none is allowed).  NULL: num_tokens / batch tokens each
+ *                  token_offsets[r] .. token_offsets[r + 1] - 1.  Offsets must
+ *                  not descend (equal ones, a request without tokens, are
+ *                  fine).  NULL: num_tokens / batch tokens each
  *                  (KVQ_ERR_INVALID_ARG unless that is a whole number).
  *   block_table, max_pages_per_seq   as in kvq_tag_check.
  *   seq_lens       int32 [batch], the request's length with its n new tokens:
@@ -427,8 +428,11 @@ KVQ_API kvq_status kvq_tag_check_window(const int32_t *block_table, const uint32
  *   attention reads V's as 48: see kvq_decode_attn_blocks.)
  * Rows behind the request's last position are left as they were.  A request
  * is skipped if it is longer than its table row, has fewer positions than new
- * tokens, or has offsets outside [0, num_tokens] or descending; a block is
- * skipped if its page id is outside [0, num_pages).  A block may be rewritten
+ * tokens, or has offsets outside [0, num_tokens]; a block is skipped if its
+ * page id is outside [0, num_pages).  Where offsets descend all the same, the
+ * request concerned is skipped and blocks of any other request may be, too (a
+ * block is found by its place in the ascending offsets); nothing is written
+ * that the requests' own offsets do not say.  A block may be rewritten
  * whole, so two requests must not append into a page they share: give one of
  * them a copy first (kvq_copy_pages).
  */
