@@ -195,6 +195,11 @@ __device__ __forceinline__ float warp_sum_over_rows(float v)
     return v;
 }
 
+__device__ __forceinline__ void mbar_inval(uint64_t *bar)
+{
+    asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 __device__ __forceinline__ void store_out(void *out, int64_t idx, float v, bool fp32)
 {
     if (fp32)
