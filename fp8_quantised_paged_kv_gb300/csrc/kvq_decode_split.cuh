@@ -1,6 +1,7 @@
 // kvq_decode_split.cuh -- paged decode attention over an FP8 e4m3 (or BF16) KV
 // cache, split along the context, with the log-sum-exp combine of the splits
-// fused into the same launch.  Compiled three times: kvq_decode.cu (per-head
+// fused into the same launch (the builds without a window always, the others
+// where that is faster).  Compiled three times: kvq_decode.cu (per-head
 // scales, every token), kvq_decode_window.cu (the same caches behind a sliding
 // window with sinks) and kvq_decode_blocks.cu (the block-scaled cache).
 //
@@ -23,12 +24,15 @@
 // online softmax, and O^T += V^T P^T.  e4m3 codes become f16 in registers
 // (exact); movmatrix turns the score fragment into the PV operand.  The four
 // warps merge in shared memory.  A request that fits in one split gets its
-// output here.  Otherwise the splits merge (the combine) in one of two forms:
+// output here.  Otherwise the splits merge (the combine) in one of three forms:
 // when every (request, KV head)'s splits can be resident at once as one
 // thread-block cluster, through distributed shared memory after a cluster
-// barrier; else each split publishes (lse, o) to the workspace and the last
-// split of the (request, KV head) to finish merges them all, counted by a
-// per-(request, KV head) arrival counter that it resets to zero.
+// barrier; else each split publishes (lse, o) to the workspace, and either the
+// last split of the (request, KV head) to finish merges them all, counted by
+// an arrival counter that it resets to zero (every build without a window, and
+// balanced launches with fewer than eight resident CTAs per pair), or a second
+// launch does (kvq_combine_rows.cu: every grid of splits of the windowed and
+// block-scaled builds, and the other balanced launches).
 //
 // Window (kWindow): the query at position p sees the positions j <= p with
 // j < num_sinks or j > p - window.  The kernel walks a shortened context: the
@@ -247,8 +251,9 @@ struct Rows {
         return id(a, r) * a.max_splits + s;
     }
 
-    // Distance of a row's partials of consecutive splits (kSlots).
-    __device__ __forceinline__ int64_t part_step() const { return base >= 0 ? rows_per_cta(kMulti) : 1; }
+    // Distance of a row's partials of consecutive splits (kSlots, where splits
+    // merge by arrival: a balanced launch).
+    __device__ __forceinline__ int64_t part_step() const { return rows_per_cta(kMulti); }
 
     __device__ __forceinline__ int64_t out_row(const DecodeArgs &a, int r) const
     {

@@ -55,6 +55,7 @@ constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;                               // issues S = Q K^T
 constexpr int kPvWarp = 10;                               // issues O += P V
 constexpr int kUThreads = 352;
+constexpr int kCombineTable = 8192;                       // (row, split) weights the combine keeps in shared memory
 constexpr int kStageBytes = 2 * kTile * 128;              // K then V rows of one tile
 constexpr int kOffRing = 0;
 constexpr int kOffKV = kOffRing + kStages * kStageBytes;  // operand buffers: K f16 [64 tok][64 d] x 2, V alike

@@ -26,7 +26,6 @@ constexpr int kMergeStride = 132;                         // floats per row of t
 constexpr int kMaxPageList = 8192 / 16 + 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRaiseThreshold = 8.f;
-constexpr int kCombineTable = 8192;                       // (row, split) weights the combine keeps in shared memory
 
 constexpr uint32_t kIdescS = umma_idesc_f16(128, kTile, false);
 constexpr uint32_t kIdescPV = umma_idesc_f16(128, 128, true);

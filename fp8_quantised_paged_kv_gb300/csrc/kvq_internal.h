@@ -120,10 +120,18 @@ cudaError_t read_w4_error(uint32_t *bits, bool clear);
 //   [0, counter_bytes)       uint32 arrivals[B][Hkv][row_blocks]: splits of each
 //                            (request, KV head, row block) that have published;
 //                            zero before the first call, and every call leaves
-//                            them zero
-//   [counter_bytes, +lse)    fp32 lse[B][n_query][Hq][S]  (log2 domain, NaN =
-//                            invalid split, -inf = a split that saw no token)
-//   [.., +o)                 fp32 o[B][n_query][Hq][S][D]  (each split's normalised output)
+//                            them zero.  A windowed or block-scaled call's
+//                            counter_bytes holds ceil(n_query * g / 16) per
+//                            (request, KV head) whichever kernel runs.
+//   [counter_bytes, +lse)    fp32 lse (log2 domain, NaN = invalid split, -inf = a
+//                            split that saw no token, +inf = one with a NaN):
+//                            a grid of S splits [B][n_query][Hq][S]; a balanced
+//                            launch [slots][8, or 16 with several query tokens]
+//                            with a slot for each (CTA, pair) that can meet
+//   [.., +o)                 fp32 o, each split's normalised output: the same
+//                            places, D numbers each
+//   [.., +pairs)             int2 (first slot, splits) of each pair: balanced
+//                            launches that a second launch combines
 struct DecodeArgs {
     const void *q;                   // bf16 [B][Hq][D]
     const float *k_scale, *v_scale;  // [Hkv] (unused for bf16 cache)
@@ -144,7 +152,8 @@ struct DecodeArgs {
     const uint32_t *page_tags;       // [num_pages] and the flags written, [B]; else null and
     uint8_t *abort_out;              // abort_flags (if any) is read instead
     int32_t n_query;                 // new query tokens per request (q, out: [B][n_query][Hq][D])
-    int32_t row_blocks;              // CTAs per (split, request, KV head): ceil(n_query * g / 8)
+    int32_t row_blocks;              // CTAs per (split, request, KV head): ceil(n_query * g / 16), or 1
+                                     // with one query token or in the tensor-memory kernels
     int32_t window, num_sinks;       // windowed builds: last positions a query sees (0: all) and
                                      // first positions that stay visible
     int32_t resident_ctas;           // balanced launch: CTAs that share the batch's units evenly; 0:
@@ -168,7 +177,7 @@ constexpr uint64_t kCopyWaitLimitNs = 1000000000ull;
 // unless the diagnostics entry point changed it.
 uint64_t decode_copy_wait_ns();
 
-// Split kernel with the combine fused into its epilogue.  The tensor maps
+// Split kernel, the combine fused into its epilogue but for combine_apart.  The tensor maps
 // describe the K and V caches as 2-D [rows][128 bytes] tensors with 128-byte
 // swizzle.
 cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
