@@ -3,7 +3,7 @@
 //
 // These calls take up to sixteen tensors and run for a few microseconds on the
 // GPU when a batch is small; checked tensor by tensor in Python they cost 15
-// to 90 us on the host, here 3 to 8 us (Grace).  The
+// to 90 us on the host, here 2.6 to 5.6 us (Grace).  The
 // checks are those of the Python binding: type, shape, contiguity, and every
 // tensor on one device, which the launch is made on whatever the current one
 // is.  Each function takes the tensors of the Python wrapper of its name and

@@ -5,8 +5,8 @@
 // copies up to 16 KB of one page of one cache: 128 threads with eight 16-byte
 // loads in flight each before the first store, so the SM's loads cover HBM's
 // latency without shared memory.  (On 8,002 pages of 64 KB this form takes
-// 157 us, 6.67 TB/s read and written, as a plain device copy of the same bytes
-// does, 155 us; bulk copies through a shared-memory ring 159 to 197 us, one
+// 153 to 154 us, 6.83 TB/s read and written, as a plain device copy of the same
+// bytes does, 152 us; bulk copies through a shared-memory ring 159 to 197 us, one
 // 16-byte load per thread 190 to 202 us.)  The exponents' pages (a few bytes) go by
 // words of the largest size that divides them and their array's address.
 #include "kvq_ptx.cuh"

@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kTagThreads) tag_check_kernel(TagCheckArgs a)
 // pages may have been given back).  The visible entries are numbered in one
 // run, so a pass takes 2,048 of them whatever the hole; unlike the check of
 // every entry it needs the length before its first table load (three rounds
-// of dependent loads).
+// of dependent loads, and two more for each further pass).
 constexpr int kWindowUnroll = 4;
 __global__ void __launch_bounds__(kTagThreads) tag_check_window_kernel(const TagWindowArgs w)
 {
