@@ -50,7 +50,7 @@ L2_FLUSH_BYTES = 512 << 20          # > 129 MB L2: written, then another read, b
 L2_FLUSH_NOTE = ("flushed before every timed step (a 512 MiB write, then a read of another "
                  "512 MiB buffer, so that no dirty line of the flush is written back inside "
                  "the timed region)")
-DECODE_SOURCES = ("kvq_decode.cu", "kvq_decode_split.cuh", "kvq_ptx.cuh")
+DECODE_SOURCES = ("kvq_decode.cu", "kvq_decode_split.cuh", "kvq_decode_split_body.cuh", "kvq_ptx.cuh")
 PROFILE_SUMMARIES = {                # committed ncu summaries of the decode kernel, by workload
     "tiny": os.path.join(ROOT, "profiles", "decode_split_tiny.json"),
     "uniform8": os.path.join(ROOT, "profiles", "decode_split_uniform8.json"),

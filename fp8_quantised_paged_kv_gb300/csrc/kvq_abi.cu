@@ -76,7 +76,7 @@ struct Plan {
     int32_t split_tokens, max_splits, row_blocks;
     bool umma;                    // the tensor-memory kernel
     int32_t cluster;              // 0, or the cluster size (= max_splits) of the cluster combine
-    // balanced launch (DecodeArgs); 0 resident CTAs: a grid of splits
+    // balanced launch (ViewArgs); 0 resident CTAs: a grid of splits
     int32_t resident_ctas, balanced_ctas, unit_shift, min_split_units, pair_cost;
     size_t counter_bytes, lse_bytes, o_bytes, pair_bytes;
     size_t bytes() const { return counter_bytes + lse_bytes + o_bytes + pair_bytes; }
@@ -462,7 +462,7 @@ bool make_cache_map(CUtensorMap *map, const kvq_cache_desc *d, const void *cache
 kvq_status to_status(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
 
 struct DecodeCall {
-    kvq::DecodeArgs args;
+    kvq::ViewArgs args;              // the builds without a view take its DecodeArgs
     Plan plan;
 };
 
@@ -499,8 +499,8 @@ kvq_status prepare_decode(const kvq_cache_desc *desc, const void *q, int32_t bat
         return KVQ_ERR_WORKSPACE;
     if (!aligned16(workspace))
         return KVQ_ERR_INVALID_ARG;
-    kvq::DecodeArgs &a = call->args;
-    a = kvq::DecodeArgs{};
+    kvq::ViewArgs &a = call->args;
+    a = kvq::ViewArgs{};
     a.q = q;
     a.k_scale = k_scale;
     a.v_scale = v_scale;

@@ -29,7 +29,7 @@ __device__ __forceinline__ void store_row4(void *out, int64_t idx, float4 v, boo
 // 32.3, 21.3).  A NaN sum (a split with lse +inf) makes the row NaN.
 constexpr int kCombineWarps = 4;
 __global__ void __launch_bounds__(32 * kCombineWarps)
-combine_rows_kernel(const DecodeArgs a)
+combine_rows_kernel(const ViewArgs a)
 {
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kCombineWarps + threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
@@ -114,7 +114,7 @@ combine_rows_kernel(const DecodeArgs a)
 
 } // namespace
 
-cudaError_t launch_combine_rows(const DecodeArgs &a, cudaStream_t stream)
+cudaError_t launch_combine_rows(const ViewArgs &a, cudaStream_t stream)
 {
     const int64_t rows = static_cast<int64_t>(a.batch) * a.n_query * a.num_q_heads;
     cudaLaunchConfig_t cfg = {};

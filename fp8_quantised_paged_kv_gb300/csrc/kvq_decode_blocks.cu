@@ -4,7 +4,7 @@
 
 namespace kvq {
 
-cudaError_t launch_decode_blocks(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+cudaError_t launch_decode_blocks(const ViewArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                                  cudaStream_t stream)
 {
     const cudaError_t e = launch_build<true, true>(a, k_map, v_map, stream);

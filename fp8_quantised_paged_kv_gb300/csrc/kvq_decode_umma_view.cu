@@ -82,7 +82,7 @@ constexpr float kLift = 7.f;                               // log2 of what P, th
 template <bool kPrecise, int kTpc, bool kBlocks>
 __global__ void __launch_bounds__(Jobs<kPrecise>::kThreads, 1)
 decode_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                   const DecodeArgs a)
+                   const ViewArgs a)
 {
     using J = Jobs<kPrecise>;
     constexpr int kThreads = J::kThreads, kKV = J::kOperands, kGroups = J::kGroups;
@@ -808,7 +808,7 @@ cudaError_t configure_rows(int dev)
 }
 
 template <bool kPrecise, int kTpc, bool kBlocks>
-cudaError_t launch_rows(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+cudaError_t launch_rows(const ViewArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                         cudaStream_t stream)
 {
     int dev = 0;
@@ -836,7 +836,7 @@ cudaError_t launch_rows(const DecodeArgs &a, const CUtensorMap &k_map, const CUt
 }
 
 template <bool kBlocks>
-cudaError_t launch_rows_build(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+cudaError_t launch_rows_build(const ViewArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                               cudaStream_t stream)
 {
     if (a.batch == 0)
@@ -853,7 +853,7 @@ cudaError_t launch_rows_build(const DecodeArgs &a, const CUtensorMap &k_map, con
 
 } // namespace
 
-cudaError_t launch_decode_umma_view(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+cudaError_t launch_decode_umma_view(const ViewArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                                     cudaStream_t stream)
 {
     return a.k_exp != nullptr ? launch_rows_build<true>(a, k_map, v_map, stream)

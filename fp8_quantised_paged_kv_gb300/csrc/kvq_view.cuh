@@ -12,7 +12,7 @@ namespace kvq {
 struct Shown {
     int64_t len, sink_pages, hole, win0;
 };
-__device__ __forceinline__ Shown shown_context(const DecodeArgs &a, int64_t real, int ps_shift)
+__device__ __forceinline__ Shown shown_context(const ViewArgs &a, int64_t real, int ps_shift)
 {
     Shown v = {real, 0, 0, 0};
     if (a.window > 0) {
