@@ -229,7 +229,8 @@ constexpr int64_t kPairCostTokens = 384;
 
 // A balanced launch: shares of at most 8,192 tokens, as many resident CTAs as
 // the GPU holds, and a workspace slot for every (CTA, pair) that can meet
-// behind the counters that make_plan placed.  False where its numbering or the combine's limits do not fit.
+// behind the counters that make_plan placed.  False where its numbering or the
+// combine's limits do not fit.
 bool plan_balanced(int64_t pairs, int64_t max_ctx, int32_t page_size, bool bf16, bool multi, Plan *p)
 {
     const int64_t unit = page_size > 64 ? page_size : 64;

@@ -184,9 +184,9 @@ constexpr uint64_t kCopyWaitLimitNs = 1000000000ull;
 // unless the diagnostics entry point changed it.
 uint64_t decode_copy_wait_ns();
 
-// Split kernel, the combine fused into its epilogue but for combine_apart.  The tensor maps
-// describe the K and V caches as 2-D [rows][128 bytes] tensors with 128-byte
-// swizzle.
+// Split kernel, the combine fused into its epilogue but for combine_apart.  The
+// tensor maps describe the K and V caches as 2-D [rows][128 bytes] tensors with
+// 128-byte swizzle.
 cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                           cudaStream_t stream);
 // The same kernel's builds with a window (any cache of launch_decode) and for

@@ -220,9 +220,9 @@ KVQ_API kvq_status kvq_quantize_pages(const kvq_cache_desc *src_desc, const void
  *   *max_splits    OUT: splits of the longest possible request,
  *                  ceil(max_pages_per_seq * page_size / *split_tokens).
  *   *workspace_bytes OUT: bytes of workspace kvq_decode_attn needs: the
- *                  arrival counters (4 bytes per request and KV head -- with
- *                  several query tokens per block of 16 query rows of one,
- *                  see those calls --, padded to 256) plus, when a request can span more than one split
+ *                  arrival counters (4 bytes per request and KV head, padded
+ *                  to 256; calls with several query tokens say how many they
+ *                  have) plus, when a request can span more than one split
  *                  and the splits merge through the workspace, the per-split
  *                  partial results.
  * Any OUT pointer may be NULL.
