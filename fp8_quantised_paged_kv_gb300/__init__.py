@@ -1,7 +1,7 @@
 """Python binding of the FP8 paged-KV decode path (libkvq.so, sm_103a).
 
-Argument marshalling only (through ctypes; for the block-scaled, windowed and
-page-copy calls in a small native extension, csrc/kvq_binding.cpp): every step runs in the CUDA kernels behind the C
+Argument marshalling only (through ctypes; for the block-scaled, windowed, page-copy and
+page-table calls in a small native extension, csrc/kvq_binding.cpp): every step runs in the CUDA kernels behind the C
 ABI declared in ``include/kvq.h``.  Functions carry the C names and take
 torch CUDA tensors (device memory, PyTorch's streams); nothing here computes
 on the host, and there is no CPU fallback -- if the library or a GPU is
@@ -18,6 +18,8 @@ missing the calls raise.
     kvq_append_blocks(...), kvq_decode_attn_blocks(...)      the block-scaled cache
     kvq_decode_attn_window(...), kvq_tag_check_window(...)   a sliding window with sinks
     kvq_copy_pages(...)     pages copied inside every cache of a pool
+    kvq_extend_tables(...), kvq_fork_tables(...), kvq_trim_tables(...)
+                            block tables and slots made on the GPU, from a PagePool
     kvq_w4a16_gemm(...)     INT4 weight-only product for decode
 """
 from __future__ import annotations
@@ -90,6 +92,9 @@ _SIGS = {
                                "f32", "i32", "i32", "p", "p", "i32", "p", "size", "i32", "p"],
     "kvq_tag_check_window": ["p", "p", "p", "i32", "i32", "i32", "p", "i32", "i32", "i32", "i32", "p", "p"],
     "kvq_append_blocks": ["desc", "p", "p", "i32", "p", "p", "i32", "p", "i32", "p", "p", "p", "p", "p", "p"],
+    "kvq_extend_tables": ["p", "p", "i32", "p", "i32", "p", "i32", "p", "p", "p", "p"],
+    "kvq_fork_tables": ["p", "p", "p", "p", "i32", "p", "i32", "p", "p", "p", "p", "p"],
+    "kvq_trim_tables": ["p", "p", "p", "i32", "p", "i32", "p"],
     "kvq_copy_pages": ["desc", "p", "i32", "p", "i32", "p", "p", "i32", "p"],
     "kvq_amax_scales": ["desc", "p", "p", "p", "i32", "p", "p", "p"],
     "kvq_quantize_pages": ["desc", "p", "p", "p", "desc", "p", "p", "p", "i32", "p", "p", "p"],
@@ -374,7 +379,7 @@ def workspace_for_blocks(desc: CacheDesc, batch, num_query_tokens, num_q_heads, 
 
 _native = None
 _NATIVE_CALLS = ("kvq_decode_attn_window", "kvq_decode_attn_blocks", "kvq_tag_check_window",
-                 "kvq_append_blocks", "kvq_copy_pages")
+                 "kvq_append_blocks", "kvq_copy_pages", "kvq_extend_tables", "kvq_fork_tables", "kvq_trim_tables")
 
 
 def _load_native():
@@ -454,6 +459,71 @@ def kvq_copy_pages(desc: CacheDesc, caches, exps, src_pages, dst_pages, stream=N
     st = (_native or _load_native()).copy_pages(desc, caches, exps, src_pages, dst_pages, stream)
     if st:
         _check("kvq_copy_pages", st)
+
+
+@dataclasses.dataclass(eq=False)
+class PagePool:
+    """A pool's pages: a stack of the free ones (``free_pages`` int32 [num_pages],
+    of which the first ``free_count`` [1] count), the rows that hold each page
+    (``page_refs`` int32 [num_pages]) and the live tags (``page_tags``, 32-bit
+    [num_pages], or None for tables without tags)."""
+    num_pages: int
+    page_size: int
+    free_pages: "torch.Tensor"
+    free_count: "torch.Tensor"
+    page_refs: "torch.Tensor"
+    page_tags: "torch.Tensor | None" = None
+    scratch: "torch.Tensor | None" = None
+
+    def __post_init__(self):
+        import torch
+        if self.scratch is None:
+            self.scratch = torch.zeros(64 + (self.num_pages + 31) // 32, dtype=torch.int32,
+                                       device=self.free_pages.device)
+
+    @classmethod
+    def create(cls, num_pages: int, page_size: int, device="cuda", tags: bool = True):
+        """A pool whose pages are all free; page 0 is given out first."""
+        import torch
+        ints = dict(dtype=torch.int32, device=device)
+        return cls(num_pages, page_size, torch.arange(num_pages - 1, -1, -1, **ints),
+                   torch.full((1,), num_pages, **ints), torch.zeros(num_pages, **ints),
+                   torch.zeros(num_pages, **ints) if tags else None)
+
+
+def kvq_extend_tables(pool: PagePool, token_offsets, num_tokens: int, seq_lens, block_table, expected_tags,
+                      slot_mapping, refused, stream=None):
+    """Pages and slots for ``num_tokens`` new tokens, rows token_offsets[r] ..
+    token_offsets[r + 1] - 1 of them request r's (int32 [B + 1], or None for
+    num_tokens / B each).  ``seq_lens`` (int32 [B]) and ``block_table`` (int32
+    [B][max_pages]) are brought up to date, ``expected_tags`` (32-bit, of the
+    table's shape; None without tags) likewise; ``slot_mapping`` (int64
+    [num_tokens], or None) and ``refused`` (uint8 [B]) are written."""
+    st = (_native or _load_native()).extend_tables(pool, token_offsets, num_tokens, seq_lens, block_table,
+                                                   expected_tags, slot_mapping, refused, stream)
+    if st:
+        _check("kvq_extend_tables", st)
+
+
+def kvq_fork_tables(pool: PagePool, parents, fork_lens, seq_lens, block_table, expected_tags, src_pages, dst_pages,
+                    refused, stream=None):
+    """Row r starts with the first fork_lens[r] tokens of row parents[r] (int32
+    [B]; negative: r is left alone): whole pages are shared, and for the tokens
+    past them ``kvq_copy_pages(.., src_pages, dst_pages)`` fills a page of its
+    own (int32 [B] each, written: -1 where there is none)."""
+    st = (_native or _load_native()).fork_tables(pool, parents, fork_lens, seq_lens, block_table, expected_tags,
+                                                 src_pages, dst_pages, refused, stream)
+    if st:
+        _check("kvq_fork_tables", st)
+
+
+def kvq_trim_tables(pool: PagePool, keep_lens, seq_lens, block_table, stream=None):
+    """Row r keeps its first keep_lens[r] tokens (int32 [B]; negative or not
+    below its length: all); pages that no row holds any more go back to the
+    pool."""
+    st = (_native or _load_native()).trim_tables(pool, keep_lens, seq_lens, block_table, stream)
+    if st:
+        _check("kvq_trim_tables", st)
 
 
 def kvq_decode_attn_append(desc, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,

@@ -1032,6 +1032,92 @@ kvq_status kvq_copy_pages(const kvq_cache_desc *desc, void *const *caches, int32
     return KVQ_OK;
 }
 
+static kvq_status check_pool(const kvq_page_pool *p, int32_t batch, int32_t max_pages, kvq::PoolArgs *to)
+{
+    if (p == nullptr || p->num_pages <= 0 || batch < 0 || max_pages <= 0)
+        return KVQ_ERR_INVALID_ARG;
+    if (!p->free_pages || !p->free_count || !p->page_refs || !p->scratch)
+        return KVQ_ERR_INVALID_ARG;
+    if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128)
+        return KVQ_ERR_UNSUPPORTED;
+    if (batch > 65535)
+        return KVQ_ERR_UNSUPPORTED;
+    *to = {p->free_pages, p->free_count, p->page_refs, p->page_tags, p->scratch, p->num_pages, p->page_size};
+    return KVQ_OK;
+}
+
+kvq_status kvq_extend_tables(const kvq_page_pool *pool, const int32_t *token_offsets, int32_t num_tokens,
+                             int32_t *seq_lens, int32_t batch, int32_t *block_table,
+                             int32_t max_pages_per_seq, uint32_t *expected_tags, int64_t *slot_mapping,
+                             uint8_t *refused, kvq_stream_t stream)
+{
+    kvq::ExtendArgs a = {};
+    const kvq_status st = check_pool(pool, batch, max_pages_per_seq, &a.pool);
+    if (st != KVQ_OK)
+        return st;
+    if (num_tokens < 0 || (batch == 0 && num_tokens != 0))
+        return KVQ_ERR_INVALID_ARG;
+    if (batch == 0)
+        return KVQ_OK;
+    if (!token_offsets && num_tokens % batch != 0)
+        return KVQ_ERR_INVALID_ARG;
+    if (!seq_lens || !block_table || !refused || !expected_tags != !pool->page_tags)
+        return KVQ_ERR_INVALID_ARG;
+    a.token_offsets = token_offsets;
+    a.seq_lens = seq_lens;
+    a.block_table = block_table;
+    a.expected_tags = expected_tags;
+    a.slot_mapping = slot_mapping;
+    a.refused = refused;
+    a.num_tokens = num_tokens;
+    a.tokens_each = num_tokens / batch;
+    a.batch = batch;
+    a.max_pages_per_seq = max_pages_per_seq;
+    return to_status(kvq::launch_extend_tables(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_fork_tables(const kvq_page_pool *pool, const int32_t *parents, const int32_t *fork_lens,
+                           int32_t *seq_lens, int32_t batch, int32_t *block_table, int32_t max_pages_per_seq,
+                           uint32_t *expected_tags, int32_t *src_pages, int32_t *dst_pages, uint8_t *refused,
+                           kvq_stream_t stream)
+{
+    kvq::ForkArgs a = {};
+    const kvq_status st = check_pool(pool, batch, max_pages_per_seq, &a.pool);
+    if (st != KVQ_OK || batch == 0)
+        return st;
+    if (!parents || !fork_lens || !seq_lens || !block_table || !src_pages || !dst_pages || !refused ||
+        !expected_tags != !pool->page_tags)
+        return KVQ_ERR_INVALID_ARG;
+    a.parents = parents;
+    a.fork_lens = fork_lens;
+    a.seq_lens = seq_lens;
+    a.block_table = block_table;
+    a.expected_tags = expected_tags;
+    a.src_pages = src_pages;
+    a.dst_pages = dst_pages;
+    a.refused = refused;
+    a.batch = batch;
+    a.max_pages_per_seq = max_pages_per_seq;
+    return to_status(kvq::launch_fork_tables(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_trim_tables(const kvq_page_pool *pool, const int32_t *keep_lens, int32_t *seq_lens, int32_t batch,
+                           int32_t *block_table, int32_t max_pages_per_seq, kvq_stream_t stream)
+{
+    kvq::TrimArgs a = {};
+    const kvq_status st = check_pool(pool, batch, max_pages_per_seq, &a.pool);
+    if (st != KVQ_OK || batch == 0)
+        return st;
+    if (!keep_lens || !seq_lens || !block_table)
+        return KVQ_ERR_INVALID_ARG;
+    a.keep_lens = keep_lens;
+    a.seq_lens = seq_lens;
+    a.block_table = block_table;
+    a.batch = batch;
+    a.max_pages_per_seq = max_pages_per_seq;
+    return to_status(kvq::launch_trim_tables(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 kvq_status kvq_decode_attn_append(const kvq_cache_desc *desc, const void *q, int32_t batch,
                                   int32_t num_q_heads, void *k_cache, void *v_cache,
                                   const float *k_scale, const float *v_scale,

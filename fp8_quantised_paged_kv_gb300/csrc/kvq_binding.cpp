@@ -1,5 +1,5 @@
-// kvq_binding.cpp -- argument marshalling of the block-scaled, windowed and
-// page-copy calls: torch tensors in, the C ABI's pointers out.
+// kvq_binding.cpp -- argument marshalling of the block-scaled, windowed,
+// page-copy and page-table calls: torch tensors in, the C ABI's pointers out.
 //
 // These calls take up to sixteen tensors and run for a few microseconds on the
 // GPU when a batch is small; checked tensor by tensor in Python they cost 15
@@ -33,6 +33,9 @@ struct Api {
     decltype(&kvq_tag_check_window) tag_check_window;
     decltype(&kvq_append_blocks) append_blocks;
     decltype(&kvq_copy_pages) copy_pages;
+    decltype(&kvq_extend_tables) extend_tables;
+    decltype(&kvq_fork_tables) fork_tables;
+    decltype(&kvq_trim_tables) trim_tables;
 } api = {};
 
 struct Refused {};                           // a Python exception is set
@@ -435,12 +438,116 @@ PyObject *py_copy_pages(PyObject *, PyObject *const *p, Py_ssize_t nargs)
     });
 }
 
-// bind(addresses): the five entry points of the loaded library, in the order of Api.
+// An attribute of a Python object, released at the end of the scope.
+struct Attribute {
+    PyObject *o;
+    Attribute(PyObject *from, const char *name) : o(PyObject_GetAttrString(from, name))
+    {
+        if (o == nullptr)
+            throw Refused();
+    }
+    ~Attribute() { Py_DECREF(o); }
+    Attribute(const Attribute &) = delete;
+    Attribute &operator=(const Attribute &) = delete;
+};
+
+// A PagePool.  Its tensors live as long as the object does, which the caller holds.
+kvq_page_pool take_pool(Args &a, PyObject *o)
+{
+    kvq_page_pool p;
+    p.num_pages = int_of(Attribute(o, "num_pages").o, "num_pages");
+    p.page_size = int_of(Attribute(o, "page_size").o, "page_size");
+    const int64_t n = p.num_pages;
+    if (n <= 0)
+        refuse(PyExc_ValueError, "num_pages: expected 1 or more");
+    const auto ints = [&](const char *name, int64_t size) {
+        return static_cast<int32_t *>(a.take(Attribute(o, name).o, name, {ScalarType::Int}, {size}));
+    };
+    p.free_pages = ints("free_pages", n);
+    p.free_count = ints("free_count", 1);
+    p.page_refs = ints("page_refs", n);
+    const Attribute tags(o, "page_tags");
+    p.page_tags = tags.o == Py_None ? nullptr : static_cast<uint32_t *>(a.take_words(tags.o, "page_tags", {n}));
+    p.scratch = reinterpret_cast<uint32_t *>(
+        ints("scratch", static_cast<int64_t>(KVQ_POOL_SCRATCH_BYTES(p.num_pages) / 4)));
+    return p;
+}
+
+// (pool, token_offsets, num_tokens, seq_lens, block_table, expected_tags, slot_mapping, refused, stream)
+PyObject *py_extend_tables(PyObject *, PyObject *const *p, Py_ssize_t nargs)
+{
+    return entry("kvq_extend_tables", nargs, 9, [&]() -> PyObject * {
+        Args a("kvq_extend_tables");
+        const kvq_page_pool pool = take_pool(a, p[0]);
+        int32_t *table;
+        const auto [B, maxp] = take_table(a, p[4], const_cast<const int32_t **>(&table));
+        const auto *off = static_cast<const int32_t *>(
+            a.take_or_none(p[1], "token_offsets", {ScalarType::Int}, {static_cast<int64_t>(B) + 1}));
+        const int32_t T = int_of(p[2], "num_tokens");
+        auto *seq = static_cast<int32_t *>(a.take(p[3], "seq_lens", {ScalarType::Int}, {B}));
+        auto *tags = p[5] == Py_None ? nullptr
+                                     : static_cast<uint32_t *>(a.take_words(p[5], "expected_tags", {B, maxp}));
+        auto *slots = static_cast<int64_t *>(a.take_or_none(p[6], "slot_mapping", {ScalarType::Long}, {T}));
+        auto *refused = static_cast<uint8_t *>(a.take(p[7], "refused", {ScalarType::Byte}, {B}));
+        const int dev = a.device();
+        const kvq_stream_t stream = a.stream(p[8]);
+        const int32_t rows = B, entries = maxp;
+        return launch(dev, [&] {
+            return api.extend_tables(&pool, off, T, seq, rows, table, entries, tags, slots, refused, stream);
+        });
+    });
+}
+
+// (pool, parents, fork_lens, seq_lens, block_table, expected_tags, src_pages, dst_pages, refused, stream)
+PyObject *py_fork_tables(PyObject *, PyObject *const *p, Py_ssize_t nargs)
+{
+    return entry("kvq_fork_tables", nargs, 10, [&]() -> PyObject * {
+        Args a("kvq_fork_tables");
+        const kvq_page_pool pool = take_pool(a, p[0]);
+        int32_t *table;
+        const auto [B, maxp] = take_table(a, p[4], const_cast<const int32_t **>(&table));
+        const int64_t b = B;
+        const auto ints = [&](PyObject *o, const char *name) {
+            return static_cast<int32_t *>(a.take(o, name, {ScalarType::Int}, {b}));
+        };
+        const int32_t *parents = ints(p[1], "parents"), *lens = ints(p[2], "fork_lens");
+        int32_t *seq = ints(p[3], "seq_lens"), *src = ints(p[6], "src_pages"), *dst = ints(p[7], "dst_pages");
+        auto *tags = p[5] == Py_None ? nullptr
+                                     : static_cast<uint32_t *>(a.take_words(p[5], "expected_tags", {B, maxp}));
+        auto *refused = static_cast<uint8_t *>(a.take(p[8], "refused", {ScalarType::Byte}, {B}));
+        const int dev = a.device();
+        const kvq_stream_t stream = a.stream(p[9]);
+        const int32_t rows = B, entries = maxp;
+        return launch(dev, [&] {
+            return api.fork_tables(&pool, parents, lens, seq, rows, table, entries, tags, src, dst, refused, stream);
+        });
+    });
+}
+
+// (pool, keep_lens, seq_lens, block_table, stream)
+PyObject *py_trim_tables(PyObject *, PyObject *const *p, Py_ssize_t nargs)
+{
+    return entry("kvq_trim_tables", nargs, 5, [&]() -> PyObject * {
+        Args a("kvq_trim_tables");
+        const kvq_page_pool pool = take_pool(a, p[0]);
+        int32_t *table;
+        const auto [B, maxp] = take_table(a, p[3], const_cast<const int32_t **>(&table));
+        const auto *keep = static_cast<const int32_t *>(a.take(p[1], "keep_lens", {ScalarType::Int}, {B}));
+        auto *seq = static_cast<int32_t *>(a.take(p[2], "seq_lens", {ScalarType::Int}, {B}));
+        const int dev = a.device();
+        const kvq_stream_t stream = a.stream(p[4]);
+        const int32_t rows = B, entries = maxp;
+        return launch(dev, [&] { return api.trim_tables(&pool, keep, seq, rows, table, entries, stream); });
+    });
+}
+
+// bind(addresses): the entry points of the loaded library, in the order of Api.
 PyObject *py_bind(PyObject *, PyObject *const *p, Py_ssize_t nargs)
 {
-    return entry("bind", nargs, 5, [&]() -> PyObject * {
-        void *f[5];
-        for (int i = 0; i < 5; ++i) {
+    constexpr int kEntries = 8;
+    return entry("bind", nargs, kEntries, [&]() -> PyObject * {
+        void *f[kEntries];
+        for (int i = 0; i < kEntries; ++i) {
             f[i] = PyLong_AsVoidPtr(p[i]);
             if (f[i] == nullptr) {
                 if (!PyErr_Occurred())
@@ -453,6 +560,9 @@ PyObject *py_bind(PyObject *, PyObject *const *p, Py_ssize_t nargs)
         api.tag_check_window = reinterpret_cast<decltype(api.tag_check_window)>(f[2]);
         api.append_blocks = reinterpret_cast<decltype(api.append_blocks)>(f[3]);
         api.copy_pages = reinterpret_cast<decltype(api.copy_pages)>(f[4]);
+        api.extend_tables = reinterpret_cast<decltype(api.extend_tables)>(f[5]);
+        api.fork_tables = reinterpret_cast<decltype(api.fork_tables)>(f[6]);
+        api.trim_tables = reinterpret_cast<decltype(api.trim_tables)>(f[7]);
         Py_RETURN_NONE;
     });
 }
@@ -470,6 +580,9 @@ PyMethodDef methods[] = {method("bind", py_bind),
                          method("tag_check_window", py_tag_check_window),
                          method("append_blocks", py_append_blocks),
                          method("copy_pages", py_copy_pages),
+                         method("extend_tables", py_extend_tables),
+                         method("fork_tables", py_fork_tables),
+                         method("trim_tables", py_trim_tables),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kvq_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

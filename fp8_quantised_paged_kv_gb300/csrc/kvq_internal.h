@@ -95,6 +95,45 @@ struct CopyPagesArgs {
 };
 cudaError_t launch_copy_pages(const CopyPagesArgs &a, cudaStream_t stream);
 
+// Page tables kept on the GPU.
+struct PoolArgs {
+    int32_t *free_pages, *free_count;       // [num_pages], [1]
+    int32_t *page_refs;                     // [num_pages]
+    uint32_t *page_tags;                    // [num_pages] or null
+    uint32_t *scratch;                      // arrival counter, a flag, from kPoolBitmapWord on a bit per page
+    int32_t num_pages, page_size;
+};
+constexpr int kPoolBitmapWord = 64;
+struct ExtendArgs {
+    PoolArgs pool;
+    const int32_t *token_offsets;           // [batch + 1], or null: tokens_each per request
+    int32_t *seq_lens, *block_table;        // [batch], [batch][max_pages]
+    uint32_t *expected_tags;                // [batch][max_pages] or null
+    int64_t *slot_mapping;                  // [num_tokens] or null
+    uint8_t *refused;                       // [batch]
+    int32_t num_tokens, tokens_each, batch, max_pages_per_seq;
+    int32_t per_cta, team;                  // set by the launch
+};
+cudaError_t launch_extend_tables(ExtendArgs a, cudaStream_t stream);
+struct ForkArgs {
+    PoolArgs pool;
+    const int32_t *parents, *fork_lens;     // [batch]
+    int32_t *seq_lens, *block_table;
+    uint32_t *expected_tags;
+    int32_t *src_pages, *dst_pages;         // [batch]
+    uint8_t *refused;
+    int32_t batch, max_pages_per_seq;
+    int32_t per_cta;                        // set by the launch
+};
+cudaError_t launch_fork_tables(ForkArgs a, cudaStream_t stream);
+struct TrimArgs {
+    PoolArgs pool;
+    const int32_t *keep_lens;               // [batch]
+    int32_t *seq_lens, *block_table;
+    int32_t batch, max_pages_per_seq;
+};
+cudaError_t launch_trim_tables(const TrimArgs &a, cudaStream_t stream);
+
 // INT4 weight-only product y[m][n] = sum_k x[m][k] q[n][k] s[n][k / 128] for
 // up to 16 rows of x per launch.  The weights are read through a 2-D tensor
 // map over W viewed as [N rows][K / 2 bytes].

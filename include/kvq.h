@@ -503,6 +503,117 @@ KVQ_API kvq_status kvq_copy_pages(const kvq_cache_desc *desc, void *const *cache
                                   const int32_t *dst_pages, int32_t num_listed, kvq_stream_t stream);
 
 /*
+ * Page tables kept on the GPU.  kvq_extend_tables gives rows pages and slots
+ * for new tokens, kvq_fork_tables starts rows on the pages of others, and
+ * kvq_trim_tables gives pages back.  Lengths, counts and ids stay in device
+ * memory: a captured step can make its own tables.
+ *
+ * kvq_page_pool -- the pool's state.  A HOST struct of device arrays, read
+ * before a call returns:
+ *   free_pages     int32 [num_pages]: a stack; its first *free_count entries
+ *                  are the pages that no row holds, the last of them the next
+ *                  to be given out.  (Entries past the count are not read.)
+ *   free_count     int32 [1].
+ *   page_refs      int32 [num_pages]: the rows that hold each page, 0 if free.
+ *   page_tags      uint32 [num_pages] or NULL: the live tags that
+ *                  kvq_tag_check reads.  A page that is given out gets the next
+ *                  number as its tag (modulo 2^32); a row's expected tag is the
+ *                  one its page had then.  expected_tags of the calls is NULL
+ *                  exactly where page_tags is.
+ *   scratch        KVQ_POOL_SCRATCH_BYTES(num_pages) bytes, zero before the first
+ *                  call; every call leaves them zero.
+ * num_pages is 1 or more, page_size 16, 32, 64 or 128.  Calls on one pool or
+ * one table must run one after another; up to 65535 requests a call
+ * (KVQ_ERR_UNSUPPORTED above).  No call copies cache contents.
+ */
+typedef struct {
+    int32_t num_pages, page_size;
+    int32_t *free_pages, *free_count, *page_refs;
+    uint32_t *page_tags, *scratch;
+} kvq_page_pool;
+#define KVQ_POOL_SCRATCH_BYTES(num_pages) (256 + 4 * (((size_t)(num_pages) + 31) / 32))
+
+/*
+ * kvq_extend_tables -- room for new tokens behind the requests' last ones.
+ * Request r of seq_lens[r] tokens and n new ones holds ceil(seq_lens[r] / ps)
+ * pages before and ceil((seq_lens[r] + n) / ps) after; the pages between come
+ * from the free list, request after request, each request's in the order of
+ * its tokens.
+ *
+ *   token_offsets  int32 [batch + 1]: request r's new tokens are the call's
+ *                  tokens token_offsets[r] .. token_offsets[r + 1] - 1.  NULL:
+ *                  num_tokens / batch each (KVQ_ERR_INVALID_ARG unless that is
+ *                  a whole number).
+ *   seq_lens       int32 [batch], IN/OUT: the tokens held, then with the new
+ *                  ones.
+ *   block_table    int32 [batch][max_pages_per_seq], IN/OUT: only the entries of
+ *                  the pages given out are written.
+ *   expected_tags  uint32 [batch][max_pages_per_seq] or NULL, OUT: likewise.
+ *   slot_mapping   int64 [num_tokens] or NULL, OUT: each new token's slot, as
+ *                  kvq_append takes it; -1 for a refused request's.  Places that
+ *                  no request's offsets name are left as they were.
+ *   refused        uint8 [batch], OUT: 1 if the request got nothing (its row,
+ *                  length and tags are as before), else 0.  It may serve as
+ *                  the step's abort_flags.
+ * A request is refused if its length or number of tokens is negative, if its
+ * offsets leave [0, num_tokens], if its row is too short, or if the pool runs
+ * out: if the pages that it and all requests before it want, refused ones for
+ * want of pages among them, are more than the list holds, and it wants one.
+ * Two requests' offsets must not overlap.  A row's last, partly filled page
+ * must be its own (kvq_fork_tables sees to that).
+ */
+KVQ_API kvq_status kvq_extend_tables(const kvq_page_pool *pool, const int32_t *token_offsets,
+                                     int32_t num_tokens, int32_t *seq_lens, int32_t batch,
+                                     int32_t *block_table, int32_t max_pages_per_seq,
+                                     uint32_t *expected_tags, int64_t *slot_mapping,
+                                     uint8_t *refused, kvq_stream_t stream);
+
+/*
+ * kvq_fork_tables -- row r starts with the first L = fork_lens[r] tokens of row
+ * p = parents[r]: it shares p's first floor(L / ps) pages (one holder more
+ * each), and where L does not end a page it gets a page of its own for the
+ * tokens past them, to be filled by
+ *   kvq_copy_pages(.., src_pages, dst_pages, batch)
+ * before either row is extended.
+ *
+ *   parents        int32 [batch]; negative: r is not forked, and nothing of it
+ *                  changes.
+ *   fork_lens      int32 [batch].
+ *   seq_lens, block_table, expected_tags   IN/OUT, as in kvq_extend_tables:
+ *                  seq_lens[r] becomes L, the shared entries and their expected
+ *                  tags are p's.
+ *   src_pages, dst_pages   int32 [batch], OUT: the page to copy and the row's
+ *                  own, or -1 and -1 (which kvq_copy_pages skips).
+ *   refused        uint8 [batch], OUT: 1 if r should have been forked and was
+ *                  not, else 0.
+ * A fork is refused if p is r or past the batch, if row r holds tokens, if L is
+ * negative or more than p held before the call, or if the pool runs out (the
+ * rule of kvq_extend_tables, over the forks that want a page).
+ */
+KVQ_API kvq_status kvq_fork_tables(const kvq_page_pool *pool, const int32_t *parents,
+                                   const int32_t *fork_lens, int32_t *seq_lens, int32_t batch,
+                                   int32_t *block_table, int32_t max_pages_per_seq,
+                                   uint32_t *expected_tags, int32_t *src_pages, int32_t *dst_pages,
+                                   uint8_t *refused, kvq_stream_t stream);
+
+/*
+ * kvq_trim_tables -- row r keeps its first keep_lens[r] tokens (0: a finished
+ * request; a few less: drafts that were rejected).  The pages past
+ * ceil(keep_lens[r] / ps) lose a holder, and those left without one go to the
+ * free list in ascending order, whatever the order of the rows.
+ *
+ *   keep_lens      int32 [batch]; a row with a negative one, or with one that
+ *                  is not below its length, stays as it is.
+ *   seq_lens, block_table   IN/OUT: the length becomes keep_lens[r], the
+ *                  entries given back -1.
+ * Entries outside [0, num_pages) are dropped, and a page is given back no more
+ * often than it is held.  A row longer than its table counts as full.
+ */
+KVQ_API kvq_status kvq_trim_tables(const kvq_page_pool *pool, const int32_t *keep_lens,
+                                   int32_t *seq_lens, int32_t batch, int32_t *block_table,
+                                   int32_t max_pages_per_seq, kvq_stream_t stream);
+
+/*
  * kvq_decode_attn_append -- kvq_append of each request's new token followed
  * by kvq_decode_attn, in one launch.  Request r's new token is the last one
  * it attends to: position seq_lens[r] - 1, written at
