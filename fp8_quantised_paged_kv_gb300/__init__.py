@@ -1,7 +1,7 @@
 """Python binding of the FP8 paged-KV decode path (libkvq.so, sm_103a).
 
-Argument marshalling only (through ctypes; for the block-scaled, windowed, page-copy and
-page-table calls in a small native extension, csrc/kvq_binding.cpp): every step runs in the CUDA kernels behind the C
+Argument marshalling only (through ctypes; for the block-scaled, windowed, shared-prefix,
+page-copy and page-table calls in a small native extension, csrc/kvq_binding.cpp): every step runs in the CUDA kernels behind the C
 ABI declared in ``include/kvq.h``.  Functions carry the C names and take
 torch CUDA tensors (device memory, PyTorch's streams); nothing here computes
 on the host, and there is no CPU fallback -- if the library or a GPU is
@@ -17,6 +17,8 @@ missing the calls raise.
     kvq_amax_scales(...), kvq_quantize_pages(...)            prefill -> decode handoff
     kvq_append_blocks(...), kvq_decode_attn_blocks(...)      the block-scaled cache
     kvq_decode_attn_window(...), kvq_tag_check_window(...)   a sliding window with sinks
+    kvq_decode_attn_prefix(...), kvq_decode_attn_prefix_blocks(...)
+                            requests that share their first pages, read once
     kvq_copy_pages(...)     pages copied inside every cache of a pool
     kvq_extend_tables(...), kvq_fork_tables(...), kvq_trim_tables(...)
                             block tables and slots made on the GPU, from a PagePool
@@ -92,6 +94,11 @@ _SIGS = {
                                "f32", "i32", "i32", "p", "p", "i32", "p", "size", "i32", "p"],
     "kvq_tag_check_window": ["p", "p", "p", "i32", "i32", "i32", "p", "i32", "i32", "i32", "i32", "p", "p"],
     "kvq_append_blocks": ["desc", "p", "p", "i32", "p", "p", "i32", "p", "i32", "p", "p", "p", "p", "p", "p"],
+    "kvq_decode_plan_prefix": ["desc", "i32", "i32", "i32", "i32", "p"],
+    "kvq_decode_attn_prefix": ["desc", "p", "i32", "i32", "i32", "p", "p", "p", "p", "p", "i32", "p", "p", "p",
+                               "f32", "p", "p", "i32", "p", "size", "p"],
+    "kvq_decode_attn_prefix_blocks": ["desc", "p", "i32", "i32", "i32", "p", "p", "p", "p", "p", "i32", "p", "p",
+                                      "p", "f32", "p", "p", "i32", "p", "size", "p"],
     "kvq_extend_tables": ["p", "p", "i32", "p", "i32", "p", "i32", "p", "p", "p", "p"],
     "kvq_fork_tables": ["p", "p", "p", "p", "i32", "p", "i32", "p", "p", "p", "p", "p"],
     "kvq_trim_tables": ["p", "p", "p", "i32", "p", "i32", "p"],
@@ -377,9 +384,31 @@ def workspace_for_blocks(desc: CacheDesc, batch, num_query_tokens, num_q_heads, 
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
 
 
+def kvq_decode_plan_prefix(desc: CacheDesc, batch: int, num_query_tokens: int, num_q_heads: int,
+                           max_pages_per_seq: int) -> int:
+    """workspace_bytes that kvq_decode_attn_prefix and kvq_decode_attn_prefix_blocks will use."""
+    for v in (batch, num_query_tokens, num_q_heads, max_pages_per_seq):
+        if not -2**31 <= v < 2**31:                       # ctypes would wrap it
+            raise OverflowError(f"kvq_decode_plan_prefix: {v} does not fit 32 bits")
+    n = ctypes.c_size_t()
+    st = load().kvq_decode_plan_prefix(ctypes.byref(desc.c()), batch, num_query_tokens, num_q_heads,
+                                       max_pages_per_seq, ctypes.byref(n))
+    _check("kvq_decode_plan_prefix", st)
+    return n.value
+
+
+def workspace_for_prefix(desc: CacheDesc, batch, num_query_tokens, num_q_heads, max_pages_per_seq, device="cuda"):
+    """Allocate (with torch) the workspace of a call over shared prefixes; it needs no contents."""
+    import torch
+    with torch.cuda.device(device):                       # the plan goes by that device's SMs
+        nbytes = kvq_decode_plan_prefix(desc, batch, num_query_tokens, num_q_heads, max_pages_per_seq)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 _native = None
 _NATIVE_CALLS = ("kvq_decode_attn_window", "kvq_decode_attn_blocks", "kvq_tag_check_window",
-                 "kvq_append_blocks", "kvq_copy_pages", "kvq_extend_tables", "kvq_fork_tables", "kvq_trim_tables")
+                 "kvq_append_blocks", "kvq_copy_pages", "kvq_extend_tables", "kvq_fork_tables", "kvq_trim_tables",
+                 "kvq_decode_attn_prefix", "kvq_decode_attn_prefix_blocks")
 
 
 def _load_native():
@@ -425,6 +454,32 @@ def kvq_decode_attn_blocks(desc: CacheDesc, q, k_cache, v_cache, k_exp, v_exp, b
         abort_flags, out, workspace, num_splits, stream)
     if st:
         _check("kvq_decode_attn_blocks", st)
+    return out
+
+
+def kvq_decode_attn_prefix(desc: CacheDesc, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, prefix_of,
+                           prefix_lens, softmax_scale, abort_flags, out, workspace, stream=None):
+    """Decode attention of n query tokens per request (q bf16 [B][n][Hq][D]) of
+    requests that share their first pages: request r's first prefix_lens[r]
+    tokens are those of request prefix_of[r] (int32 [B] each; negative: r shares
+    nothing).  Into ``out`` (bf16 or fp32 [B][n][Hq][D])."""
+    st = (_native or _load_native()).attn_prefix(
+        desc, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, prefix_of, prefix_lens, softmax_scale,
+        abort_flags, out, workspace, stream)
+    if st:
+        _check("kvq_decode_attn_prefix", st)
+    return out
+
+
+def kvq_decode_attn_prefix_blocks(desc: CacheDesc, q, k_cache, v_cache, k_exp, v_exp, block_table, seq_lens,
+                                  prefix_of, prefix_lens, softmax_scale, abort_flags, out, workspace, stream=None):
+    """kvq_decode_attn_prefix over a block-scaled cache: uint8 e4m3 codes with
+    exponents int8 [num_pages][Hkv][page_size / 16]."""
+    st = (_native or _load_native()).attn_prefix_blocks(
+        desc, q, k_cache, v_cache, k_exp, v_exp, block_table, seq_lens, prefix_of, prefix_lens, softmax_scale,
+        abort_flags, out, workspace, stream)
+    if st:
+        _check("kvq_decode_attn_prefix_blocks", st)
     return out
 
 

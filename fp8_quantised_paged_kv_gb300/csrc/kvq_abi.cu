@@ -460,6 +460,24 @@ bool make_cache_map(CUtensorMap *map, const kvq_cache_desc *d, const void *cache
     return r == CUDA_SUCCESS;
 }
 
+// A bf16 cache as rows of 128 values, read 64 wide: what the kernel over shared
+// pages feeds to the tensor cores as it is.
+bool make_half_row_map(CUtensorMap *map, const kvq_cache_desc *d, const void *cache, int box_tokens)
+{
+    EncodeFn fn = encode_fn();
+    if (fn == nullptr)
+        return false;
+    const cuuint64_t dims[2] = {kHeadDim, static_cast<cuuint64_t>(d->num_pages) * d->num_kv_heads * d->page_size};
+    const cuuint64_t strides[1] = {2 * kHeadDim};
+    const cuuint32_t box[2] = {kHeadDim / 2, static_cast<cuuint32_t>(box_tokens)};
+    const cuuint32_t estr[2] = {1, 1};
+    std::memset(map, 0, sizeof *map);
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(cache), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 kvq_status to_status(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
 
 struct DecodeCall {
@@ -1032,6 +1050,178 @@ kvq_status kvq_copy_pages(const kvq_cache_desc *desc, void *const *caches, int32
     return KVQ_OK;
 }
 
+// The plan of a call over shared prefixes: the requests' own pages as one
+// balanced launch whose every split goes to the workspace, and a place per
+// (CTA, row) that can meet for the parts of the shared pages.  No arrival
+// counters.
+struct PrefixPlan {
+    Plan own;
+    int64_t places;
+    size_t lse_at, pairs_at, rec_at, pre_lse_at, pre_o_at, bytes;
+    int32_t ctas;
+};
+
+static kvq_status make_prefix_plan(const kvq_cache_desc *d, int32_t batch, int32_t n_query, int32_t num_q_heads,
+                                   int32_t max_pages, bool blocks, PrefixPlan *p)
+{
+    const View view = {0, 0, blocks, nullptr, nullptr};
+    kvq_status st = make_plan(d, batch, num_q_heads, max_pages, 0, &p->own, n_query, &view);
+    if (st != KVQ_OK)
+        return st;
+    const int g = num_q_heads / d->num_kv_heads;
+    const bool bf16 = d->cache_dtype == KVQ_CACHE_BF16, multi = n_query > 1;
+    Plan &own = p->own;
+    own.umma = false;
+    own.cluster = 0;
+    own.row_blocks = multi ? (n_query * g + kvq::kMultiRowsPerCta - 1) / kvq::kMultiRowsPerCta : 1;
+    const int64_t pairs = static_cast<int64_t>(batch > 0 ? batch : 1) * d->num_kv_heads * own.row_blocks;
+    if (!plan_balanced(pairs, static_cast<int64_t>(max_pages) * d->page_size, d->page_size, bf16, multi, &own))
+        return KVQ_ERR_UNSUPPORTED;
+    p->ctas = kvq::device_sm_count();
+    const int64_t rows = static_cast<int64_t>(batch) * n_query * num_q_heads;
+    p->places = static_cast<int64_t>(p->ctas) * kvq::kPrefixRows + 2 * rows;
+    if (p->places > 0x7FFFFFFF)
+        return KVQ_ERR_UNSUPPORTED;
+    size_t at = 0;
+    const auto take = [&](size_t bytes) {
+        const size_t was = at;
+        at += (bytes + 255) / 256 * 256;
+        return was;
+    };
+    p->lse_at = take(own.lse_bytes + own.o_bytes);
+    p->pairs_at = take(static_cast<size_t>(pairs) * sizeof(int2));
+    p->rec_at = take(static_cast<size_t>(rows) * sizeof(int4));
+    p->pre_lse_at = take(static_cast<size_t>(p->places) * sizeof(float));
+    p->pre_o_at = take(static_cast<size_t>(p->places) * kHeadDim * sizeof(float));
+    p->bytes = at;
+    return KVQ_OK;
+}
+
+kvq_status kvq_decode_plan_prefix(const kvq_cache_desc *desc, int32_t batch, int32_t num_query_tokens,
+                                  int32_t num_q_heads, int32_t max_pages_per_seq, size_t *workspace_bytes)
+{
+    PrefixPlan p;
+    const kvq_status st = make_prefix_plan(desc, batch, num_query_tokens, num_q_heads, max_pages_per_seq, false, &p);
+    if (st == KVQ_OK && workspace_bytes)
+        *workspace_bytes = p.bytes;
+    return st;
+}
+
+static kvq_status decode_prefix(const kvq_cache_desc *desc, const void *q, int32_t batch, int32_t num_query_tokens,
+                                int32_t num_q_heads, const void *k_cache, const void *v_cache, const float *k_scale,
+                                const float *v_scale, const int8_t *k_exp, const int8_t *v_exp, bool blocks,
+                                const int32_t *block_table, int32_t max_pages_per_seq, const int32_t *seq_lens,
+                                const int32_t *prefix_of, const int32_t *prefix_lens, float softmax_scale,
+                                const uint8_t *abort_flags, void *out, int32_t out_dtype, void *workspace,
+                                size_t workspace_bytes, kvq_stream_t stream)
+{
+    PrefixPlan p;
+    kvq_status st = make_prefix_plan(desc, batch, num_query_tokens, num_q_heads, max_pages_per_seq, blocks, &p);
+    if (st != KVQ_OK)
+        return st;
+    if (out_dtype != KVQ_OUT_BF16 && out_dtype != KVQ_OUT_FP32)
+        return KVQ_ERR_INVALID_ARG;
+    if (!std::isfinite(softmax_scale))
+        return KVQ_ERR_INVALID_ARG;
+    if (batch == 0)
+        return KVQ_OK;
+    const bool bf16 = desc->cache_dtype == KVQ_CACHE_BF16;
+    if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !prefix_of || !prefix_lens || !out)
+        return KVQ_ERR_INVALID_ARG;
+    if (blocks ? !k_exp || !v_exp : !bf16 && (!k_scale || !v_scale))
+        return KVQ_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+        return KVQ_ERR_INVALID_ARG;
+    if (workspace == nullptr || workspace_bytes < p.bytes)
+        return KVQ_ERR_WORKSPACE;
+    if (!aligned16(workspace))
+        return KVQ_ERR_INVALID_ARG;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    kvq::PrefixArgs a = {};
+    a.q = q;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.k_exp = k_exp;
+    a.v_exp = v_exp;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.abort_flags = abort_flags;
+    a.out = out;
+    a.ws_lse = reinterpret_cast<float *>(ws + p.lse_at);
+    a.ws_o = reinterpret_cast<float *>(ws + p.lse_at + p.own.lse_bytes);
+    a.ws_pairs = reinterpret_cast<int2 *>(ws + p.pairs_at);
+    a.combine_apart = true;
+    a.batch = batch;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = desc->num_kv_heads;
+    a.group = num_q_heads / desc->num_kv_heads;
+    a.page_size = desc->page_size;
+    a.num_pages = desc->num_pages;
+    a.max_pages_per_seq = max_pages_per_seq;
+    a.split_tokens = p.own.split_tokens;
+    a.max_splits = p.own.max_splits;
+    a.resident_ctas = p.own.resident_ctas;
+    a.balanced_ctas = p.own.balanced_ctas;
+    a.unit_shift = p.own.unit_shift;
+    a.min_split_units = p.own.min_split_units;
+    a.pair_cost = p.own.pair_cost;
+    a.n_query = num_query_tokens;
+    a.row_blocks = p.own.row_blocks;
+    a.qk_scale_log2 = softmax_scale * 1.4426950408889634f;
+    a.copy_wait_ns = kvq::decode_copy_wait_ns();
+    a.out_fp32 = out_dtype == KVQ_OUT_FP32;
+    a.bf16_cache = bf16;
+    a.prefix_of = prefix_of;
+    a.prefix_lens = prefix_lens;
+    a.pre_rec = reinterpret_cast<int4 *>(ws + p.rec_at);
+    a.pre_lse = reinterpret_cast<float *>(ws + p.pre_lse_at);
+    a.pre_o = reinterpret_cast<float4 *>(ws + p.pre_o_at);
+    a.pre_ctas = p.ctas;
+    CUtensorMap km, vm, pk, pv;
+    if (!make_cache_map(&km, desc, k_cache) || !make_cache_map(&vm, desc, v_cache))
+        return KVQ_ERR_CUDA;
+    if (bf16) {
+        const int box = kvq::prefix_box_tokens(desc->page_size, true, a.out_fp32);
+        if (!make_half_row_map(&pk, desc, k_cache, box) || !make_half_row_map(&pv, desc, v_cache, box))
+            return KVQ_ERR_CUDA;
+    }
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = kvq::launch_prefix_rows(a, bf16 ? pk : km, bf16 ? pv : vm, s);
+    if (e == cudaSuccess)
+        e = blocks ? kvq::launch_decode_own_blocks(a, km, vm, s) : kvq::launch_decode_own(a, km, vm, s);
+    if (e == cudaSuccess)
+        e = kvq::launch_combine_prefix(a, s);
+    return to_status(e);
+}
+
+kvq_status kvq_decode_attn_prefix(const kvq_cache_desc *desc, const void *q, int32_t batch,
+                                  int32_t num_query_tokens, int32_t num_q_heads, const void *k_cache,
+                                  const void *v_cache, const float *k_scale, const float *v_scale,
+                                  const int32_t *block_table, int32_t max_pages_per_seq,
+                                  const int32_t *seq_lens, const int32_t *prefix_of,
+                                  const int32_t *prefix_lens, float softmax_scale,
+                                  const uint8_t *abort_flags, void *out, int32_t out_dtype,
+                                  void *workspace, size_t workspace_bytes, kvq_stream_t stream)
+{
+    return decode_prefix(desc, q, batch, num_query_tokens, num_q_heads, k_cache, v_cache, k_scale, v_scale, nullptr,
+                         nullptr, false, block_table, max_pages_per_seq, seq_lens, prefix_of, prefix_lens,
+                         softmax_scale, abort_flags, out, out_dtype, workspace, workspace_bytes, stream);
+}
+
+kvq_status kvq_decode_attn_prefix_blocks(const kvq_cache_desc *desc, const void *q, int32_t batch,
+                                         int32_t num_query_tokens, int32_t num_q_heads, const void *k_cache,
+                                         const void *v_cache, const int8_t *k_exp, const int8_t *v_exp,
+                                         const int32_t *block_table, int32_t max_pages_per_seq,
+                                         const int32_t *seq_lens, const int32_t *prefix_of,
+                                         const int32_t *prefix_lens, float softmax_scale,
+                                         const uint8_t *abort_flags, void *out, int32_t out_dtype,
+                                         void *workspace, size_t workspace_bytes, kvq_stream_t stream)
+{
+    return decode_prefix(desc, q, batch, num_query_tokens, num_q_heads, k_cache, v_cache, nullptr, nullptr, k_exp,
+                         v_exp, true, block_table, max_pages_per_seq, seq_lens, prefix_of, prefix_lens, softmax_scale,
+                         abort_flags, out, out_dtype, workspace, workspace_bytes, stream);
+}
+
 static kvq_status check_pool(const kvq_page_pool *p, int32_t batch, int32_t max_pages, kvq::PoolArgs *to)
 {
     if (p == nullptr || p->num_pages <= 0 || batch < 0 || max_pages <= 0)
@@ -1203,7 +1393,7 @@ KVQ_API kvq_status kvq_phase_stamps(int32_t which, unsigned long long *host, siz
 
 kvq_status kvq_device_error(uint32_t *bits, int32_t clear)
 {
-    uint32_t a = 0, b = 0, c = 0, d = 0, f = 0, g = 0;
+    uint32_t a = 0, b = 0, c = 0, d = 0, f = 0, g = 0, h = 0, i = 0, j = 0;
     cudaError_t e = kvq::read_device_error(&a, clear != 0);
     if (e == cudaSuccess)
         e = kvq::read_w4_error(&b, clear != 0);
@@ -1215,8 +1405,14 @@ kvq_status kvq_device_error(uint32_t *bits, int32_t clear)
         e = kvq::read_blocks_error(&f, clear != 0);
     if (e == cudaSuccess)
         e = kvq::read_umma_view_error(&g, clear != 0);
+    if (e == cudaSuccess)
+        e = kvq::read_prefix_error(&h, clear != 0);
+    if (e == cudaSuccess)
+        e = kvq::read_own_error(&i, clear != 0);
+    if (e == cudaSuccess)
+        e = kvq::read_own_blocks_error(&j, clear != 0);
     if (bits)
-        *bits = a | b | c | d | f | g;
+        *bits = a | b | c | d | f | g | h | i | j;
     return to_status(e);
 }
 

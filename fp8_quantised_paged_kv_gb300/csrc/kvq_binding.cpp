@@ -1,5 +1,5 @@
 // kvq_binding.cpp -- argument marshalling of the block-scaled, windowed,
-// page-copy and page-table calls: torch tensors in, the C ABI's pointers out.
+// shared-prefix, page-copy and page-table calls: torch tensors in, the C ABI's pointers out.
 //
 // These calls take up to sixteen tensors and run for a few microseconds on the
 // GPU when a batch is small; checked tensor by tensor in Python they cost 15
@@ -36,6 +36,8 @@ struct Api {
     decltype(&kvq_extend_tables) extend_tables;
     decltype(&kvq_fork_tables) fork_tables;
     decltype(&kvq_trim_tables) trim_tables;
+    decltype(&kvq_decode_attn_prefix) attn_prefix;
+    decltype(&kvq_decode_attn_prefix_blocks) attn_prefix_blocks;
 } api = {};
 
 struct Refused {};                           // a Python exception is set
@@ -263,23 +265,28 @@ PyObject *entry(const char *fn, Py_ssize_t nargs, Py_ssize_t want, const Body &b
     }
 }
 
-// (desc, q, k_cache, v_cache, k_scale | k_exp, v_scale | v_exp, block_table,
-//  seq_lens, softmax_scale, window, num_sinks, abort_flags, out, workspace, num_splits, stream)
-PyObject *decode_attn(const char *fn, bool blocks, PyObject *const *p, Py_ssize_t nargs)
-{
-    return entry(fn, nargs, 16, [&]() -> PyObject * {
-        Args a(fn);
-        const kvq_cache_desc d = desc_of(p[0]);
+// What every attention call takes: (desc, q, k_cache, v_cache, k_scale | k_exp, v_scale | v_exp, block_table,
+// seq_lens) from p[0] on, and further on out and the workspace.
+struct Attention {
+    kvq_cache_desc d;
+    int32_t B, n, hq, maxp, out_type;
+    const void *q, *k, *v, *s0 = nullptr, *s1 = nullptr;
+    const int32_t *table, *seq;
+    void *out, *ws = nullptr;
+    size_t ws_bytes = 0;
+
+    Attention(Args &a, bool blocks, PyObject *const *p, PyObject *out_tensor, PyObject *workspace) : d(desc_of(p[0]))
+    {
         const at::Tensor &qt = a.tensor(p[1], "q");
         if (qt.dim() != 4)
             refuse(PyExc_ValueError, "q: expected [batch][query tokens][query heads][head_dim]");
-        const int64_t B = qt.size(0), n = qt.size(1), hq = qt.size(2);
-        if (B > INT32_MAX || n > INT32_MAX || hq > INT32_MAX)
+        const int64_t b64 = qt.size(0), n64 = qt.size(1), h64 = qt.size(2);
+        if (b64 > INT32_MAX || n64 > INT32_MAX || h64 > INT32_MAX)
             refuse(PyExc_ValueError, "q: too large");
-        a.expect(qt, "q", {ScalarType::BFloat16}, {B, n, hq, d.head_dim});
-        const void *q = a.at(qt, "q");
-        const void *k = take_cache(a, d, p[2], "k_cache"), *v = take_cache(a, d, p[3], "v_cache");
-        const void *s0 = nullptr, *s1 = nullptr;
+        a.expect(qt, "q", {ScalarType::BFloat16}, {b64, n64, h64, d.head_dim});
+        q = a.at(qt, "q");
+        k = take_cache(a, d, p[2], "k_cache");
+        v = take_cache(a, d, p[3], "v_cache");
         if (blocks) {
             s0 = take_exps(a, d, p[4], "k_exp");
             s1 = take_exps(a, d, p[5], "v_exp");
@@ -287,46 +294,101 @@ PyObject *decode_attn(const char *fn, bool blocks, PyObject *const *p, Py_ssize_
             s0 = a.take(p[4], "k_scale", {ScalarType::Float}, {d.num_kv_heads});
             s1 = a.take(p[5], "v_scale", {ScalarType::Float}, {d.num_kv_heads});
         }
-        const int32_t *table;
-        const auto [rows, maxp] = take_table(a, p[6], &table);
-        if (rows != B)
-            refuse(PyExc_ValueError, "block_table: expected " + std::to_string(B) + " rows, got " +
+        const auto [rows, entries] = take_table(a, p[6], &table);
+        if (rows != b64)
+            refuse(PyExc_ValueError, "block_table: expected " + std::to_string(b64) + " rows, got " +
                                          std::to_string(rows));
-        const auto *seq = static_cast<const int32_t *>(a.take(p[7], "seq_lens", {ScalarType::Int}, {B}));
-        const double scale = PyFloat_AsDouble(p[8]);
-        if (scale == -1.0 && PyErr_Occurred())
-            throw Refused();
-        const int32_t window = int_of(p[9], "window"), sinks = int_of(p[10], "num_sinks");
-        const auto *abort =
-            static_cast<const uint8_t *>(a.take_or_none(p[11], "abort_flags", {ScalarType::Byte}, {B}));
-        const at::Tensor &ot = a.tensor(p[12], "out");
-        a.expect(ot, "out", {ScalarType::BFloat16, ScalarType::Float}, {B, n, hq, d.head_dim});
-        void *out = a.at(ot, "out");
-        void *ws = nullptr;
-        size_t ws_bytes = 0;
-        if (p[13] != Py_None) {
-            const at::Tensor &wt = a.tensor(p[13], "workspace");
+        seq = static_cast<const int32_t *>(a.take(p[7], "seq_lens", {ScalarType::Int}, {b64}));
+        const at::Tensor &ot = a.tensor(out_tensor, "out");
+        a.expect(ot, "out", {ScalarType::BFloat16, ScalarType::Float}, {b64, n64, h64, d.head_dim});
+        out = a.at(ot, "out");
+        if (workspace != Py_None) {
+            const at::Tensor &wt = a.tensor(workspace, "workspace");
             ws = a.at(wt, "workspace");
             ws_bytes = static_cast<size_t>(wt.numel()) * wt.element_size();
         }
+        out_type = ot.scalar_type() == ScalarType::Float ? KVQ_OUT_FP32 : KVQ_OUT_BF16;
+        B = static_cast<int32_t>(b64);
+        n = static_cast<int32_t>(n64);
+        hq = static_cast<int32_t>(h64);
+        maxp = entries;
+    }
+    const float *scale(const void *s) const { return static_cast<const float *>(s); }
+    const int8_t *exps(const void *s) const { return static_cast<const int8_t *>(s); }
+};
+
+float float_of(PyObject *o)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred())
+        throw Refused();
+    return static_cast<float>(v);
+}
+
+const uint8_t *take_flags(Args &a, PyObject *o, int32_t B)
+{
+    return static_cast<const uint8_t *>(a.take_or_none(o, "abort_flags", {ScalarType::Byte}, {B}));
+}
+
+// (desc, q, k_cache, v_cache, k_scale | k_exp, v_scale | v_exp, block_table,
+//  seq_lens, softmax_scale, window, num_sinks, abort_flags, out, workspace, num_splits, stream)
+PyObject *decode_attn(const char *fn, bool blocks, PyObject *const *p, Py_ssize_t nargs)
+{
+    return entry(fn, nargs, 16, [&]() -> PyObject * {
+        Args a(fn);
+        const Attention t(a, blocks, p, p[12], p[13]);
+        const float scale = float_of(p[8]);
+        const int32_t window = int_of(p[9], "window"), sinks = int_of(p[10], "num_sinks");
+        const uint8_t *abort = take_flags(a, p[11], t.B);
         const int32_t splits = int_of(p[14], "num_splits");
         const int dev = a.device();
         const kvq_stream_t stream = a.stream(p[15]);
-        const int32_t type = ot.scalar_type() == ScalarType::Float ? KVQ_OUT_FP32 : KVQ_OUT_BF16;
-        const int32_t b32 = static_cast<int32_t>(B), n32 = static_cast<int32_t>(n), h32 = static_cast<int32_t>(hq);
-        const int32_t entries = maxp;
         return launch(dev, [&] {
             if (blocks)
-                return api.decode_attn_blocks(&d, q, b32, n32, h32, k, v, static_cast<const int8_t *>(s0),
-                                              static_cast<const int8_t *>(s1), table, entries, seq,
-                                              static_cast<float>(scale), window, sinks, abort, out, type, ws, ws_bytes,
-                                              splits, stream);
-            return api.decode_attn_window(&d, q, b32, n32, h32, k, v, static_cast<const float *>(s0),
-                                          static_cast<const float *>(s1), table, entries, seq,
-                                          static_cast<float>(scale), window, sinks, abort, out, type, ws, ws_bytes,
-                                          splits, stream);
+                return api.decode_attn_blocks(&t.d, t.q, t.B, t.n, t.hq, t.k, t.v, t.exps(t.s0), t.exps(t.s1), t.table,
+                                              t.maxp, t.seq, scale, window, sinks, abort, t.out, t.out_type, t.ws,
+                                              t.ws_bytes, splits, stream);
+            return api.decode_attn_window(&t.d, t.q, t.B, t.n, t.hq, t.k, t.v, t.scale(t.s0), t.scale(t.s1), t.table,
+                                          t.maxp, t.seq, scale, window, sinks, abort, t.out, t.out_type, t.ws,
+                                          t.ws_bytes, splits, stream);
         });
     });
+}
+
+// (desc, q, k_cache, v_cache, k_scale | k_exp, v_scale | v_exp, block_table,
+//  seq_lens, prefix_of, prefix_lens, softmax_scale, abort_flags, out, workspace, stream)
+PyObject *attn_prefix(const char *fn, bool blocks, PyObject *const *p, Py_ssize_t nargs)
+{
+    return entry(fn, nargs, 15, [&]() -> PyObject * {
+        Args a(fn);
+        const Attention t(a, blocks, p, p[12], p[13]);
+        const auto ints = [&](PyObject *o, const char *name) {
+            return static_cast<const int32_t *>(a.take(o, name, {ScalarType::Int}, {t.B}));
+        };
+        const int32_t *of = ints(p[8], "prefix_of"), *lens = ints(p[9], "prefix_lens");
+        const float scale = float_of(p[10]);
+        const uint8_t *abort = take_flags(a, p[11], t.B);
+        const int dev = a.device();
+        const kvq_stream_t stream = a.stream(p[14]);
+        return launch(dev, [&] {
+            if (blocks)
+                return api.attn_prefix_blocks(&t.d, t.q, t.B, t.n, t.hq, t.k, t.v, t.exps(t.s0), t.exps(t.s1), t.table,
+                                              t.maxp, t.seq, of, lens, scale, abort, t.out, t.out_type, t.ws,
+                                              t.ws_bytes, stream);
+            return api.attn_prefix(&t.d, t.q, t.B, t.n, t.hq, t.k, t.v, t.scale(t.s0), t.scale(t.s1), t.table, t.maxp,
+                                   t.seq, of, lens, scale, abort, t.out, t.out_type, t.ws, t.ws_bytes, stream);
+        });
+    });
+}
+
+PyObject *py_attn_prefix(PyObject *, PyObject *const *p, Py_ssize_t n)
+{
+    return attn_prefix("kvq_decode_attn_prefix", false, p, n);
+}
+
+PyObject *py_attn_prefix_blocks(PyObject *, PyObject *const *p, Py_ssize_t n)
+{
+    return attn_prefix("kvq_decode_attn_prefix_blocks", true, p, n);
 }
 
 PyObject *py_decode_attn_window(PyObject *, PyObject *const *p, Py_ssize_t n)
@@ -544,7 +606,7 @@ PyObject *py_trim_tables(PyObject *, PyObject *const *p, Py_ssize_t nargs)
 // bind(addresses): the entry points of the loaded library, in the order of Api.
 PyObject *py_bind(PyObject *, PyObject *const *p, Py_ssize_t nargs)
 {
-    constexpr int kEntries = 8;
+    constexpr int kEntries = 10;
     return entry("bind", nargs, kEntries, [&]() -> PyObject * {
         void *f[kEntries];
         for (int i = 0; i < kEntries; ++i) {
@@ -563,6 +625,8 @@ PyObject *py_bind(PyObject *, PyObject *const *p, Py_ssize_t nargs)
         api.extend_tables = reinterpret_cast<decltype(api.extend_tables)>(f[5]);
         api.fork_tables = reinterpret_cast<decltype(api.fork_tables)>(f[6]);
         api.trim_tables = reinterpret_cast<decltype(api.trim_tables)>(f[7]);
+        api.attn_prefix = reinterpret_cast<decltype(api.attn_prefix)>(f[8]);
+        api.attn_prefix_blocks = reinterpret_cast<decltype(api.attn_prefix_blocks)>(f[9]);
         Py_RETURN_NONE;
     });
 }
@@ -583,6 +647,8 @@ PyMethodDef methods[] = {method("bind", py_bind),
                          method("extend_tables", py_extend_tables),
                          method("fork_tables", py_fork_tables),
                          method("trim_tables", py_trim_tables),
+                         method("attn_prefix", py_attn_prefix),
+                         method("attn_prefix_blocks", py_attn_prefix_blocks),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kvq_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -2,9 +2,11 @@
 // cache, split along the context, with the log-sum-exp combine of the splits
 // fused into the same launch (the builds without a window always, the others
 // where that is faster).  What works off one split stands in
-// kvq_decode_split_body.cuh.  Compiled three times: kvq_decode.cu (per-head
+// kvq_decode_split_body.cuh.  Compiled five times: kvq_decode.cu (per-head
 // scales, every token), kvq_decode_window.cu (the same caches behind a sliding
-// window with sinks) and kvq_decode_blocks.cu (the block-scaled cache).
+// window with sinks), kvq_decode_blocks.cu (the block-scaled cache), and, with
+// KVQ_OWN_ROWS, kvq_decode_own.cu and kvq_decode_own_blocks.cu (either cache
+// past the pages that requests share: kSharing below).
 //
 // What it computes (blog post "Smaller, faster, safer: running Kimi and GLM
 // at scale", page-1 mirror section "量化KV缓存"; page-3 mirror section
@@ -65,6 +67,7 @@
 #include <cuda_bf16.h>
 
 #include "kvq_internal.h"
+#include "kvq_prefix.cuh"
 #include "kvq_ptx.cuh"
 #include "kvq_rowops.cuh"
 #include "kvq_view.cuh"
@@ -73,8 +76,19 @@ namespace kvq {
 
 namespace {
 
+// Builds behind shared pages (kvq_prefix.cu attends to those): a request shows
+// what its own row holds past them, as a context with the shared pages for a
+// hole; balanced launches only; every split goes to the workspace, one of a
+// request's only split among them, and launch_combine_prefix joins them.
+#ifdef KVQ_OWN_ROWS
+constexpr bool kSharing = true;
+using CallArgs = PrefixArgs;
+#else
+constexpr bool kSharing = false;
+using CallArgs = ViewArgs;
+#endif
 template <bool kWindow>
-using ArgsOf = std::conditional_t<kWindow, ViewArgs, DecodeArgs>;
+using ArgsOf = std::conditional_t<kWindow, CallArgs, DecodeArgs>;
 
 // Sticky device error word of this build of the kernel.  Bit 0: a bulk-copy
 // wait timed out.  Bit 1: the drain that follows also gave up, so a copy may
@@ -532,7 +546,7 @@ template <bool kMulti, bool kNanFlows>
 __device__ void drop_split(const ArgsOf<kNanFlows> &a, const Rows<kMulti, kNanFlows> &R, int split, int nsplit, float *smem,
                            uint32_t lse_bits = kLseInvalid)
 {
-    if (nsplit == 1) {
+    if (!kSharing && nsplit == 1) {
         for (int i = threadIdx.x; i < R.nrows * kHeadDim; i += kThreads)
             store_out(a.out, R.out_row(a, i / kHeadDim) * kHeadDim + i % kHeadDim, 0.f, a.out_fp32);
         if (a.expected_tags != nullptr)
@@ -659,6 +673,7 @@ __device__ bool cluster_finish(const DecodeArgs &a, const Rows<kMulti, kNanFlows
 struct Job {
     int b, kvh, rb, split, nsplit, span;
     int64_t t0, base, real;                  // real: the request's tokens, or -1 (read them)
+    int shared;                              // kSharing: those of them that are not its own row's
 };
 
 // Launched as a programmatic dependent of the previous kernel on the
@@ -687,11 +702,11 @@ __device__ __forceinline__ void run_split(const CUtensorMap &k_map, const CUtens
 
 // Units (of 1 << unit_shift tokens) that a call shows of a request of `real`
 // tokens; 0 if its outputs are zeros.
-__device__ __forceinline__ int shown_units(const ViewArgs &a, int64_t real, bool aborted, int ps_shift)
+__device__ __forceinline__ int shown_units(const CallArgs &a, int64_t real, bool aborted, int shared, int ps_shift)
 {
     if (aborted || real <= 0 || real > static_cast<int64_t>(a.max_pages_per_seq) << ps_shift)
         return 0;
-    return static_cast<int>((shown_context(a, real, ps_shift).len + (1 << a.unit_shift) - 1) >> a.unit_shift);
+    return static_cast<int>((own_context(a, real, shared, ps_shift).len + (1 << a.unit_shift) - 1) >> a.unit_shift);
 }
 
 // A balanced launch.  The host knows neither the lengths nor, with a table
@@ -721,20 +736,22 @@ struct Share {
     int acc, u;                              // places before request r, places of each of its pairs
     int r;
     int64_t real;                            // tokens of request r
+    int shared;                              // kSharing: those not its own row's
     Job job;                                 // the split at x
 
     // Places of each pair of request r.
-    __device__ __forceinline__ int places(const ViewArgs &a, int r, int ps_shift, int64_t &real) const
+    __device__ __forceinline__ int places(const CallArgs &a, int r, int ps_shift, int64_t &real, int &shared) const
     {
         real = __ldcg(a.seq_lens + r);
         const bool aborted = a.abort_flags != nullptr && __ldcg(a.abort_flags + r) != 0;
-        const int n = shown_units(a, real, aborted, ps_shift);
+        shared = shared_tokens(a, r, ps_shift);
+        const int n = shown_units(a, real, aborted, shared, ps_shift);
         return n > 0 ? n + a.pair_cost : 0;
     }
 
     // False if the CTA has none.  Also writes the zeros of the requests that
     // show nothing, one CTA each.  Called by the whole block.
-    __device__ __forceinline__ bool find(const ViewArgs &a, int ps_shift)
+    __device__ __forceinline__ bool find(const CallArgs &a, int ps_shift)
     {
         __shared__ int s_sum[kWarps];
         __shared__ bool s_some;
@@ -744,9 +761,10 @@ struct Share {
         const int m = (a.batch + kThreads - 1) / kThreads;
         const int r0 = min(a.batch, static_cast<int>(threadIdx.x) * m), r1 = min(a.batch, r0 + m);
         int64_t real = 0;
+        int shared = 0;
         int mine = 0, first = 0;
         for (int i = r0; i < r1; ++i) {
-            const int n = places(a, i, ps_shift, real);
+            const int n = places(a, i, ps_shift, real, shared);
             first = i == r0 ? n : first;
             mine += n;
         }
@@ -767,9 +785,10 @@ struct Share {
             before += w < warp ? s_sum[w] : 0;
             total += s_sum[w];
         }
-        for (int64_t i = blockIdx.x; i < a.batch; i += gridDim.x) {
+        for (int64_t i = blockIdx.x; !kSharing && i < a.batch; i += gridDim.x) {
             int64_t unused;
-            if (places(a, static_cast<int>(i), ps_shift, unused) == 0) {
+            int unshared;
+            if (places(a, static_cast<int>(i), ps_shift, unused, unshared) == 0) {
                 const int64_t n = static_cast<int64_t>(a.n_query) * a.num_q_heads * kHeadDim;
                 for (int64_t j = threadIdx.x; j < n; j += kThreads)
                     store_out(a.out, i * n + j, 0.f, a.out_fp32);
@@ -784,9 +803,10 @@ struct Share {
         if (static_cast<int64_t>(blockIdx.x) * share < all && x >= before * lines && x < (before + mine) * lines) {
             int sum = before, n = first, i = r0;
             if (m > 1)
-                for (n = places(a, i, ps_shift, real); x >= (sum + n) * lines; n = places(a, ++i, ps_shift, real))
+                for (n = places(a, i, ps_shift, real, shared); x >= (sum + n) * lines;
+                     n = places(a, ++i, ps_shift, real, shared))
                     sum += n;
-            *this = {lines, share, x, end, sum, n, i, real, {}};
+            *this = {lines, share, x, end, sum, n, i, real, shared, {}};
             s_some = set_job(a);
         }
         __syncthreads();
@@ -795,7 +815,7 @@ struct Share {
 
     // The split at x; moves x to the share's next pair.  False if the share
     // ends in the empty places in front of the pair's units.
-    __device__ __forceinline__ bool set_job(const ViewArgs &a)
+    __device__ __forceinline__ bool set_job(const CallArgs &a)
     {
         const int line = (x - acc * lines) / u, start = acc * lines + line * u + a.pair_cost;
         const int from = max(x, start), to = min(end, start - a.pair_cost + u);
@@ -812,13 +832,14 @@ struct Share {
         job.span = (to - from) << a.unit_shift;
         job.base = c0 + static_cast<int64_t>(r) * lines + line;
         job.real = real;
+        job.shared = shared;
         if (a.ws_pairs != nullptr && job.split == 0)       // for the combine
             a.ws_pairs[static_cast<int64_t>(r) * lines + line] = make_int2(static_cast<int>(job.base), job.nsplit);
         return true;
     }
 
     // On to the next job, by the whole block; false at the end of the share.
-    __device__ __forceinline__ bool next(const ViewArgs &a, int ps_shift)
+    __device__ __forceinline__ bool next(const CallArgs &a, int ps_shift)
     {
         __shared__ bool s_more;
         // the next split's copies overwrite what this one's merge read
@@ -830,7 +851,7 @@ struct Share {
         return s_more;
     }
 
-    __device__ __forceinline__ bool advance(const ViewArgs &a, int ps_shift)
+    __device__ __forceinline__ bool advance(const CallArgs &a, int ps_shift)
     {
         if (x >= end)
             return false;
@@ -839,7 +860,7 @@ struct Share {
             do {
                 if (++r >= a.batch)
                     return false;                          // only if the lengths changed meanwhile
-                u = places(a, r, ps_shift, real);
+                u = places(a, r, ps_shift, real, shared);
             } while (u == 0);
         }
         return set_job(a);
@@ -868,6 +889,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
         job.span = a.split_tokens;
         job.t0 = static_cast<int64_t>(job.split) * a.split_tokens;
         job.base = job.real = -1;
+        job.shared = 0;
         if constexpr (kWindow && !kCluster) {
             const bool balanced = a.resident_ctas > 0;
             const int ps_shift = __ffs(a.page_size) - 1;

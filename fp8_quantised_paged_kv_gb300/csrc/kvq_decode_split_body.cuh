@@ -100,7 +100,7 @@
     int32_t ids[kIdsPerThread];
     bool every = true;                                     // no window
     if constexpr (kWindow)
-        every = a.window == 0;
+        every = !kSharing && a.window == 0;
     if (every) {
 #pragma unroll
         for (int k = 0; k < kIdsPerThread; ++k) {
@@ -127,8 +127,8 @@
     int64_t len = real_len;
     [[maybe_unused]] int64_t win0 = 0;                     // where the first query's window starts
     if constexpr (kWindow) {
-        if (a.window > 0) {
-            const Shown shown = shown_context(a, real_len, ps_shift);
+        if (kSharing || a.window > 0) {
+            const Shown shown = own_context(a, real_len, job.shared, ps_shift);
             len = shown.len;
             win0 = shown.win0;
             // only entries of pages with a token of the shortened context are read
@@ -975,7 +975,7 @@
                 *reinterpret_cast<float4 *>(part + kRowsT + h * kHeadDim + d) = acc;
                 if (lane == 0)
                     part[h] = sm_t[kRowsT + h];
-            } else if (nsplit == 1) {
+            } else if (!kSharing && nsplit == 1) {
                 store_out4(a.out, R.ids[h] * kHeadDim + d, acc, a.out_fp32);
             } else {
                 const int64_t at = R.part(a, h, split);

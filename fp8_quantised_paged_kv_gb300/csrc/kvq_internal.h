@@ -216,6 +216,36 @@ struct ViewArgs : DecodeArgs {
     bool combine_apart;              // launch_combine_rows combines the splits
 };
 
+// What a call over shared prefixes takes beside it.
+struct PrefixArgs : ViewArgs {
+    const int32_t *prefix_of, *prefix_lens;  // [B]
+    // partials of the shared pages (kvq_prefix.cu)
+    float *pre_lse;                          // a place per (CTA, row)
+    float4 *pre_o;                           // 32 of each place
+    int4 *pre_rec;                           // [B][n][Hq]: first place, parts, the tile's rows, the row among them
+    int32_t pre_ctas;
+};
+constexpr int kPrefixRows = 256;     // most rows of a CTA's job over shared pages
+// Over the shared pages (box heights of k_map and v_map: prefix_box_tokens),
+// over the requests' own pages past them, and the parts of both joined.
+cudaError_t launch_prefix_rows(const PrefixArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                               cudaStream_t stream);
+cudaError_t launch_decode_own(const PrefixArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                              cudaStream_t stream);
+cudaError_t launch_decode_own_blocks(const PrefixArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                                     cudaStream_t stream);
+cudaError_t launch_combine_prefix(const PrefixArgs &a, cudaStream_t stream);
+cudaError_t read_prefix_error(uint32_t *bits, bool clear);
+cudaError_t read_own_error(uint32_t *bits, bool clear);
+cudaError_t read_own_blocks_error(uint32_t *bits, bool clear);
+// Tokens of a copy of the shared pages.  A bf16 cache is read through a map of
+// [rows][128] values, 64 of a row at a time.
+inline int prefix_box_tokens(int page_size, bool bf16_cache, bool out_fp32)
+{
+    const int most = !bf16_cache ? kChunkTokens : out_fp32 ? 64 : 128;
+    return page_size < most ? page_size : most;
+}
+
 // Default limit of a wait on a bulk copy in the decode kernel: about one
 // second.  The drain that follows a timeout always waits this long.
 constexpr uint64_t kCopyWaitLimitNs = 1000000000ull;

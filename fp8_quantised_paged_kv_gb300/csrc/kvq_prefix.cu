@@ -1,0 +1,1166 @@
+// kvq_prefix.cu -- attention over pages that several requests share, once for
+// all of them, on the 5th-generation tensor cores.
+//
+// Consecutive requests whose shared tokens come from one row of the table (a
+// run) put the query rows of a KV head together: m requests of n tokens and g
+// heads are m n g rows over the same K and V, and
+//   s = q K^T,  o = sum_j 2^(s_j - M) V_j / l,  l = sum_j 2^(s_j - M)
+// (scores in log2 units, M a running maximum) is a product of matrices again.
+// What each request's own pages add, kvq_decode_own.cu computes;
+// combine_prefix_kernel below joins the parts by their log-sum-exps.
+//
+// A CTA takes up to 256 rows, two tiles of 128, through a range of the run's
+// pages, 128 tokens (64 with the widest P) at a time.  Its warps have one job
+// each: copies by TMA; over an FP8 cache the conversion of K and V to f16 (once
+// for all rows); per row tile a thread that issues S = Q K^T and O += P V, and
+// a softmax group of four warps, a row per thread, which reads S from tensor
+// memory, and writes P over it.  One tile's exponentials run beside the other's
+// products.  With up to 128 rows both groups serve the same rows on alternate
+// token tiles, and their results are two parts.  Tensor memory is full: two S
+// of 128 columns and two accumulators of 128; so Q is read from shared memory.
+//
+// Block scales mean what they mean in kvq_decode_split.cuh: ek on the scores,
+// ev in the exponent with 2^-ev undone in l.  Over an FP8 cache P is kept 2^7
+// larger, so that f16 cuts weights at 2^-32 of the largest; the maximum may lag
+// by 2^8 before O is rescaled.  Over a bf16 cache P is bf16 and kept 2^-8 times
+// as large, at most 1, so that large values do not overflow sums.
+//
+// How the work is shared out is decided on the device, as in
+// kvq_decode_split.cuh: one line of places, run after run, KV head after KV
+// head, row pair after row pair; CTA c takes an equal stretch of it.
+#include "kvq_decode_umma.cuh"
+#include "kvq_prefix.cuh"
+
+namespace kvq {
+namespace {
+
+enum CacheKind { kFp8, kBlocksFp8, kBf16 };
+
+// The most that differs between the builds.
+template <int kKind, bool kPrecise>
+struct Build {
+    static constexpr bool kConvert = kKind != kBf16, kBlocks = kKind == kBlocksFp8;
+    // 16-bit terms of a weight: one for bf16 output; for fp32 output two of
+    // f16 (2^-22) or three of bf16 (2^-24)
+    static constexpr int kTerms = !kPrecise ? 1 : kConvert ? 2 : 3;
+    // tokens of a tile: P's terms have to fit in the 128 columns of S
+    static constexpr int kTok = kTerms == 3 ? 64 : 128;
+    static constexpr int kHalfBytes = kTok * 256;          // K or V of a tile, 16-bit
+    static constexpr int kSliceBytes = kTok * 128;         // 64 dims of it
+    static constexpr int kConv = 8;                        // first of four converting warps
+    static constexpr int kCopy = kConvert ? 12 : 8;        // the copying warp
+    static constexpr int kIssue = kCopy + 1;               // two issuing warps, one per group
+    static constexpr int kThreads = 32 * (kIssue + 2);
+    static constexpr float kLift = kConvert ? 7.f : -8.f;  // log2 of what P, l and O are larger by
+};
+
+constexpr int kBufs = 4;                                   // K and V of two tiles
+constexpr int kQBytes = 128 * 256;                         // 128 rows as 16-bit values
+constexpr int kStageTok = 64;                              // of a stage of the e4m3 ring (K rows, or V rows)
+constexpr int kRingStage = kStageTok * 128;
+// Two row tiles' Q leave room for three stages; with one tile the ring has
+// the place of the second Q as well.
+constexpr int kWideStages = 3, kNarrowStages = 7;
+constexpr int kOffQ = 0, kOffQ2 = kQBytes;
+constexpr int kOffRingNarrow = kOffQ2, kOffRingWide = kOffQ2 + kQBytes;
+constexpr int kOffBufs = kOffRingWide + kWideStages * kRingStage;
+static_assert(kOffRingNarrow + kNarrowStages * kRingStage == kOffBufs, "the narrow ring ends where the buffers start");
+constexpr int kData = kOffBufs + kBufs * 128 * 256;
+
+constexpr int kBlockReq = 128;                             // a run does not cross a multiple of it
+constexpr int kMaxBlocks = 512;                            // of up to 65,535 requests
+constexpr int kMinTiles = 2;                               // of a CTA's share, in wide tiles
+constexpr int kWideCost = 2, kNarrowCost = 1;              // places of a tile of tokens by the row tiles served
+constexpr int kBorderCost = 4;                             // and of a border between two jobs
+
+constexpr uint32_t kColS = 0, kColO = 256;                 // + 128 for the second group
+constexpr int kFlush = 16;                                 // fp32 output: tiles between O's ways out of tensor memory
+
+// Column, from S's first, of term t of P for tokens 32 c .. 32 c + 31 of a tile.
+// P is written 32 tokens after 32, over scores that have been read.
+template <int kTerms>
+__device__ __forceinline__ uint32_t p_column(int c, int t)
+{
+    if constexpr (kTerms < 3)
+        return 32u * c + 16u * t;
+    else                                                   // 64 tokens: S has columns 0 .. 63
+        return c == 0 ? 64u + 16u * t : t < 2 ? 16u * t : 112u;
+}
+
+struct Run {
+    int first, count, tiles;                               // requests, and tiles of the longest shared part
+    int len;                                               // its tokens
+    int64_t start;                                         // first place
+};
+
+struct Bars {
+    uint64_t wide_landed[kWideStages], wide_empty[kWideStages];
+    uint64_t narrow_landed[kNarrowStages], narrow_empty[kNarrowStages];
+    uint64_t full[kBufs], free[kBufs];                     // K and V buffers (kBf16: full when the copies landed)
+    uint64_t s_full[2], p_full[2], o_done[2], drain[2];
+};
+
+// A CTA's stretch of the line and where it is on it.
+struct Walk {
+    int64_t share, x, end, block_start;                    // block_start: first place of the block in s.runs
+    int64_t total, block_total;
+    int block, n_runs;
+    // the job at hand: rows [row0, row0 + rows) of run (first, count), tokens [t0, t1)
+    int first, lead, kvh, row0, rows, len, tile0, tile1;
+    int run_rows, c0, nsplit;                              // rows of the run's KV head; first CTA of the job, and CTAs
+    bool wide;
+};
+
+struct Shared {
+    Bars bars;
+    uint32_t tmem_slot;
+    int abort, bad_from;                                   // bad_from: first token whose page is out of range
+    int state;                                             // of the search for the next job
+    Walk w;
+    Run runs[kBlockReq];
+    int len[kBlockReq];                                    // shared tokens of each request of the block
+    int64_t part[16];
+};
+static_assert(kData + 1024 + sizeof(Shared) <= 232448, "one CTA fits an SM");
+
+// Scratch of the search, in Q's place.
+struct Scratch {
+    int lead[3][kBlockReq], len[3][kBlockReq], most[3][kBlockReq];
+    uint32_t cont[3][4];
+    int64_t warp_sum[3][4];
+    int64_t total[kMaxBlocks];
+};
+static_assert(sizeof(Scratch) <= kQBytes, "the scratch fits in Q's place");
+
+// Instruction descriptor of kind::f16, 128 x n, fp32 accumulator.
+template <bool kBf>
+__host__ __device__ constexpr uint32_t idesc(int n, bool b_mn)
+{
+    return umma_idesc_f16(128, n, b_mn) | (kBf ? (1u << 7) | (1u << 10) : 0u);
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// The row's O, out of tensor memory onto its sums (from zero, the first time).
+__device__ __forceinline__ void flush_sums(uint32_t ocol, float4 *part, int rows, bool valid, bool onto, float mul)
+{
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+        uint32_t o[16];
+        tmem_ld16(ocol + 16u * c, o);
+        if (valid)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float4 *at = part + (4 * c + k) * rows;
+                const float4 u = onto ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
+                *at = make_float4(fmaf(u.x, mul, __uint_as_float(o[4 * k])), fmaf(u.y, mul, __uint_as_float(o[4 * k + 1])),
+                                  fmaf(u.z, mul, __uint_as_float(o[4 * k + 2])),
+                                  fmaf(u.w, mul, __uint_as_float(o[4 * k + 3])));
+            }
+    }
+}
+
+// Place of a request's run on the line, worked out by the 128 threads of a team
+// (called by the whole CTA; block < 0: nothing to do).  total: its places.
+// list: also the runs themselves and every request's shared tokens, for team 0.
+template <int kTok>
+__device__ __forceinline__ void find_runs(const PrefixArgs &a, Shared &s, Scratch &c, int team, int block, int ps_shift,
+                                          bool list)
+{
+    const int i = threadIdx.x & 127, lane = threadIdx.x & 31, quarter = i >> 5;
+    const bool mine = team < 3 && block >= 0;
+    const int r = block * kBlockReq + i;
+    int lead = -1, len = 0;
+    if (mine && r < a.batch) {
+        len = shared_tokens(a, r, ps_shift);
+        lead = len > 0 ? __ldcg(a.prefix_of + r) : -1;
+    }
+    if (mine) {
+        c.lead[team][i] = lead;
+        c.len[team][i] = len;
+        c.most[team][i] = 0;
+    }
+    __syncthreads();
+    // whether request i goes on with the run of request i - 1
+    const bool goes_on = mine && i > 0 && len > 0 && c.lead[team][i - 1] == lead;
+    if (mine) {
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, goes_on);
+        if (lane == 0)
+            c.cont[team][quarter] = m;
+    }
+    __syncthreads();
+    int head = i, next = kBlockReq;
+    if (mine) {
+        // the nearest request at or before i that starts a run or holds nothing
+        for (int k = quarter; k >= 0; --k) {
+            uint32_t z = ~c.cont[team][k];
+            if (k == quarter)
+                z &= 0xFFFFFFFFu >> (31 - lane);
+            if (z != 0) {
+                head = 32 * k + 31 - __clz(z);
+                break;
+            }
+        }
+        // and the nearest after i
+        for (int k = quarter; k < 4; ++k) {
+            uint32_t z = ~c.cont[team][k];
+            if (k == quarter)
+                z &= lane == 31 ? 0u : 0xFFFFFFFFu << (lane + 1);
+            if (z != 0) {
+                next = 32 * k + __ffs(z) - 1;
+                break;
+            }
+        }
+        if (len > 0)
+            atomicMax(&c.most[team][head], len);
+    }
+    __syncthreads();
+    const bool starts = mine && len > 0 && !goes_on;
+    int64_t places = 0;
+    Run run = {};
+    if (starts) {
+        run.first = r;
+        run.count = next - i;
+        run.len = c.most[team][i];
+        run.tiles = (run.len + kTok - 1) / kTok;
+        const int rows = run.count * a.n_query * a.group, row_tiles = (rows + 127) / 128;
+        places = static_cast<int64_t>(row_tiles / 2) * (kBorderCost + static_cast<int64_t>(kWideCost) * run.tiles) +
+                 (row_tiles & 1) * (kBorderCost + static_cast<int64_t>(kNarrowCost) * run.tiles);
+        places *= a.num_kv_heads;
+    }
+    int64_t upto = places;
+    if (mine) {
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+            upto += lane >= off ? o : 0;
+        }
+        if (lane == 31)
+            c.warp_sum[team][quarter] = upto;
+    }
+    __syncthreads();
+    if (mine) {
+        int64_t before = 0, all = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            before += k < quarter ? c.warp_sum[team][k] : 0;
+            all += c.warp_sum[team][k];
+        }
+        if (i == 0)
+            c.total[block] = all;
+        if (list) {
+            // its number among the block's runs: starts before i, counted by warp
+            const uint32_t heads = __ballot_sync(0xFFFFFFFFu, starts);
+            if (lane == 0)
+                s.part[quarter] = __popc(heads);
+            named_barrier_sync(2, 128);
+            int n = __popc(heads & ((1u << lane) - 1u)), of = 0;
+            for (int k = 0; k < 4; ++k) {
+                n += k < quarter ? static_cast<int>(s.part[k]) : 0;
+                of += static_cast<int>(s.part[k]);
+            }
+            run.start = before + upto - places;
+            if (starts)
+                s.runs[n] = run;
+            s.len[i] = len;
+            if (i == 0) {
+                s.w.n_runs = of;
+                s.w.block = block;
+                s.w.block_total = all;
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// The job at place x of the line, by one thread; moves x past what this CTA does
+// of it.  False if that is nothing (x lies in the border).
+__device__ __forceinline__ bool set_job(const PrefixArgs &a, Shared &s)
+{
+    Walk &w = s.w;
+    int k = 0;
+    // the run that holds x (places of the block before a run's start are the run before's)
+    const int64_t at = w.x - w.block_start;
+    int hi = w.n_runs - 1;
+    while (k < hi) {
+        const int mid = (k + hi + 1) / 2;
+        if (s.runs[mid].start <= at)
+            k = mid;
+        else
+            hi = mid - 1;
+    }
+    const Run run = s.runs[k];
+    const int all_rows = run.count * a.n_query * a.group, row_tiles = (all_rows + 127) / 128;
+    const int64_t wide = kBorderCost + static_cast<int64_t>(kWideCost) * run.tiles;
+    const int64_t narrow = kBorderCost + static_cast<int64_t>(kNarrowCost) * run.tiles;
+    const int64_t per_head = row_tiles / 2 * wide + (row_tiles & 1) * narrow;
+    const int64_t in_run = at - run.start;
+    const int kvh = static_cast<int>(in_run / per_head);
+    const int64_t in_head = in_run - kvh * per_head;
+    const int pair = static_cast<int>(min(in_head / wide, static_cast<int64_t>(row_tiles / 2)));
+    w.wide = pair < row_tiles / 2;
+    const int cost = w.wide ? kWideCost : kNarrowCost;
+    // places [job, job + size) of the line; tiles from `start` on
+    const int64_t job = w.block_start + run.start + kvh * per_head + pair * wide, size = w.wide ? wide : narrow;
+    const int64_t start = job + kBorderCost;
+    const int64_t from = max(w.x - start, static_cast<int64_t>(0)), to = min(w.end - start, size - kBorderCost);
+    w.x = min(w.end, job + size);
+    // a tile is the CTA's in whose stretch its first place lies
+    w.tile0 = static_cast<int>((from + cost - 1) / cost);
+    w.tile1 = to <= 0 ? 0 : static_cast<int>((to + cost - 1) / cost);
+    if (w.tile0 >= w.tile1)
+        return false;
+    const int64_t c0 = start / w.share, c1 = (start + static_cast<int64_t>(run.tiles - 1) * cost) / w.share;
+    w.c0 = static_cast<int>(c0);
+    w.nsplit = static_cast<int>(c1 - c0) + 1;
+    w.run_rows = all_rows;
+    w.first = run.first;
+    w.kvh = kvh;
+    w.row0 = 256 * pair;
+    w.rows = min(all_rows - w.row0, w.wide ? 256 : 128);
+    w.len = run.len;
+    w.lead = __ldcg(a.prefix_of + run.first);
+    return true;
+}
+
+template <int kKind, bool kPrecise>
+__global__ void __launch_bounds__(Build<kKind, kPrecise>::kThreads, 1)
+prefix_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                   const PrefixArgs a)
+{
+    using B = Build<kKind, kPrecise>;
+    constexpr int kTok = B::kTok, kThreads = B::kThreads;
+    constexpr bool kBlocks = B::kBlocks;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    Shared &s = *reinterpret_cast<Shared *>(sm + kData);
+    Scratch &scratch = *reinterpret_cast<Scratch *>(sm + kOffQ);
+    Bars &bar = s.bars;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int ps_shift = __ffs(a.page_size) - 1;
+
+    if (tid == 0) {
+        prefetch_tensor_map(&k_map);
+        prefetch_tensor_map(&v_map);
+        for (int i = 0; i < kWideStages; ++i) {
+            mbar_init(&bar.wide_landed[i], 1);
+            mbar_init(&bar.wide_empty[i], 4);
+        }
+        for (int i = 0; i < kNarrowStages; ++i) {
+            mbar_init(&bar.narrow_landed[i], 1);
+            mbar_init(&bar.narrow_empty[i], 4);
+        }
+        for (int i = 0; i < kBufs; ++i) {
+            mbar_init(&bar.full[i], B::kConvert ? 4 : 1);
+            mbar_init(&bar.free[i], 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.p_full[i], 4);
+            mbar_init(&bar.o_done[i], 1);
+            mbar_init(&bar.drain[i], 1);
+        }
+        fence_mbar_init();
+        s.abort = 0;
+        s.bad_from = 0x7FFFFFFF;
+    }
+    grid_dependency_wait();
+
+    // ---------------------------------------------- this CTA's stretch of the line
+    const int n_blocks = (a.batch + kBlockReq - 1) / kBlockReq;
+    constexpr int kTeams = kThreads / 128 < 3 ? kThreads / 128 : 3;
+    for (int b0 = 0; b0 < n_blocks; b0 += kTeams) {
+        const int team = tid / 128;
+        find_runs<kTok>(a, s, scratch, team, team < kTeams && b0 + team < n_blocks ? b0 + team : -1, ps_shift, false);
+    }
+    if (tid == 0) {
+        Walk &w = s.w;
+        w.total = 0;
+        for (int b = 0; b < n_blocks; ++b)
+            w.total += scratch.total[b];
+        const int64_t even = (w.total + gridDim.x - 1) / gridDim.x;
+        w.share = max(even, static_cast<int64_t>(kMinTiles * kWideCost));
+        w.x = min(w.total, w.share * blockIdx.x);
+        w.end = min(w.total, w.x + w.share);
+        int b = 0;
+        int64_t start = 0;
+        if (w.x < w.end)
+            while (w.x >= start + scratch.total[b])
+                start += scratch.total[b++];
+        w.block = b;
+        w.block_start = start;
+    }
+    __syncthreads();
+    if (s.w.x >= s.w.end)
+        return;
+    if (warp == 0)
+        tmem_alloc(&s.tmem_slot, kTmemCols);
+    {
+        const int first = s.w.block;
+        __syncthreads();
+        find_runs<kTok>(a, s, scratch, tid / 128, tid < 128 ? first : -1, ps_shift, true);
+    }
+    tmem_fence_before_sync();
+    __syncthreads();
+    tmem_fence_after_sync();
+    const uint32_t tmem = s.tmem_slot;
+
+    // What went through the rings, buffers and barriers in the jobs before:
+    // stages of either ring, K and V items, tiles of this thread's group, jobs.
+    uint32_t wide_done = 0, narrow_done = 0, items_done = 0, group_done = 0, jobs_done = 0;
+    volatile int *abort_flag = &s.abort;
+
+    const int gr = warp < 8 ? warp >> 2 : warp - B::kIssue; // group of a softmax or an issuing warp
+    const int m = tid & 127;
+    const int hkv = a.num_kv_heads, per_request = a.n_query * a.group;
+    for (;;) {
+        // ---------------------------------------------- the next job
+        if (tid == 0) {
+            Walk &w = s.w;
+            s.state = w.x >= w.end ? 0 : w.x >= w.block_start + w.block_total ? 2 : set_job(a, s) ? 1 : 3;
+            s.bad_from = 0x7FFFFFFF;
+        }
+        __syncthreads();
+        const int state = s.state;
+        if (state == 0)
+            break;
+        if (state != 1) {
+            const int block = s.w.block + 1;
+            __syncthreads();                               // everyone has read the state
+            if (state == 2) {
+                if (tid == 0)
+                    s.w.block_start += s.w.block_total;
+                find_runs<kTok>(a, s, scratch, tid / 128, tid < 128 ? block : -1, ps_shift, true);
+            }
+            continue;
+        }
+        const Walk &w = s.w;
+        const bool wide = w.wide, failed_before = s.abort != 0;
+        const int tile0 = w.tile0, tile1 = w.tile1, kvh = w.kvh, first = w.first;
+        const int step = wide ? 1 : 2;
+        const int n_tiles = tile1 - tile0;
+        const int mine0 = wide ? 0 : gr, mine = (n_tiles - mine0 + step - 1) / step;   // the group's tiles
+        const int tile_rows = wide ? min(128, w.rows - 128 * gr) : w.rows;             // rows of the group's row tile
+        const int32_t *bt = a.block_table + static_cast<int64_t>(w.lead) * a.max_pages_per_seq;
+        // place of the group's part: the job's, behind one of the same number per CTA
+        const int64_t place0 =
+            2 * (static_cast<int64_t>(first) * per_request * hkv +
+                 static_cast<int64_t>(kvh) * w.run_rows + w.row0) +
+            gr * (wide ? 128 : w.rows);
+
+        // this thread's row (softmax groups)
+        const int local = wide ? 128 * gr + m : m;
+        const bool row_valid = warp < 8 && m < tile_rows;
+        int64_t id = 0;
+        int lim = 0x7FFFFFFF;                              // tokens the row sees (a slot without a row: no masks)
+        if (row_valid) {
+            const int at = w.row0 + local, req = at / per_request, in = at - req * per_request;
+            id = (static_cast<int64_t>(first + req) * a.n_query + in / a.group) * a.num_q_heads + kvh * a.group +
+                 in % a.group;
+            lim = s.len[first % kBlockReq + req];
+        }
+        float m_used = -INFINITY, l_sum = 0.f;
+        // fp32 output: this row's sums so far are in its place, behind m_used by sums_mul
+        [[maybe_unused]] float sums_mul = 1.f;
+        float4 *const part = a.pre_o + (256ll * blockIdx.x + place0) * 32 + m;
+        int issued = 0;                                    // copying warp: stages or items it issued in this job
+
+        if (!failed_before) {
+            if (warp < 8) {
+                // ------------------------------------------ Q, then softmax
+                const float kv_scale = B::kConvert && !kBlocks ? a.k_scale[kvh] : 1.f;
+                const float signed_mul = a.qk_scale_log2 * kv_scale;
+                uint32_t qw[64];
+                int e = 0;
+                {
+                    uint32_t mx = 0;
+                    if (row_valid) {
+                        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + id * kHeadDim);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const uint4 v = __ldcg(src + i);
+                            qw[4 * i] = v.x; qw[4 * i + 1] = v.y; qw[4 * i + 2] = v.z; qw[4 * i + 3] = v.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            qw[i] = 0u;
+                    }
+                    if constexpr (B::kConvert) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            mx = max(mx, max(qw[i] & 0x7FFFu, (qw[i] >> 16) & 0x7FFFu));
+                        e = q_row_exponent(mx);
+                    }
+                }
+                // the scores' multiplier is not negative: a negative one turns q
+                const float mul = fabsf(signed_mul) * __int_as_float((127 - e) << 23);
+                if (wide || gr == 0) {
+                    uint8_t *qs = sm + kOffQ + gr * kQBytes;
+                    const float q_mul = signed_mul < 0.f ? -__int_as_float((127 + e) << 23) : __int_as_float((127 + e) << 23);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if constexpr (B::kConvert) {
+                                const float2 f = bf16x2_to_f32x2(qw[4 * i + k]);
+                                h[k] = f32x2_to_f16x2(f.x * q_mul, f.y * q_mul);
+                            } else {
+                                h[k] = qw[4 * i + k] ^ (signed_mul < 0.f ? 0x80008000u : 0u);
+                            }
+                        }
+                        *reinterpret_cast<uint4 *>(qs + (i >> 3) * (kQBytes / 2) + sw128_chunk(m, i & 7)) =
+                            make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                    fence_proxy_async_smem();
+                }
+                named_barrier_sync(1, 320);                // the softmax and the issuing warps
+
+                const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+                const uint32_t scol = tmem + lanes + kColS + 128u * gr, ocol = tmem + lanes + kColO + 128u * gr;
+                // block-scaled: lane i has the exponents of the tile's block i,
+                // fetched a tile ahead (ek in the low byte, ev in the high one)
+                [[maybe_unused]] int exps = 0, exps_next = 0, page_next = -1;
+                const int blk = lane * kBlockTokens;
+                const auto page_at = [&](int tile) {
+                    const int tok = tile * kTok + blk;
+                    return lane < kTok / kBlockTokens && tile < tile1 && tok < w.len ? __ldcg(bt + (tok >> ps_shift)) : -1;
+                };
+                const auto exps_at = [&](int tile, int page) {
+                    if (page < 0 || page >= a.num_pages)
+                        return 0;
+                    const int64_t at = ((static_cast<int64_t>(page) * hkv + kvh) << (ps_shift - 4)) +
+                                       (((tile * kTok + blk) & (a.page_size - 1)) >> 4);
+                    const int ek = max(static_cast<int>(__ldcg(a.k_exp + at)), kReadKeyExpMin);
+                    const int ev = max(static_cast<int>(__ldcg(a.v_exp + at)), kReadValueExpMin);
+                    return (ek & 0xFF) | (min(ev, kReadValueExpMax) << 8);
+                };
+                if constexpr (kBlocks) {
+                    const int t = tile0 + mine0;
+                    exps_next = exps_at(t, page_at(t));
+                    page_next = page_at(t + step);
+                }
+                for (int i = 0; i < mine; ++i) {
+                    const int tile = tile0 + mine0 + i * step;
+                    if constexpr (kBlocks) {
+                        exps = exps_next;
+                        exps_next = exps_at(tile + step, page_next);
+                        page_next = page_at(tile + 2 * step);
+                    }
+                    if (!__all_sync(0xFFFFFFFFu, wait_or_abort(&bar.s_full[gr], (group_done + i) & 1, kCopyWaitLimitNs,
+                                                               abort_flag, 4u)))
+                        break;
+                    tmem_fence_after_sync();
+                    const int vis = lim - tile * kTok;     // columns below it are visible
+                    const bool all = __all_sync(0xFFFFFFFFu, vis >= kTok);
+                    // ev and the multiplier of block q (16 columns) of the tile
+                    const auto block = [&](int q, float &mk, float &ev) {
+                        mk = mul;
+                        ev = 0.f;
+                        if constexpr (kBlocks) {
+                            const int x = __shfl_sync(0xFFFFFFFFu, exps, q);
+                            mk = mul * __int_as_float((127 + static_cast<int8_t>(x & 0xFF)) << 23);
+                            ev = static_cast<float>(x >> 8);
+                        }
+                    };
+                    // ---- the tile's largest score
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < kTok / 32; ++c) {
+                        uint32_t sv[32];
+                        tmem_ld32(scol + 32u * c, sv);
+                        if (!all) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                sv[k] = 32 * c + k < vis ? sv[k] : 0xFF800000u;
+                        }
+                        float half[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2)
+                            half[k / 16] = fmaxf(half[k / 16], fmaxf(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])));
+                        if constexpr (kBlocks) {
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                float mk, ev;
+                                block(2 * c + q, mk, ev);
+                                if (half[q] != -INFINITY)
+                                    mx = fmaxf(mx, fmaf(half[q], mk, ev));
+                            }
+                        } else {
+                            mx = fmaxf(mx, fmaxf(half[0], half[1]));
+                        }
+                    }
+                    if constexpr (!kBlocks)
+                        mx = mx == -INFINITY ? mx : mx * mul;
+                    const bool raise = row_valid && mx > m_used + kRaiseThreshold;
+                    const float alpha = raise ? (m_used == -INFINITY ? 0.f : fast_exp2(m_used - mx)) : 1.f;
+                    // O += P V of the group's last tile was done before S of this one was issued.
+                    // fp32 output: O goes out of tensor memory every kFlush tiles
+                    // into fp32 sums that round (the tensor core cuts what it adds
+                    // to a large accumulator towards zero).
+                    const bool flush = kPrecise && i > 0 && i % kFlush == 0;
+                    const bool rescale = raise && m_used != -INFINITY && i > 0 && !flush;
+                    if constexpr (kPrecise) {
+                        if (flush) {
+                            flush_sums(ocol, part, tile_rows, row_valid, i > kFlush, sums_mul);
+                            sums_mul = 1.f;
+                        }
+                        if (raise)
+                            sums_mul *= alpha;
+                    }
+                    if (__any_sync(0xFFFFFFFFu, rescale)) {
+                        const float f = rescale ? alpha : 1.f;
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(ocol + 16u * c, o);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st16(ocol + 16u * c, o);
+                        }
+                    }
+                    if (raise) {
+                        l_sum *= alpha;
+                        m_used = mx;
+                    }
+                    // ---- P = 2^(s - m_used + kLift), written over S
+                    const float base = (m_used == -INFINITY ? 0.f : m_used) - B::kLift;
+                    float sum = 0.f;
+                    uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+                    for (int c = 0; c < kTok / 32; ++c) {
+                        uint32_t sv[32];
+                        tmem_ld32(scol + 32u * c, sv);
+                        float p[32];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            float mk, ev;
+                            block(2 * c + q, mk, ev);
+                            const uint64_t mk2 = f2_pack(mk, mk), off2 = f2_pack(ev - base, ev - base);
+#pragma unroll
+                            for (int k = 16 * q; k < 16 * q + 16; k += 2) {
+                                float x0, x1;
+                                f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), mk2, off2),
+                                          x0, x1);
+                                if (!all) {
+                                    x0 = 32 * c + k < vis ? x0 : -INFINITY;
+                                    x1 = 32 * c + k + 1 < vis ? x1 : -INFINITY;
+                                }
+                                p[k] = fast_exp2(x0);
+                                p[k + 1] = fast_exp2(x1);
+                                sum2[(k >> 1) & 1] = f2_add(sum2[(k >> 1) & 1], f2_pack(p[k], p[k + 1]));
+                            }
+                            if constexpr (kBlocks) {       // a block's weights, times 2^-ev
+                                float s0, s1, s2, s3;
+                                f2_unpack(sum2[0], s0, s1);
+                                f2_unpack(sum2[1], s2, s3);
+                                sum = fmaf((s0 + s1) + (s2 + s3), __int_as_float((127 - static_cast<int>(ev)) << 23), sum);
+                                sum2[0] = sum2[1] = f2_pack(0.f, 0.f);
+                            }
+                        }
+                        // the terms of P, each what the rounding of those before it dropped
+#pragma unroll
+                        for (int t = 0; t < B::kTerms; ++t) {
+                            uint32_t h[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                h[k] = B::kConvert ? f32x2_to_f16x2(p[2 * k], p[2 * k + 1])
+                                                   : f32x2_to_bf16x2(p[2 * k], p[2 * k + 1]);
+                                if (t + 1 < B::kTerms) {
+                                    const float2 f = B::kConvert ? f16x2_to_f32x2(h[k]) : bf16x2_to_f32x2(h[k]);
+                                    p[2 * k] -= f.x;
+                                    p[2 * k + 1] -= f.y;
+                                }
+                            }
+                            tmem_st16(scol + p_column<B::kTerms>(c, t), h);
+                        }
+                    }
+                    if constexpr (!kBlocks) {
+                        float s0, s1, s2, s3;
+                        f2_unpack(sum2[0], s0, s1);
+                        f2_unpack(sum2[1], s2, s3);
+                        sum = (s0 + s1) + (s2 + s3);
+                    }
+                    l_sum += sum;
+                    tmem_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&bar.p_full[gr]);
+                }
+                // the last tile's O += P V
+                if (mine > 0 && !*abort_flag)
+                    wait_or_abort(&bar.o_done[gr], (group_done + mine - 1) & 1, kCopyWaitLimitNs, abort_flag, 4u);
+                __syncwarp();
+                tmem_fence_after_sync();
+            } else if (warp >= B::kIssue) {
+                // ------------------------------------------ S = Q K^T and O += P V of one group
+                named_barrier_sync(1, 320);
+                if (lane == 0) {
+                    constexpr uint32_t idesc_s = idesc<!B::kConvert>(kTok, false), idesc_o = idesc<!B::kConvert>(128, true);
+                    const uint64_t dq = umma_desc(smem_addr(sm + kOffQ + (wide ? gr : 0) * kQBytes), 0, 1024);
+                    const uint64_t dk = umma_desc(smem_addr(sm + kOffBufs), 0, 1024);
+                    const uint64_t dv = umma_desc(smem_addr(sm + kOffBufs), B::kSliceBytes, 1024);
+                    const uint32_t scol = tmem + kColS + 128u * gr, ocol = tmem + kColO + 128u * gr;
+                    const uint64_t limit = B::kConvert ? kCopyWaitLimitNs : a.copy_wait_ns;
+                    const unsigned bit = B::kConvert ? 4u : 1u;
+                    int i = 0;                             // the group's tiles
+                    for (int j = 0; j < n_tiles; ++j) {
+                        const uint32_t k_item = items_done + 2 * j, v_item = k_item + 1;
+                        uint64_t *k_free = &bar.free[k_item % kBufs], *v_free = &bar.free[v_item % kBufs];
+                        if (!wide && (j & 1) != gr) {      // the other group's tile: nothing to read
+                            if (!wait_or_abort(&bar.full[k_item % kBufs], (k_item / kBufs) & 1, limit, abort_flag, bit))
+                                break;
+                            mbar_arrive(k_free);
+                            if (!wait_or_abort(&bar.full[v_item % kBufs], (v_item / kBufs) & 1, limit, abort_flag, bit))
+                                break;
+                            mbar_arrive(v_free);
+                            continue;
+                        }
+                        // S goes where P of the last tile was read from
+                        if (i > 0 && !wait_or_abort(&bar.o_done[gr], (group_done + i - 1) & 1, kCopyWaitLimitNs,
+                                                    abort_flag, 4u))
+                            break;
+                        if (!wait_or_abort(&bar.full[k_item % kBufs], (k_item / kBufs) & 1, limit, abort_flag, bit))
+                            break;
+                        tmem_fence_after_sync();
+                        const uint64_t kb = dk + (((k_item % kBufs) * B::kHalfBytes) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            umma_f16(scol, dq + (((kk >> 2) * (kQBytes / 2) + (kk & 3) * 32) >> 4),
+                                     kb + (((kk >> 2) * B::kSliceBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+                        umma_commit(&bar.s_full[gr]);
+                        umma_commit(k_free);
+                        if (!wait_or_abort(&bar.full[v_item % kBufs], (v_item / kBufs) & 1, limit, abort_flag, bit))
+                            break;
+                        if (!wait_or_abort(&bar.p_full[gr], (group_done + i) & 1, kCopyWaitLimitNs, abort_flag, 4u))
+                            break;
+                        tmem_fence_after_sync();
+                        const uint64_t vb = dv + (((v_item % kBufs) * B::kHalfBytes) >> 4);
+                        const bool onto = kPrecise ? i % kFlush != 0 : i > 0;
+#pragma unroll
+                        for (int t = 0; t < B::kTerms; ++t)
+#pragma unroll
+                            for (int kk = 0; kk < kTok / 16; ++kk)
+                                umma_f16_ts(ocol, scol + p_column<B::kTerms>(kk >> 1, t) + 8u * (kk & 1),
+                                            vb + static_cast<uint64_t>((kk * 2048) >> 4), idesc_o,
+                                            onto || t > 0 || kk > 0);
+                        umma_commit(&bar.o_done[gr]);
+                        umma_commit(v_free);
+                        ++i;
+                    }
+                    // nothing this lane issued may still run when the job ends
+                    umma_commit(&bar.drain[gr]);
+                    if (!mbar_wait_bounded(&bar.drain[gr], jobs_done & 1, kCopyWaitLimitNs))
+                        atomicOr(&g_umma_error, 4u);
+                }
+                __syncwarp();
+            } else if (warp == B::kCopy) {
+                // ------------------------------------------ copies of K's and V's rows
+                const uint64_t policy = l2_policy_evict_normal();
+                // boxes of a tile: one lane each; a box does not cross a page
+                constexpr int kMaxBox = B::kConvert ? kChunkTokens : kTok;
+                const int box = min(a.page_size, kMaxBox), boxes = kTok / box;
+                const int64_t outside = -256;              // rows no copy finds: zeros
+                const auto page_at = [&](int tile) {
+                    const int tok = tile * kTok + lane * box;
+                    return lane < boxes && tile < tile1 && tok < w.len ? __ldcg(bt + (tok >> ps_shift)) : -1;
+                };
+                int page = page_at(tile0);
+                bool ok = true;
+                for (int tile = tile0; ok && tile < tile1; ++tile) {
+                    const int tok = tile * kTok + lane * box;
+                    const bool held = lane < boxes && tok < w.len, fine = held && page >= 0 && page < a.num_pages;
+                    if (held && !fine)
+                        atomicMin(&s.bad_from, tok);
+                    const int y = static_cast<int>(
+                        fine ? (static_cast<int64_t>(page) * hkv + kvh) * a.page_size + (tok & (a.page_size - 1)) : outside);
+                    page = page_at(tile + 1);
+                    if constexpr (B::kConvert) {
+                        uint64_t *landed = wide ? bar.wide_landed : bar.narrow_landed;
+                        uint64_t *empty = wide ? bar.wide_empty : bar.narrow_empty;
+                        uint8_t *ring = sm + (wide ? kOffRingWide : kOffRingNarrow);
+                        const uint32_t before = wide ? wide_done : narrow_done;
+                        const int per = kStageTok / box;   // boxes of a stage
+                        for (int q = 0; ok && q < 2 * kTok / kStageTok; ++q) {
+                            const uint32_t n = before + issued;
+                            const uint32_t st = wide ? n % kWideStages : n % kNarrowStages;
+                            const uint32_t round = wide ? n / kWideStages : n / kNarrowStages;
+                            if (round > 0 && !__all_sync(0xFFFFFFFFu, wait_or_abort(&empty[st], (round - 1) & 1,
+                                                                                    kCopyWaitLimitNs, abort_flag, 4u))) {
+                                ok = false;
+                                break;
+                            }
+                            const bool is_v = q >= kTok / kStageTok;
+                            const int part0 = (is_v ? q - kTok / kStageTok : q) * per;
+                            if (lane == 0)
+                                mbar_arrive_expect_tx(&landed[st], kRingStage);
+                            __syncwarp();
+                            if (lane >= part0 && lane < part0 + per)
+                                tma_load_2d(ring + st * kRingStage + (lane - part0) * box * 128,
+                                            is_v ? static_cast<const void *>(&v_map) : static_cast<const void *>(&k_map),
+                                            0, y, &landed[st], policy);
+                            ++issued;
+                        }
+                    } else {
+                        for (int q = 0; q < 2; ++q) {
+                            const uint32_t item = items_done + issued, b = item % kBufs;
+                            if (item >= kBufs && !__all_sync(0xFFFFFFFFu, wait_or_abort(&bar.free[b], (item / kBufs - 1) & 1,
+                                                                                        kCopyWaitLimitNs, abort_flag, 4u))) {
+                                ok = false;
+                                break;
+                            }
+                            if (lane == 0)
+                                mbar_arrive_expect_tx(&bar.full[b], B::kHalfBytes);
+                            __syncwarp();
+                            if (lane < boxes)
+#pragma unroll
+                                for (int half = 0; half < 2; ++half)
+                                    tma_load_2d(sm + kOffBufs + b * B::kHalfBytes + half * B::kSliceBytes + lane * box * 128,
+                                                q ? static_cast<const void *>(&v_map) : static_cast<const void *>(&k_map),
+                                                64 * half, y, &bar.full[b], policy);
+                            ++issued;
+                        }
+                    }
+                }
+            } else if constexpr (B::kConvert) {
+                // ------------------------------------------ e4m3 -> f16 (exact)
+                const int ct = tid - 32 * B::kConv;        // 0 .. 127
+                const int c = ct & 7;                      // 16-byte chunk (16 dims) of a row
+                uint64_t *landed = wide ? bar.wide_landed : bar.narrow_landed;
+                uint64_t *empty = wide ? bar.wide_empty : bar.narrow_empty;
+                const uint8_t *ring = sm + (wide ? kOffRingWide : kOffRingNarrow);
+                const uint32_t before = wide ? wide_done : narrow_done;
+                constexpr int kPer = kTok / kStageTok;     // stages of an item
+                bool ok = true;
+                for (int it = 0; ok && it < 2 * n_tiles; ++it) {
+                    const uint32_t item = items_done + it, b = item % kBufs;
+                    uint8_t *to = sm + kOffBufs + b * B::kHalfBytes;
+#pragma unroll
+                    for (int part_of = 0; part_of < kPer; ++part_of) {
+                        const uint32_t n = before + it * kPer + part_of;
+                        const uint32_t st = wide ? n % kWideStages : n % kNarrowStages;
+                        const uint32_t round = wide ? n / kWideStages : n / kNarrowStages;
+                        // every lane polls; the warp goes on or gives up as one
+                        if (!__all_sync(0xFFFFFFFFu, wait_or_abort(&landed[st], round & 1, a.copy_wait_ns, abort_flag, 1u))) {
+                            ok = false;
+                            break;
+                        }
+                        if (part_of == 0 && item >= kBufs &&
+                            !__all_sync(0xFFFFFFFFu, wait_or_abort(&bar.free[b], (item / kBufs - 1) & 1, kCopyWaitLimitNs,
+                                                                   abort_flag, 4u))) {
+                            ok = false;
+                            break;
+                        }
+                        const uint8_t *from = ring + st * kRingStage;
+                        uint4 x[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int t = (ct >> 3) + 16 * k;
+                            x[k] = *reinterpret_cast<const uint4 *>(from + t * 128 + ((c ^ (t & 7)) << 4));
+                        }
+                        // chunk c of row t goes to the operand's chunks 2 c, 2 c + 1;
+                        // lanes with c >= 4 (the other slice, the same banks)
+                        // store theirs in the other order
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int t = (ct >> 3) + 16 * k + part_of * kStageTok;
+                            const uint32_t slice = static_cast<uint32_t>((c >> 2) * B::kSliceBytes);
+                            const uint32_t o0 = slice + sw128_chunk(t, 2 * (c & 3));
+                            const uint32_t o1 = slice + sw128_chunk(t, 2 * (c & 3) + 1);
+                            const bool swap = c >= 4;
+                            const uint32_t a0 = swap ? x[k].z : x[k].x, a1 = swap ? x[k].w : x[k].y;
+                            const uint32_t b0 = swap ? x[k].x : x[k].z, b1 = swap ? x[k].y : x[k].w;
+                            *reinterpret_cast<uint4 *>(to + (swap ? o1 : o0)) =
+                                make_uint4(lo16_e4m3x2_to_f16x2(a0), hi16_e4m3x2_to_f16x2(a0),
+                                           lo16_e4m3x2_to_f16x2(a1), hi16_e4m3x2_to_f16x2(a1));
+                            *reinterpret_cast<uint4 *>(to + (swap ? o0 : o1)) =
+                                make_uint4(lo16_e4m3x2_to_f16x2(b0), hi16_e4m3x2_to_f16x2(b0),
+                                           lo16_e4m3x2_to_f16x2(b1), hi16_e4m3x2_to_f16x2(b1));
+                        }
+                        fence_proxy_async_smem();          // the writes, for the tensor core;
+                        __syncwarp();                      // the ring reads, for the next copy
+                        if (lane == 0) {
+                            mbar_arrive(&empty[st]);
+                            if (part_of == kPer - 1)
+                                mbar_arrive(&bar.full[b]);
+                        }
+                    }
+                }
+            }
+        }
+        tmem_fence_before_sync();
+        __syncthreads();                                   // every role has finished or given up
+        tmem_fence_after_sync();
+        const bool failed = s.abort != 0;
+        if (failed && !failed_before && warp == B::kCopy && lane == 0) {
+            // none of the copies in flight may land after the CTA has moved on
+            bool drained = true;
+            if constexpr (B::kConvert) {
+                const uint32_t n_st = wide ? kWideStages : kNarrowStages, all = (wide ? wide_done : narrow_done) + issued;
+                uint64_t *landed = wide ? bar.wide_landed : bar.narrow_landed;
+                for (uint32_t n = all - min(n_st, static_cast<uint32_t>(issued)); n < all; ++n)
+                    drained &= mbar_wait_bounded(&landed[n % n_st], (n / n_st) & 1, kCopyWaitLimitNs);
+            } else {
+                const uint32_t all = items_done + issued;
+                for (uint32_t n = all - min(static_cast<uint32_t>(kBufs), static_cast<uint32_t>(issued)); n < all; ++n)
+                    drained &= mbar_wait_bounded(&bar.full[n % kBufs], (n / kBufs) & 1, kCopyWaitLimitNs);
+            }
+            if (!drained)
+                atomicOr(&g_umma_error, 2u);
+        }
+        // ---------------------------------------------- the rows' results
+        if (warp < 8) {
+            const int64_t place = 256ll * blockIdx.x + place0 + m;
+            if (row_valid) {
+                float lse = l_sum == 0.f ? -INFINITY : l_sum == l_sum ? m_used + __log2f(l_sum) - B::kLift : INFINITY;
+                if (failed || lim > s.bad_from)            // the row gets zeros
+                    lse = __uint_as_float(0x7FC00000u);
+                a.pre_lse[place] = lse;
+                if (w.c0 == static_cast<int>(blockIdx.x) && (wide || gr == 0))
+                    a.pre_rec[id] = make_int4(static_cast<int>(256ll * w.c0 + place0), wide ? w.nsplit : -w.nsplit,
+                                              tile_rows, m);
+            }
+            if (!failed && mine > 0) {
+                const float vs = B::kConvert && !kBlocks ? a.v_scale[kvh] : 1.f;
+                const float wgt = l_sum == 0.f ? 0.f : vs / l_sum;
+                const uint32_t ocol = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kColO + 128u * gr;
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t o[16];
+                    tmem_ld16(ocol + 16u * c, o);
+                    if (row_valid)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float4 v = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                   __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                            float4 *at = part + (4 * c + k) * tile_rows;
+                            if (kPrecise && mine > kFlush) {
+                                const float4 u = *at;
+                                v.x = fmaf(u.x, sums_mul, v.x);
+                                v.y = fmaf(u.y, sums_mul, v.y);
+                                v.z = fmaf(u.z, sums_mul, v.z);
+                                v.w = fmaf(u.w, sums_mul, v.w);
+                            }
+                            *at = wgt != 0.f ? make_float4(v.x * wgt, v.y * wgt, v.z * wgt, v.w * wgt)
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+                }
+            }
+            tmem_fence_before_sync();
+        }
+        (wide ? wide_done : narrow_done) += 2 * n_tiles * (kTok / (B::kConvert ? kStageTok : kTok));
+        items_done += 2 * n_tiles;
+        group_done += mine;
+        ++jobs_done;
+        __syncthreads();                                   // the job's numbers have been read
+        tmem_fence_after_sync();
+    }
+    tmem_fence_before_sync();
+    __syncthreads();
+    if (warp == 0) {
+        tmem_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ combine
+
+// out = sum_s w_s o_s / sum_s w_s with w_s = 2^(lse_s - max lse), over the parts
+// of the shared pages and of the row's own.  A warp takes two rows, even lanes
+// one and odd lanes the other, so that a load of the shared pages' parts, which
+// lie row beside row, uses whole sectors.  Zeros where any part is invalid
+// (lse NaN); a NaN sum (lse +inf) makes the row NaN.
+constexpr int kCombineWarps = 4;
+__global__ void __launch_bounds__(32 * kCombineWarps)
+combine_prefix_kernel(const PrefixArgs a)
+{
+    const int lane = threadIdx.x % 32, col = lane >> 1;
+    const int64_t row = 2 * (static_cast<int64_t>(blockIdx.x) * kCombineWarps + threadIdx.x / 32) + (lane & 1);
+    const int64_t per_request = static_cast<int64_t>(a.n_query) * a.num_q_heads;
+    const int ps_shift = __ffs(a.page_size) - 1;
+    grid_dependency_wait();
+    const bool real_row = row < a.batch * per_request;
+    int np = 0, ns = 0;                                    // parts of the shared pages, and of the row's own
+    bool narrow = false;
+    int4 rec = make_int4(0, 0, 0, 0);
+    int64_t own_at = 0;
+    const int per = a.n_query > 1 ? kMultiRowsPerCta : kMaxGroup;
+    if (real_row) {
+        const int b = static_cast<int>(row / per_request);
+        const int64_t real = __ldcg(a.seq_lens + b);
+        const bool aborted = a.abort_flags != nullptr && __ldcg(a.abort_flags + b) != 0;
+        if (!aborted && real > 0 && real <= static_cast<int64_t>(a.max_pages_per_seq) << ps_shift) {
+            const int shared = shared_tokens(a, b, ps_shift);
+            if (shared > 0) {
+                rec = __ldcg(a.pre_rec + row);
+                narrow = rec.y < 0;
+                np = narrow ? -2 * rec.y : rec.y;
+            }
+            if (real > shared) {
+                const int in = static_cast<int>(row % per_request), hq = in % a.num_q_heads;
+                const int kvh = hq / a.group, r = in / a.num_q_heads * a.group + hq % a.group;
+                const int2 pair =
+                    __ldcg(a.ws_pairs + (static_cast<int64_t>(b) * a.num_kv_heads + kvh) * a.row_blocks + r / per);
+                own_at = static_cast<int64_t>(pair.x) * per + r % per;
+                ns = pair.y;
+            }
+        }
+    }
+    const int nt = np + ns;
+    const auto place = [&](int q) -> int64_t {             // of part q < np, its tile's first row
+        return static_cast<int64_t>(rec.x) + (narrow ? 256ll * (q >> 1) + (q & 1) * rec.z : 256ll * q);
+    };
+    const auto lse_of = [&](int q) {
+        return q < np ? __ldcg(a.pre_lse + place(q) + rec.w) : __ldcg(a.ws_lse + own_at + static_cast<int64_t>(q - np) * per);
+    };
+    const int most = max(nt, __shfl_xor_sync(0xFFFFFFFFu, nt, 1));
+    float M = -INFINITY;
+    bool bad = false;
+    for (int q = col; q < nt; q += 16) {
+        const float y = lse_of(q);
+        bad |= y != y;
+        M = fmaxf(M, y);
+    }
+    int flag = bad;
+#pragma unroll
+    for (int off = 2; off < 32; off <<= 1) {
+        M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+        flag |= __shfl_xor_sync(0xFFFFFFFFu, flag, off);
+    }
+    float sum = 0.f;
+    for (int q = col; q < nt; q += 16) {
+        const float y = lse_of(q);
+        sum += y == -INFINITY ? 0.f : fast_exp2(y - M);
+    }
+#pragma unroll
+    for (int off = 2; off < 32; off <<= 1)
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+    const float inv = flag || sum == 0.f ? 0.f : 1.f / sum;      // NaN stays
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int q0 = 0; q0 < most; q0 += 16) {
+        float wq = 0.f;
+        if (q0 + col < nt && inv != 0.f) {
+            const float y = lse_of(q0 + col);
+            wq = y == -INFINITY ? 0.f : fast_exp2(y - M) * inv;
+        }
+        const int n = min(16, most - q0);
+        for (int k0 = 0; k0 < n; k0 += 4) {
+            float4 v[4][2];
+            float wk[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int q = q0 + k0 + k;
+                wk[k] = __shfl_sync(0xFFFFFFFFu, wq, (2 * (k0 + k) + (lane & 1)) & 31);
+                v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (q < nt && wk[k] != 0.f) {              // a part without weight may hold anything
+                    if (q < np) {
+                        const float4 *from = a.pre_o + place(q) * 32 + rec.w + static_cast<int64_t>(col) * rec.z;
+                        v[k][0] = __ldcg(from);
+                        v[k][1] = __ldcg(from + 16ll * rec.z);
+                    } else {
+                        const float4 *from = reinterpret_cast<const float4 *>(
+                                                 a.ws_o + (own_at + static_cast<int64_t>(q - np) * per) * kHeadDim) + col;
+                        v[k][0] = __ldcg(from);
+                        v[k][1] = __ldcg(from + 16);
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (wk[k] != 0.f)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        acc[h].x += wk[k] * v[k][h].x;
+                        acc[h].y += wk[k] * v[k][h].y;
+                        acc[h].z += wk[k] * v[k][h].z;
+                        acc[h].w += wk[k] * v[k][h].w;
+                    }
+        }
+    }
+    if (real_row)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            store_row_value4(a.out, row * kHeadDim + 4 * col + 64 * h, acc[h], a.out_fp32);
+}
+
+cudaLaunchConfig_t dependent(dim3 grid, int threads, size_t smem, cudaStream_t stream, cudaLaunchAttribute (&attr)[1])
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+template <int kKind, bool kPrecise>
+cudaError_t launch_rows(const PrefixArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map, cudaStream_t stream)
+{
+    constexpr int kBytes = 1024 + kData + static_cast<int>(sizeof(Shared));
+    static int configured[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(prefix_rows_kernel<kKind, kPrecise>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+        if (e != cudaSuccess)
+            return e;
+        if (dev >= 0 && dev < 64)
+            configured[dev] = 1;
+    }
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg =
+        dependent(dim3(static_cast<unsigned>(a.pre_ctas)), Build<kKind, kPrecise>::kThreads, kBytes, stream, attr);
+    e = cudaLaunchKernelEx(&cfg, prefix_rows_kernel<kKind, kPrecise>, k_map, v_map, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+} // namespace
+
+cudaError_t launch_prefix_rows(const PrefixArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                               cudaStream_t stream)
+{
+    if (a.bf16_cache)
+        return a.out_fp32 ? launch_rows<kBf16, true>(a, k_map, v_map, stream)
+                          : launch_rows<kBf16, false>(a, k_map, v_map, stream);
+    if (a.k_exp != nullptr)
+        return a.out_fp32 ? launch_rows<kBlocksFp8, true>(a, k_map, v_map, stream)
+                          : launch_rows<kBlocksFp8, false>(a, k_map, v_map, stream);
+    return a.out_fp32 ? launch_rows<kFp8, true>(a, k_map, v_map, stream)
+                      : launch_rows<kFp8, false>(a, k_map, v_map, stream);
+}
+
+cudaError_t launch_combine_prefix(const PrefixArgs &a, cudaStream_t stream)
+{
+    const int64_t rows = static_cast<int64_t>(a.batch) * a.n_query * a.num_q_heads, per = 2 * kCombineWarps;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg =
+        dependent(dim3(static_cast<unsigned>((rows + per - 1) / per)), 32 * kCombineWarps, 0, stream, attr);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, combine_prefix_kernel, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t read_prefix_error(uint32_t *bits, bool clear) { return read_umma_error_word(bits, clear); }
+
+} // namespace kvq

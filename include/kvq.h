@@ -480,6 +480,73 @@ KVQ_API kvq_status kvq_decode_attn_blocks(const kvq_cache_desc *desc, const void
                                           int32_t num_splits, kvq_stream_t stream);
 
 /*
+ * kvq_decode_plan_prefix / kvq_decode_attn_prefix -- decode attention for
+ * requests of which several begin with the same pages: a system prompt, the
+ * samples of one prompt, the branches of a search (kvq_fork_tables makes such
+ * rows).  The result is kvq_decode_attn_mt's over each request's own row; the
+ * shared pages are read and multiplied once for all the requests that share
+ * them.
+ *
+ *   prefix_of      int32 [batch]: the request in whose row of the block table
+ *                  request r's first pages are looked up (its own index is
+ *                  fine); negative or past the batch: r shares nothing.
+ *   prefix_lens    int32 [batch]: the first prefix_lens[r] tokens of r are those
+ *                  of request prefix_of[r].  Both rows must hold them, in the
+ *                  same pages or in copies of them: the call looks up whole
+ *                  pages of min(prefix_lens[r], seq_lens[prefix_of[r]],
+ *                  seq_lens[r] - n + 1) tokens in the other row, the rest in
+ *                  r's, and all of them in r's if request prefix_of[r] is
+ *                  aborted or longer than its row.
+ *                  Consecutive requests with one value of prefix_of are served
+ *                  together, whatever their lengths; the same value again
+ *                  further on starts over, as does every 128th request.  A
+ *                  request that shares with no other is best given a
+ *                  prefix_lens of 0.
+ *   num_query_tokens, q, out, seq_lens, abort_flags and every other argument
+ *                  as in kvq_decode_attn_mt, with either cache type; n = 1 to 16.
+ *   workspace      of at least the plan's size, on the plan's device.  It needs
+ *                  no contents, and holds nothing once the call is done.  Two
+ *                  calls in flight at once must not share it.
+ * A request is zeroed as in kvq_decode_attn_mt; so is one whose shared pages the
+ * other row gives an id outside [0, num_pages).  A NaN that some query of a
+ * request sees may reach the other queries of that request and, in the V row of
+ * a position below the longest prefix_lens of those served together, theirs.
+ * Three launches: the shared pages on the 5th-generation tensor cores, up to
+ * 256 query rows (request, token, head) of a KV head at a time; the requests'
+ * own pages; the parts of both joined.  Each shares its work out evenly on the
+ * device, whatever the lengths.
+ */
+KVQ_API kvq_status kvq_decode_plan_prefix(const kvq_cache_desc *desc, int32_t batch,
+                                          int32_t num_query_tokens, int32_t num_q_heads,
+                                          int32_t max_pages_per_seq, size_t *workspace_bytes);
+KVQ_API kvq_status kvq_decode_attn_prefix(const kvq_cache_desc *desc, const void *q, int32_t batch,
+                                          int32_t num_query_tokens, int32_t num_q_heads,
+                                          const void *k_cache, const void *v_cache,
+                                          const float *k_scale, const float *v_scale,
+                                          const int32_t *block_table, int32_t max_pages_per_seq,
+                                          const int32_t *seq_lens, const int32_t *prefix_of,
+                                          const int32_t *prefix_lens, float softmax_scale,
+                                          const uint8_t *abort_flags, void *out, int32_t out_dtype,
+                                          void *workspace, size_t workspace_bytes,
+                                          kvq_stream_t stream);
+
+/*
+ * kvq_decode_attn_prefix_blocks -- kvq_decode_attn_prefix over a block-scaled
+ * cache: k_exp and v_exp as in kvq_decode_attn_blocks, every other argument and
+ * the plan as in kvq_decode_attn_prefix, with KVQ_CACHE_FP8_E4M3 only.
+ */
+KVQ_API kvq_status kvq_decode_attn_prefix_blocks(const kvq_cache_desc *desc, const void *q, int32_t batch,
+                                                 int32_t num_query_tokens, int32_t num_q_heads,
+                                                 const void *k_cache, const void *v_cache,
+                                                 const int8_t *k_exp, const int8_t *v_exp,
+                                                 const int32_t *block_table, int32_t max_pages_per_seq,
+                                                 const int32_t *seq_lens, const int32_t *prefix_of,
+                                                 const int32_t *prefix_lens, float softmax_scale,
+                                                 const uint8_t *abort_flags, void *out,
+                                                 int32_t out_dtype, void *workspace,
+                                                 size_t workspace_bytes, kvq_stream_t stream);
+
+/*
  * kvq_copy_pages -- page src_pages[i] of every listed cache becomes page
  * dst_pages[i] of the same cache: a fork's own copy of a last page that it
  * will append to, or pages moved to close gaps.
