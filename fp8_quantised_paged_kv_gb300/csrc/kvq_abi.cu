@@ -1181,7 +1181,7 @@ static kvq_status decode_prefix(const kvq_cache_desc *desc, const void *q, int32
     if (!make_cache_map(&km, desc, k_cache) || !make_cache_map(&vm, desc, v_cache))
         return KVQ_ERR_CUDA;
     if (bf16) {
-        const int box = kvq::prefix_box_tokens(desc->page_size, true, a.out_fp32);
+        const int box = kvq::prefix_box_tokens(desc->page_size, true);
         if (!make_half_row_map(&pk, desc, k_cache, box) || !make_half_row_map(&pv, desc, v_cache, box))
             return KVQ_ERR_CUDA;
     }

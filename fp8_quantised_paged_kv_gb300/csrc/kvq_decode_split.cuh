@@ -879,7 +879,19 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
         constexpr bool first = true;
 #include "kvq_decode_split_body.cuh"
     } else {
-        start_dependent(k_map, v_map);
+        if constexpr (kSharing) {
+            // Launched beside the kernel over the shared pages, once every CTA of
+            // that one has seen the launches before it end.  Nothing here
+            // reads what that kernel writes; CTA 0 ends after it, so that the
+            // combine, which waits for this launch, comes after both.
+            if (threadIdx.x == 0) {
+                prefetch_tensor_map(&k_map);
+                prefetch_tensor_map(&v_map);
+            }
+            grid_launch_dependents();
+        } else {
+            start_dependent(k_map, v_map);
+        }
         Job job;                                           // unused without a window
         job.split = blockIdx.x;
         job.b = blockIdx.z;
@@ -894,14 +906,20 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
             const bool balanced = a.resident_ctas > 0;
             const int ps_shift = __ffs(a.page_size) - 1;
             __shared__ Share<kMulti> share;
-            if (balanced && !share.find(a, ps_shift))
+            if (balanced && !share.find(a, ps_shift)) {
+                if (kSharing && blockIdx.x == 0)
+                    grid_dependency_wait();
                 return;
+            }
             for (bool first = true;; first = false) {
                 if (balanced)
                     job = share.job;
                 run_split<kBf16Cache, kPreciseP, kCluster, kMulti, kWindow, kBlocks>(k_map, v_map, a, job, first);
-                if (!balanced || !share.next(a, ps_shift))
+                if (!balanced || !share.next(a, ps_shift)) {
+                    if (kSharing && blockIdx.x == 0)
+                        grid_dependency_wait();
                     return;
+                }
             }
         } else {
             run_split<kBf16Cache, kPreciseP, kCluster, kMulti, kWindow, kBlocks>(k_map, v_map, a, job, true);

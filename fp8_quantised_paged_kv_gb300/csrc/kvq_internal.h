@@ -240,9 +240,9 @@ cudaError_t read_own_error(uint32_t *bits, bool clear);
 cudaError_t read_own_blocks_error(uint32_t *bits, bool clear);
 // Tokens of a copy of the shared pages.  A bf16 cache is read through a map of
 // [rows][128] values, 64 of a row at a time.
-inline int prefix_box_tokens(int page_size, bool bf16_cache, bool out_fp32)
+inline int prefix_box_tokens(int page_size, bool bf16_cache)
 {
-    const int most = !bf16_cache ? kChunkTokens : out_fp32 ? 64 : 128;
+    const int most = bf16_cache ? 64 : kChunkTokens;
     return page_size < most ? page_size : most;
 }
 

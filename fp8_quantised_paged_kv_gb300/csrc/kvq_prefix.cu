@@ -10,14 +10,15 @@
 // combine_prefix_kernel below joins the parts by their log-sum-exps.
 //
 // A CTA takes up to 256 rows, two tiles of 128, through a range of the run's
-// pages, 128 tokens (64 with the widest P) at a time.  Its warps have one job
+// pages, 64 tokens at a time.  Its warps have one job
 // each: copies by TMA; over an FP8 cache the conversion of K and V to f16 (once
 // for all rows); per row tile a thread that issues S = Q K^T and O += P V, and
 // a softmax group of four warps, a row per thread, which reads S from tensor
 // memory, and writes P over it.  One tile's exponentials run beside the other's
-// products.  With up to 128 rows both groups serve the same rows on alternate
-// token tiles, and their results are two parts.  Tensor memory is full: two S
-// of 128 columns and two accumulators of 128; so Q is read from shared memory.
+// products, and each group has the next tile's S while it works on one.  With
+// up to 128 rows both groups serve the same rows on alternate token tiles, and
+// their results are two parts.  Tensor memory is full: four S of 64 columns and
+// two accumulators of 128; so Q is read from shared memory.
 //
 // Block scales mean what they mean in kvq_decode_split.cuh: ek on the scores,
 // ev in the exponent with 2^-ev undone in l.  Over an FP8 cache P is kept 2^7
@@ -36,6 +37,20 @@ namespace {
 
 enum CacheKind { kFp8, kBlocksFp8, kBf16 };
 
+constexpr int kTok = 64;                                   // tokens of a tile
+constexpr int kHalfBytes = kTok * 256;                     // K or V of a tile, 16-bit
+constexpr int kSliceBytes = kTok * 128;                    // 64 dims of it
+constexpr int kQBytes = 128 * 256;                         // 128 rows as 16-bit values
+constexpr int kRingStage = kTok * 128;                     // a stage of the e4m3 ring: K, or V, of a tile
+// Two row tiles' Q leave room for eleven stages; with one tile the ring has
+// the place of the second Q as well.
+constexpr int kWideStages = 11, kNarrowStages = 15;
+constexpr int kOffQ = 0, kOffQ2 = kQBytes;
+constexpr int kOffRingNarrow = kOffQ2, kOffRingWide = kOffQ2 + kQBytes;
+constexpr int kOffRingEnd = kOffRingWide + kWideStages * kRingStage;
+static_assert(kOffRingNarrow + kNarrowStages * kRingStage == kOffRingEnd, "both rings end where the buffers start");
+constexpr int kData = kOffRingEnd + 2 * 2 * kHalfBytes;
+
 // The most that differs between the builds.
 template <int kKind, bool kPrecise>
 struct Build {
@@ -43,52 +58,44 @@ struct Build {
     // 16-bit terms of a weight: one for bf16 output; for fp32 output two of
     // f16 (2^-22) or three of bf16 (2^-24)
     static constexpr int kTerms = !kPrecise ? 1 : kConvert ? 2 : 3;
-    // tokens of a tile: P's terms have to fit in the 128 columns of S
-    static constexpr int kTok = kTerms == 3 ? 64 : 128;
-    static constexpr int kHalfBytes = kTok * 256;          // K or V of a tile, 16-bit
-    static constexpr int kSliceBytes = kTok * 128;         // 64 dims of it
-    static constexpr int kConv = 8;                        // first of four converting warps
-    static constexpr int kCopy = kConvert ? 12 : 8;        // the copying warp
+    // S buffers per group, of 64 columns; three terms of P need the place of both
+    static constexpr int kSBufs = kTerms == 3 ? 1 : 2;
+    // Tiles whose K and V are in 16-bit buffers at a time, converted or as the
+    // copies bring them.  An even number: with two groups on alternate tiles a
+    // buffer is then one group's alone.
+    static constexpr int kSlots = kConvert ? 2 : 4;
+    static constexpr int kOffBufs = kConvert ? kOffRingEnd : kOffQ2 + kQBytes;
+    static_assert(kOffBufs + 2 * kSlots * kHalfBytes <= kData);
+    static constexpr int kCopy = kConvert ? 16 : 8;        // the copying warp; before it eight converting ones
     static constexpr int kIssue = kCopy + 1;               // two issuing warps, one per group
-    static constexpr int kThreads = 32 * (kIssue + 2);
+    // With converters whole warpgroups, which divide the launch's registers
+    // (640 x 96) otherwise: 136 for the softmax, 72 for the converters, 56 for the rest.
+    static constexpr int kThreads = kConvert ? 640 : 32 * (kIssue + 2);
     static constexpr float kLift = kConvert ? 7.f : -8.f;  // log2 of what P, l and O are larger by
 };
 
-constexpr int kBufs = 4;                                   // K and V of two tiles
-constexpr int kQBytes = 128 * 256;                         // 128 rows as 16-bit values
-constexpr int kStageTok = 64;                              // of a stage of the e4m3 ring (K rows, or V rows)
-constexpr int kRingStage = kStageTok * 128;
-// Two row tiles' Q leave room for three stages; with one tile the ring has
-// the place of the second Q as well.
-constexpr int kWideStages = 3, kNarrowStages = 7;
-constexpr int kOffQ = 0, kOffQ2 = kQBytes;
-constexpr int kOffRingNarrow = kOffQ2, kOffRingWide = kOffQ2 + kQBytes;
-constexpr int kOffBufs = kOffRingWide + kWideStages * kRingStage;
-static_assert(kOffRingNarrow + kNarrowStages * kRingStage == kOffBufs, "the narrow ring ends where the buffers start");
-constexpr int kData = kOffBufs + kBufs * 128 * 256;
-
 constexpr int kBlockReq = 128;                             // a run does not cross a multiple of it
 constexpr int kMaxBlocks = 512;                            // of up to 65,535 requests
-constexpr int kMinTiles = 2;                               // of a CTA's share, in wide tiles
-constexpr int kWideCost = 2, kNarrowCost = 1;              // places of a tile of tokens by the row tiles served
-constexpr int kBorderCost = 4;                             // and of a border between two jobs
+constexpr int kMinTiles = 4;                               // of a CTA's share, in wide tiles
+constexpr int kWideCost = 8, kNarrowCost = 7;              // places of a tile of tokens by the row tiles served
+constexpr int kBorderCost = 40;                            // and of a border between two jobs
 
 constexpr uint32_t kColS = 0, kColO = 256;                 // + 128 for the second group
 constexpr int kFlush = 16;                                 // fp32 output: tiles between O's ways out of tensor memory
 
-// Column, from S's first, of term t of P for tokens 32 c .. 32 c + 31 of a tile.
-// P is written 32 tokens after 32, over scores that have been read.
+// Column, from its S buffer's first, of term t of P for tokens 32 c .. 32 c + 31
+// of a tile.  P is written over scores that have been read.
 template <int kTerms>
 __device__ __forceinline__ uint32_t p_column(int c, int t)
 {
     if constexpr (kTerms < 3)
         return 32u * c + 16u * t;
-    else                                                   // 64 tokens: S has columns 0 .. 63
-        return c == 0 ? 64u + 16u * t : t < 2 ? 16u * t : 112u;
+    else
+        return 48u * c + 16u * t;
 }
 
 struct Run {
-    int first, count, tiles;                               // requests, and tiles of the longest shared part
+    int first, count, lead, tiles;                         // requests, the row that is read, tiles of the longest part
     int len;                                               // its tokens
     int64_t start;                                         // first place
 };
@@ -96,8 +103,9 @@ struct Run {
 struct Bars {
     uint64_t wide_landed[kWideStages], wide_empty[kWideStages];
     uint64_t narrow_landed[kNarrowStages], narrow_empty[kNarrowStages];
-    uint64_t full[kBufs], free[kBufs];                     // K and V buffers (kBf16: full when the copies landed)
-    uint64_t s_full[2], p_full[2], o_done[2], drain[2];
+    uint64_t full[8], free[8];                             // K and V of each slot (kBf16: full when the copies landed)
+    uint64_t s_full[2][2], p_full[2][2];                   // of each group's S buffers
+    uint64_t o_done[2], drain[2];
 };
 
 // A CTA's stretch of the line and where it is on it.
@@ -115,18 +123,18 @@ struct Shared {
     Bars bars;
     uint32_t tmem_slot;
     int abort, bad_from;                                   // bad_from: first token whose page is out of range
-    int state;                                             // of the search for the next job
+    int search, job_there;                                 // for the next job: what find_job found
     Walk w;
     Run runs[kBlockReq];
     int len[kBlockReq];                                    // shared tokens of each request of the block
-    int64_t part[16];
 };
 static_assert(kData + 1024 + sizeof(Shared) <= 232448, "one CTA fits an SM");
 
 // Scratch of the search, in Q's place.
 struct Scratch {
-    int lead[3][kBlockReq], len[3][kBlockReq], most[3][kBlockReq];
+    int lead[3][kBlockReq], most[3][kBlockReq];
     uint32_t cont[3][4];
+    int heads[3][4];
     int64_t warp_sum[3][4];
     int64_t total[kMaxBlocks];
 };
@@ -139,19 +147,47 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool b_mn)
     return umma_idesc_f16(128, n, b_mn) | (kBf ? (1u << 7) | (1u << 10) : 0u);
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
+// A score buffer: 64 columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64])
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 "
                  "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+                 "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+                 "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
                  "tcgen05.wait::ld.sync.aligned;"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
                    "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
                    "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
                    "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
+                   "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]),
+                   "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]),
+                   "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+                   "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
                  : "r"(taddr)
                  : "memory");
+}
+
+// One thread of a whole warp.  What it alone issues needs no vote over the
+// operands, which a branch on the lane would cost the tensor-core instructions.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on != 0;
+}
+
+// Registers of this warpgroup's threads from here on.
+template <int kRegs>
+__device__ __forceinline__ void more_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // The row's O, out of tensor memory onto its sums (from zero, the first time).
@@ -173,66 +209,61 @@ __device__ __forceinline__ void flush_sums(uint32_t ocol, float4 *part, int rows
     }
 }
 
-// Place of a request's run on the line, worked out by the 128 threads of a team
-// (called by the whole CTA; block < 0: nothing to do).  total: its places.
-// list: also the runs themselves and every request's shared tokens, for team 0.
-template <int kTok>
+// The runs of a block of requests and their places on the line, worked out by
+// the 128 threads of a team.  c.total[block]: all its places.  list: also the
+// runs themselves and every request's shared tokens, into s.
 __device__ __forceinline__ void find_runs(const PrefixArgs &a, Shared &s, Scratch &c, int team, int block, int ps_shift,
                                           bool list)
 {
     const int i = threadIdx.x & 127, lane = threadIdx.x & 31, quarter = i >> 5;
-    const bool mine = team < 3 && block >= 0;
+    const uint32_t bar = 2 + team;
     const int r = block * kBlockReq + i;
     int lead = -1, len = 0;
-    if (mine && r < a.batch) {
+    if (r < a.batch) {
         len = shared_tokens(a, r, ps_shift);
         lead = len > 0 ? __ldcg(a.prefix_of + r) : -1;
     }
-    if (mine) {
-        c.lead[team][i] = lead;
-        c.len[team][i] = len;
-        c.most[team][i] = 0;
-    }
-    __syncthreads();
+    c.lead[team][i] = lead;
+    c.most[team][i] = 0;
+    named_barrier_sync(bar, 128);
     // whether request i goes on with the run of request i - 1
-    const bool goes_on = mine && i > 0 && len > 0 && c.lead[team][i - 1] == lead;
-    if (mine) {
-        const uint32_t m = __ballot_sync(0xFFFFFFFFu, goes_on);
-        if (lane == 0)
-            c.cont[team][quarter] = m;
+    const bool goes_on = i > 0 && len > 0 && c.lead[team][i - 1] == lead;
+    const bool starts = len > 0 && !goes_on;
+    const uint32_t cont = __ballot_sync(0xFFFFFFFFu, goes_on), heads = __ballot_sync(0xFFFFFFFFu, starts);
+    if (lane == 0) {
+        c.cont[team][quarter] = cont;
+        c.heads[team][quarter] = __popc(heads);
     }
-    __syncthreads();
+    named_barrier_sync(bar, 128);
+    // the nearest request at or before i that starts a run or shares nothing,
+    // and the nearest after i
     int head = i, next = kBlockReq;
-    if (mine) {
-        // the nearest request at or before i that starts a run or holds nothing
-        for (int k = quarter; k >= 0; --k) {
-            uint32_t z = ~c.cont[team][k];
-            if (k == quarter)
-                z &= 0xFFFFFFFFu >> (31 - lane);
-            if (z != 0) {
-                head = 32 * k + 31 - __clz(z);
-                break;
-            }
+    for (int k = quarter; k >= 0; --k) {
+        uint32_t z = ~c.cont[team][k];
+        if (k == quarter)
+            z &= 0xFFFFFFFFu >> (31 - lane);
+        if (z != 0) {
+            head = 32 * k + 31 - __clz(z);
+            break;
         }
-        // and the nearest after i
-        for (int k = quarter; k < 4; ++k) {
-            uint32_t z = ~c.cont[team][k];
-            if (k == quarter)
-                z &= lane == 31 ? 0u : 0xFFFFFFFFu << (lane + 1);
-            if (z != 0) {
-                next = 32 * k + __ffs(z) - 1;
-                break;
-            }
-        }
-        if (len > 0)
-            atomicMax(&c.most[team][head], len);
     }
-    __syncthreads();
-    const bool starts = mine && len > 0 && !goes_on;
+    for (int k = quarter; k < 4; ++k) {
+        uint32_t z = ~c.cont[team][k];
+        if (k == quarter)
+            z &= lane == 31 ? 0u : 0xFFFFFFFFu << (lane + 1);
+        if (z != 0) {
+            next = 32 * k + __ffs(z) - 1;
+            break;
+        }
+    }
+    if (len > 0)
+        atomicMax(&c.most[team][head], len);
+    named_barrier_sync(bar, 128);
     int64_t places = 0;
     Run run = {};
     if (starts) {
         run.first = r;
+        run.lead = lead;
         run.count = next - i;
         run.len = c.most[team][i];
         run.tiles = (run.len + kTok - 1) / kTok;
@@ -242,48 +273,44 @@ __device__ __forceinline__ void find_runs(const PrefixArgs &a, Shared &s, Scratc
         places *= a.num_kv_heads;
     }
     int64_t upto = places;
-    if (mine) {
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, off);
-            upto += lane >= off ? o : 0;
-        }
-        if (lane == 31)
-            c.warp_sum[team][quarter] = upto;
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+        upto += lane >= off ? o : 0;
     }
-    __syncthreads();
-    if (mine) {
-        int64_t before = 0, all = 0;
+    if (lane == 31)
+        c.warp_sum[team][quarter] = upto;
+    named_barrier_sync(bar, 128);
+    int64_t before = 0, all = 0;
+    int number = __popc(heads & ((1u << lane) - 1u)), of = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            before += k < quarter ? c.warp_sum[team][k] : 0;
-            all += c.warp_sum[team][k];
-        }
-        if (i == 0)
-            c.total[block] = all;
-        if (list) {
-            // its number among the block's runs: starts before i, counted by warp
-            const uint32_t heads = __ballot_sync(0xFFFFFFFFu, starts);
-            if (lane == 0)
-                s.part[quarter] = __popc(heads);
-            named_barrier_sync(2, 128);
-            int n = __popc(heads & ((1u << lane) - 1u)), of = 0;
-            for (int k = 0; k < 4; ++k) {
-                n += k < quarter ? static_cast<int>(s.part[k]) : 0;
-                of += static_cast<int>(s.part[k]);
-            }
-            run.start = before + upto - places;
-            if (starts)
-                s.runs[n] = run;
-            s.len[i] = len;
-            if (i == 0) {
-                s.w.n_runs = of;
-                s.w.block = block;
-                s.w.block_total = all;
-            }
+    for (int k = 0; k < 4; ++k) {
+        before += k < quarter ? c.warp_sum[team][k] : 0;
+        all += c.warp_sum[team][k];
+        number += k < quarter ? c.heads[team][k] : 0;
+        of += c.heads[team][k];
+    }
+    if (i == 0)
+        c.total[block] = all;
+    if (list) {
+        run.start = before + upto - places;
+        if (starts)
+            s.runs[number] = run;
+        s.len[i] = len;
+        if (i == 0) {
+            s.w.n_runs = of;
+            s.w.block = block;
+            s.w.block_total = all;
         }
     }
-    __syncthreads();
+}
+
+// Quotient of numbers that are not negative, nearly always of 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    if (((a | b) >> 32) == 0)
+        return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
 }
 
 // The job at place x of the line, by one thread; moves x past what this CTA does
@@ -308,22 +335,22 @@ __device__ __forceinline__ bool set_job(const PrefixArgs &a, Shared &s)
     const int64_t narrow = kBorderCost + static_cast<int64_t>(kNarrowCost) * run.tiles;
     const int64_t per_head = row_tiles / 2 * wide + (row_tiles & 1) * narrow;
     const int64_t in_run = at - run.start;
-    const int kvh = static_cast<int>(in_run / per_head);
+    const int kvh = static_cast<int>(quotient(in_run, per_head));
     const int64_t in_head = in_run - kvh * per_head;
-    const int pair = static_cast<int>(min(in_head / wide, static_cast<int64_t>(row_tiles / 2)));
+    const int pair = static_cast<int>(min(quotient(in_head, wide), static_cast<int64_t>(row_tiles / 2)));
     w.wide = pair < row_tiles / 2;
-    const int cost = w.wide ? kWideCost : kNarrowCost;
+    const int cost = w.wide ? kWideCost : kNarrowCost;     // (a share is longer: every CTA of a job has a tile)
     // places [job, job + size) of the line; tiles from `start` on
     const int64_t job = w.block_start + run.start + kvh * per_head + pair * wide, size = w.wide ? wide : narrow;
     const int64_t start = job + kBorderCost;
     const int64_t from = max(w.x - start, static_cast<int64_t>(0)), to = min(w.end - start, size - kBorderCost);
     w.x = min(w.end, job + size);
     // a tile is the CTA's in whose stretch its first place lies
-    w.tile0 = static_cast<int>((from + cost - 1) / cost);
-    w.tile1 = to <= 0 ? 0 : static_cast<int>((to + cost - 1) / cost);
+    w.tile0 = static_cast<int>(quotient(from + cost - 1, cost));
+    w.tile1 = to <= 0 ? 0 : static_cast<int>(quotient(to + cost - 1, cost));
     if (w.tile0 >= w.tile1)
         return false;
-    const int64_t c0 = start / w.share, c1 = (start + static_cast<int64_t>(run.tiles - 1) * cost) / w.share;
+    const int64_t c0 = quotient(start, w.share), c1 = quotient(start + static_cast<int64_t>(run.tiles - 1) * cost, w.share);
     w.c0 = static_cast<int>(c0);
     w.nsplit = static_cast<int>(c1 - c0) + 1;
     w.run_rows = all_rows;
@@ -332,139 +359,116 @@ __device__ __forceinline__ bool set_job(const PrefixArgs &a, Shared &s)
     w.row0 = 256 * pair;
     w.rows = min(all_rows - w.row0, w.wide ? 256 : 128);
     w.len = run.len;
-    w.lead = __ldcg(a.prefix_of + run.first);
+    w.lead = run.lead;
     return true;
 }
 
-template <int kKind, bool kPrecise>
-__global__ void __launch_bounds__(Build<kKind, kPrecise>::kThreads, 1)
-prefix_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                   const PrefixArgs a)
-{
-    using B = Build<kKind, kPrecise>;
-    constexpr int kTok = B::kTok, kThreads = B::kThreads;
-    constexpr bool kBlocks = B::kBlocks;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    Shared &s = *reinterpret_cast<Shared *>(sm + kData);
-    Scratch &scratch = *reinterpret_cast<Scratch *>(sm + kOffQ);
-    Bars &bar = s.bars;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int ps_shift = __ffs(a.page_size) - 1;
+// The job at hand as a warp works it off.
+struct Job {
+    bool wide;
+    int tile0, n_tiles, kvh, first, len;
+    const int32_t *bt;                       // the row of the table that is read
 
-    if (tid == 0) {
-        prefetch_tensor_map(&k_map);
-        prefetch_tensor_map(&v_map);
-        for (int i = 0; i < kWideStages; ++i) {
-            mbar_init(&bar.wide_landed[i], 1);
-            mbar_init(&bar.wide_empty[i], 4);
-        }
-        for (int i = 0; i < kNarrowStages; ++i) {
-            mbar_init(&bar.narrow_landed[i], 1);
-            mbar_init(&bar.narrow_empty[i], 4);
-        }
-        for (int i = 0; i < kBufs; ++i) {
-            mbar_init(&bar.full[i], B::kConvert ? 4 : 1);
-            mbar_init(&bar.free[i], 2);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 4);
-            mbar_init(&bar.o_done[i], 1);
-            mbar_init(&bar.drain[i], 1);
-        }
-        fence_mbar_init();
-        s.abort = 0;
-        s.bad_from = 0x7FFFFFFF;
-    }
-    grid_dependency_wait();
-
-    // ---------------------------------------------- this CTA's stretch of the line
-    const int n_blocks = (a.batch + kBlockReq - 1) / kBlockReq;
-    constexpr int kTeams = kThreads / 128 < 3 ? kThreads / 128 : 3;
-    for (int b0 = 0; b0 < n_blocks; b0 += kTeams) {
-        const int team = tid / 128;
-        find_runs<kTok>(a, s, scratch, team, team < kTeams && b0 + team < n_blocks ? b0 + team : -1, ps_shift, false);
-    }
-    if (tid == 0) {
-        Walk &w = s.w;
-        w.total = 0;
-        for (int b = 0; b < n_blocks; ++b)
-            w.total += scratch.total[b];
-        const int64_t even = (w.total + gridDim.x - 1) / gridDim.x;
-        w.share = max(even, static_cast<int64_t>(kMinTiles * kWideCost));
-        w.x = min(w.total, w.share * blockIdx.x);
-        w.end = min(w.total, w.x + w.share);
-        int b = 0;
-        int64_t start = 0;
-        if (w.x < w.end)
-            while (w.x >= start + scratch.total[b])
-                start += scratch.total[b++];
-        w.block = b;
-        w.block_start = start;
-    }
-    __syncthreads();
-    if (s.w.x >= s.w.end)
-        return;
-    if (warp == 0)
-        tmem_alloc(&s.tmem_slot, kTmemCols);
+    __device__ __forceinline__ Job(const PrefixArgs &a, const Shared &s)
+        : wide(s.w.wide), tile0(s.w.tile0), n_tiles(s.w.tile1 - s.w.tile0), kvh(s.w.kvh), first(s.w.first), len(s.w.len),
+          bt(a.block_table + static_cast<int64_t>(s.w.lead) * a.max_pages_per_seq)
     {
-        const int first = s.w.block;
-        __syncthreads();
-        find_runs<kTok>(a, s, scratch, tid / 128, tid < 128 ? first : -1, ps_shift, true);
     }
+    // of group gr: the first tile (of the job's), how far apart they are, and how many
+    __device__ __forceinline__ int first_tile(int gr) const { return wide ? 0 : gr; }
+    __device__ __forceinline__ int step() const { return wide ? 1 : 2; }
+    __device__ __forceinline__ int tiles(int gr) const { return (n_tiles - first_tile(gr) + step() - 1) / step(); }
+};
+
+// What went through the rings, the buffers and the barriers in the jobs before:
+// stages of either ring, tiles, tiles of the warp's group, jobs.
+struct Done {
+    uint32_t wide = 0, narrow = 0, tiles = 0, group = 0, jobs = 0;
+    __device__ __forceinline__ void add(const Job &j, int gr)
+    {
+        (j.wide ? wide : narrow) += 2 * j.n_tiles;
+        tiles += j.n_tiles;
+        group += j.tiles(gr);
+        ++jobs;
+    }
+};
+
+// One block-wide barrier opens a job: its numbers are in s.  False: there is none.
+// Another ends its work, by all but the results.
+__device__ __forceinline__ bool open_job(const Shared &s)
+{
+    __syncthreads();
+    return s.job_there;
+}
+__device__ __forceinline__ void end_job()
+{
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
-    const uint32_t tmem = s.tmem_slot;
+}
 
-    // What went through the rings, buffers and barriers in the jobs before:
-    // stages of either ring, K and V items, tiles of this thread's group, jobs.
-    uint32_t wide_done = 0, narrow_done = 0, items_done = 0, group_done = 0, jobs_done = 0;
-    volatile int *abort_flag = &s.abort;
-
-    const int gr = warp < 8 ? warp >> 2 : warp - B::kIssue; // group of a softmax or an issuing warp
-    const int m = tid & 127;
-    const int hkv = a.num_kv_heads, per_request = a.n_query * a.group;
+// The next job, found by the softmax warps.
+__device__ __forceinline__ void find_job(const PrefixArgs &a, Shared &s, Scratch &scratch, int ps_shift)
+{
+    named_barrier_sync(1, 256);              // the last job's numbers have been read
+    if (threadIdx.x >= 128)
+        return;
     for (;;) {
-        // ---------------------------------------------- the next job
-        if (tid == 0) {
+        if (threadIdx.x == 0) {
             Walk &w = s.w;
-            s.state = w.x >= w.end ? 0 : w.x >= w.block_start + w.block_total ? 2 : set_job(a, s) ? 1 : 3;
+            s.search = w.x >= w.end ? 0 : w.x >= w.block_start + w.block_total ? 2 : set_job(a, s) ? 1 : 3;
             s.bad_from = 0x7FFFFFFF;
+            s.job_there = s.search == 1;
         }
-        __syncthreads();
-        const int state = s.state;
-        if (state == 0)
-            break;
-        if (state != 1) {
-            const int block = s.w.block + 1;
-            __syncthreads();                               // everyone has read the state
-            if (state == 2) {
-                if (tid == 0)
-                    s.w.block_start += s.w.block_total;
-                find_runs<kTok>(a, s, scratch, tid / 128, tid < 128 ? block : -1, ps_shift, true);
-            }
-            continue;
+        named_barrier_sync(2, 128);
+        const int found = s.search, block = s.w.block + 1;
+        if (found < 2)
+            return;
+        named_barrier_sync(2, 128);          // everyone has read it
+        if (found == 2) {
+            if (threadIdx.x == 0)
+                s.w.block_start += s.w.block_total;
+            find_runs(a, s, scratch, 0, block, ps_shift, true);
+            named_barrier_sync(2, 128);
         }
-        const Walk &w = s.w;
-        const bool wide = w.wide, failed_before = s.abort != 0;
-        const int tile0 = w.tile0, tile1 = w.tile1, kvh = w.kvh, first = w.first;
-        const int step = wide ? 1 : 2;
-        const int n_tiles = tile1 - tile0;
-        const int mine0 = wide ? 0 : gr, mine = (n_tiles - mine0 + step - 1) / step;   // the group's tiles
-        const int tile_rows = wide ? min(128, w.rows - 128 * gr) : w.rows;             // rows of the group's row tile
-        const int32_t *bt = a.block_table + static_cast<int64_t>(w.lead) * a.max_pages_per_seq;
-        // place of the group's part: the job's, behind one of the same number per CTA
-        const int64_t place0 =
-            2 * (static_cast<int64_t>(first) * per_request * hkv +
-                 static_cast<int64_t>(kvh) * w.run_rows + w.row0) +
-            gr * (wide ? 128 : w.rows);
+    }
+}
 
-        // this thread's row (softmax groups)
+// ------------------------------------------------------------------ Q, softmax, the rows' results
+
+template <int kKind, bool kPrecise>
+__device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uint8_t *sm, uint32_t tmem, int warp)
+{
+    using B = Build<kKind, kPrecise>;
+    constexpr int kSBufs = B::kSBufs;
+    constexpr bool kBlocks = B::kBlocks;
+    Bars &bar = s.bars;
+    Scratch &scratch = *reinterpret_cast<Scratch *>(sm + kOffQ);
+    const int lane = threadIdx.x & 31, m = threadIdx.x & 127, gr = warp >> 2;
+    const int ps_shift = __ffs(a.page_size) - 1;
+    const int hkv = a.num_kv_heads, per_request = a.n_query * a.group;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t scol = tmem + lanes + kColS + 128u * gr, ocol = tmem + lanes + kColO + 128u * gr;
+    volatile int *abort_flag = &s.abort;
+    Done done;
+    for (;;) {
+        find_job(a, s, scratch, ps_shift);
+        if (!open_job(s))
+            return;
+        const Walk &w = s.w;
+        const Job job(a, s);
+        const bool wide = job.wide;
+        const int tile0 = job.tile0, tile1 = tile0 + job.n_tiles, kvh = job.kvh, first = job.first;
+        const int step = job.step(), mine0 = job.first_tile(gr), mine = job.tiles(gr);
+        const uint32_t group_done = done.group;
+        const int32_t *bt = job.bt;
+        const int tile_rows = wide ? min(128, w.rows - 128 * gr) : w.rows;             // of the group's row tile
+        // place of the group's part: the job's, behind one of the same number per CTA
+        const int64_t place0 = 2 * (static_cast<int64_t>(first) * per_request * hkv +
+                                    static_cast<int64_t>(kvh) * w.run_rows + w.row0) +
+                               gr * (wide ? 128 : w.rows);
         const int local = wide ? 128 * gr + m : m;
-        const bool row_valid = warp < 8 && m < tile_rows;
+        const bool row_valid = m < tile_rows;
         int64_t id = 0;
         int lim = 0x7FFFFFFF;                              // tokens the row sees (a slot without a row: no masks)
         if (row_valid) {
@@ -477,153 +481,145 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         // fp32 output: this row's sums so far are in its place, behind m_used by sums_mul
         [[maybe_unused]] float sums_mul = 1.f;
         float4 *const part = a.pre_o + (256ll * blockIdx.x + place0) * 32 + m;
-        int issued = 0;                                    // copying warp: stages or items it issued in this job
 
-        if (!failed_before) {
-            if (warp < 8) {
-                // ------------------------------------------ Q, then softmax
-                const float kv_scale = B::kConvert && !kBlocks ? a.k_scale[kvh] : 1.f;
-                const float signed_mul = a.qk_scale_log2 * kv_scale;
-                uint32_t qw[64];
-                int e = 0;
-                {
-                    uint32_t mx = 0;
-                    if (row_valid) {
-                        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + id * kHeadDim);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const uint4 v = __ldcg(src + i);
-                            qw[4 * i] = v.x; qw[4 * i + 1] = v.y; qw[4 * i + 2] = v.z; qw[4 * i + 3] = v.w;
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            qw[i] = 0u;
-                    }
-                    if constexpr (B::kConvert) {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            mx = max(mx, max(qw[i] & 0x7FFFu, (qw[i] >> 16) & 0x7FFFu));
-                        e = q_row_exponent(mx);
-                    }
-                }
-                // the scores' multiplier is not negative: a negative one turns q
-                const float mul = fabsf(signed_mul) * __int_as_float((127 - e) << 23);
-                if (wide || gr == 0) {
-                    uint8_t *qs = sm + kOffQ + gr * kQBytes;
-                    const float q_mul = signed_mul < 0.f ? -__int_as_float((127 + e) << 23) : __int_as_float((127 + e) << 23);
+        if (s.abort == 0) {                                // after an error nothing more is computed
+            const float kv_scale = B::kConvert && !kBlocks ? a.k_scale[kvh] : 1.f;
+            const float signed_mul = a.qk_scale_log2 * kv_scale;
+            uint32_t qw[64];
+            int e = 0;
+            {
+                uint32_t mx = 0;
+                if (row_valid) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + id * kHeadDim);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        uint32_t h[4];
+                        const uint4 v = __ldcg(src + i);
+                        qw[4 * i] = v.x; qw[4 * i + 1] = v.y; qw[4 * i + 2] = v.z; qw[4 * i + 3] = v.w;
+                    }
+                } else {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if constexpr (B::kConvert) {
-                                const float2 f = bf16x2_to_f32x2(qw[4 * i + k]);
-                                h[k] = f32x2_to_f16x2(f.x * q_mul, f.y * q_mul);
-                            } else {
-                                h[k] = qw[4 * i + k] ^ (signed_mul < 0.f ? 0x80008000u : 0u);
-                            }
+                    for (int i = 0; i < 64; ++i)
+                        qw[i] = 0u;
+                }
+                if constexpr (B::kConvert) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        mx = max(mx, max(qw[i] & 0x7FFFu, (qw[i] >> 16) & 0x7FFFu));
+                    e = q_row_exponent(mx);
+                }
+            }
+            // the scores' multiplier is not negative: a negative one turns q
+            const float mul = fabsf(signed_mul) * __int_as_float((127 - e) << 23);
+            if (wide || gr == 0) {
+                uint8_t *qs = sm + kOffQ + gr * kQBytes;
+                const float q_mul = signed_mul < 0.f ? -__int_as_float((127 + e) << 23) : __int_as_float((127 + e) << 23);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if constexpr (B::kConvert) {
+                            const float2 f = bf16x2_to_f32x2(qw[4 * i + k]);
+                            h[k] = f32x2_to_f16x2(f.x * q_mul, f.y * q_mul);
+                        } else {
+                            h[k] = qw[4 * i + k] ^ (signed_mul < 0.f ? 0x80008000u : 0u);
                         }
-                        *reinterpret_cast<uint4 *>(qs + (i >> 3) * (kQBytes / 2) + sw128_chunk(m, i & 7)) =
-                            make_uint4(h[0], h[1], h[2], h[3]);
                     }
-                    fence_proxy_async_smem();
+                    *reinterpret_cast<uint4 *>(qs + (i >> 3) * (kQBytes / 2) + sw128_chunk(m, i & 7)) =
+                        make_uint4(h[0], h[1], h[2], h[3]);
                 }
-                named_barrier_sync(1, 320);                // the softmax and the issuing warps
+                fence_proxy_async_smem();
+            }
+            named_barrier_sync(5, 320);                // the softmax and the issuing warps
 
-                const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-                const uint32_t scol = tmem + lanes + kColS + 128u * gr, ocol = tmem + lanes + kColO + 128u * gr;
-                // block-scaled: lane i has the exponents of the tile's block i,
-                // fetched a tile ahead (ek in the low byte, ev in the high one)
-                [[maybe_unused]] int exps = 0, exps_next = 0, page_next = -1;
-                const int blk = lane * kBlockTokens;
-                const auto page_at = [&](int tile) {
-                    const int tok = tile * kTok + blk;
-                    return lane < kTok / kBlockTokens && tile < tile1 && tok < w.len ? __ldcg(bt + (tok >> ps_shift)) : -1;
-                };
-                const auto exps_at = [&](int tile, int page) {
-                    if (page < 0 || page >= a.num_pages)
-                        return 0;
-                    const int64_t at = ((static_cast<int64_t>(page) * hkv + kvh) << (ps_shift - 4)) +
-                                       (((tile * kTok + blk) & (a.page_size - 1)) >> 4);
-                    const int ek = max(static_cast<int>(__ldcg(a.k_exp + at)), kReadKeyExpMin);
-                    const int ev = max(static_cast<int>(__ldcg(a.v_exp + at)), kReadValueExpMin);
-                    return (ek & 0xFF) | (min(ev, kReadValueExpMax) << 8);
-                };
+            // block-scaled: lane i has the exponents of the tile's block i,
+            // fetched a tile ahead (ek in the low byte, ev in the high one)
+            [[maybe_unused]] int exps = 0, exps_next = 0, page_next = -1;
+            const int blk = lane * kBlockTokens;
+            const auto page_at = [&](int tile) {
+                const int tok = tile * kTok + blk;
+                return lane < kTok / kBlockTokens && tile < tile1 && tok < w.len ? __ldcg(bt + (tok >> ps_shift)) : -1;
+            };
+            const auto exps_at = [&](int tile, int page) {
+                if (page < 0 || page >= a.num_pages)
+                    return 0;
+                const int64_t at = ((static_cast<int64_t>(page) * hkv + kvh) << (ps_shift - 4)) +
+                                   (((tile * kTok + blk) & (a.page_size - 1)) >> 4);
+                const int ek = max(static_cast<int>(__ldcg(a.k_exp + at)), kReadKeyExpMin);
+                const int ev = max(static_cast<int>(__ldcg(a.v_exp + at)), kReadValueExpMin);
+                return (ek & 0xFF) | (min(ev, kReadValueExpMax) << 8);
+            };
+            if constexpr (kBlocks) {
+                const int t = tile0 + mine0;
+                exps_next = exps_at(t, page_at(t));
+                page_next = page_at(t + step);
+            }
+            for (int i = 0; i < mine; ++i) {
+                const int tile = tile0 + mine0 + i * step;
+                const uint32_t gi = group_done + i, sb = gi % kSBufs;
                 if constexpr (kBlocks) {
-                    const int t = tile0 + mine0;
-                    exps_next = exps_at(t, page_at(t));
-                    page_next = page_at(t + step);
+                    exps = exps_next;
+                    exps_next = exps_at(tile + step, page_next);
+                    page_next = page_at(tile + 2 * step);
                 }
-                for (int i = 0; i < mine; ++i) {
-                    const int tile = tile0 + mine0 + i * step;
-                    if constexpr (kBlocks) {
-                        exps = exps_next;
-                        exps_next = exps_at(tile + step, page_next);
-                        page_next = page_at(tile + 2 * step);
+                if (!__all_sync(0xFFFFFFFFu, wait_or_abort(&bar.s_full[gr][sb], (gi / kSBufs) & 1, kCopyWaitLimitNs,
+                                                           abort_flag, 4u)))
+                    break;
+                tmem_fence_after_sync();
+                const uint32_t col = scol + 64u * sb;
+                uint32_t sv[kTok];
+                tmem_ld64(col, sv);
+                const int vis = lim - tile * kTok;     // columns below it are visible
+                if (!__all_sync(0xFFFFFFFFu, vis >= kTok)) {
+#pragma unroll
+                    for (int k = 0; k < kTok; ++k)
+                        sv[k] = k < vis ? sv[k] : 0xFF800000u;
+                }
+                // block q (16 columns) of the tile: its multiplier and its ev
+                [[maybe_unused]] float mk[4], ev[4];
+                if constexpr (kBlocks) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int x = __shfl_sync(0xFFFFFFFFu, exps, q);
+                        mk[q] = mul * __int_as_float((127 + static_cast<int8_t>(x & 0xFF)) << 23);
+                        ev[q] = static_cast<float>(x >> 8);
                     }
-                    if (!__all_sync(0xFFFFFFFFu, wait_or_abort(&bar.s_full[gr], (group_done + i) & 1, kCopyWaitLimitNs,
+                }
+                // ---- the tile's largest score
+                float mx = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 16 * q; k < 16 * q + 16; k += 4) {
+                        top[0] = fmaxf(top[0], fmaxf(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])));
+                        top[1] = fmaxf(top[1], fmaxf(__uint_as_float(sv[k + 2]), __uint_as_float(sv[k + 3])));
+                    }
+                    const float t = fmaxf(top[0], top[1]);
+                    if constexpr (kBlocks)
+                        mx = t != -INFINITY ? fmaxf(mx, fmaf(t, mk[q], ev[q])) : mx;
+                    else
+                        mx = fmaxf(mx, t);
+                }
+                if constexpr (!kBlocks)
+                    mx = mx == -INFINITY ? mx : mx * mul;
+                const bool raise = row_valid && mx > m_used + kRaiseThreshold;
+                const float alpha = raise ? (m_used == -INFINITY ? 0.f : fast_exp2(m_used - mx)) : 1.f;
+                // fp32 output: O goes out of tensor memory every kFlush tiles
+                // into fp32 sums that round (the tensor core cuts what it adds
+                // to a large accumulator towards zero).
+                const bool flush = kPrecise && i > 0 && i % kFlush == 0;
+                const bool rescale = raise && m_used != -INFINITY && i > 0 && !flush;
+                if (__any_sync(0xFFFFFFFFu, rescale) || flush) {
+                    // O holds the group's earlier tiles once O += P V of the last one is done
+                    if (!__all_sync(0xFFFFFFFFu, wait_or_abort(&bar.o_done[gr], (gi - 1) & 1, kCopyWaitLimitNs,
                                                                abort_flag, 4u)))
                         break;
                     tmem_fence_after_sync();
-                    const int vis = lim - tile * kTok;     // columns below it are visible
-                    const bool all = __all_sync(0xFFFFFFFFu, vis >= kTok);
-                    // ev and the multiplier of block q (16 columns) of the tile
-                    const auto block = [&](int q, float &mk, float &ev) {
-                        mk = mul;
-                        ev = 0.f;
-                        if constexpr (kBlocks) {
-                            const int x = __shfl_sync(0xFFFFFFFFu, exps, q);
-                            mk = mul * __int_as_float((127 + static_cast<int8_t>(x & 0xFF)) << 23);
-                            ev = static_cast<float>(x >> 8);
-                        }
-                    };
-                    // ---- the tile's largest score
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < kTok / 32; ++c) {
-                        uint32_t sv[32];
-                        tmem_ld32(scol + 32u * c, sv);
-                        if (!all) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                sv[k] = 32 * c + k < vis ? sv[k] : 0xFF800000u;
-                        }
-                        float half[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2)
-                            half[k / 16] = fmaxf(half[k / 16], fmaxf(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])));
-                        if constexpr (kBlocks) {
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                float mk, ev;
-                                block(2 * c + q, mk, ev);
-                                if (half[q] != -INFINITY)
-                                    mx = fmaxf(mx, fmaf(half[q], mk, ev));
-                            }
-                        } else {
-                            mx = fmaxf(mx, fmaxf(half[0], half[1]));
-                        }
-                    }
-                    if constexpr (!kBlocks)
-                        mx = mx == -INFINITY ? mx : mx * mul;
-                    const bool raise = row_valid && mx > m_used + kRaiseThreshold;
-                    const float alpha = raise ? (m_used == -INFINITY ? 0.f : fast_exp2(m_used - mx)) : 1.f;
-                    // O += P V of the group's last tile was done before S of this one was issued.
-                    // fp32 output: O goes out of tensor memory every kFlush tiles
-                    // into fp32 sums that round (the tensor core cuts what it adds
-                    // to a large accumulator towards zero).
-                    const bool flush = kPrecise && i > 0 && i % kFlush == 0;
-                    const bool rescale = raise && m_used != -INFINITY && i > 0 && !flush;
-                    if constexpr (kPrecise) {
-                        if (flush) {
-                            flush_sums(ocol, part, tile_rows, row_valid, i > kFlush, sums_mul);
-                            sums_mul = 1.f;
-                        }
-                        if (raise)
-                            sums_mul *= alpha;
-                    }
-                    if (__any_sync(0xFFFFFFFFu, rescale)) {
+                    if (flush) {
+                        flush_sums(ocol, part, tile_rows, row_valid, i > kFlush, sums_mul);
+                        sums_mul = 1.f;
+                    } else {
                         const float f = rescale ? alpha : 1.f;
 #pragma unroll 1
                         for (int c = 0; c < 8; ++c) {
@@ -635,297 +631,78 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                             tmem_st16(ocol + 16u * c, o);
                         }
                     }
-                    if (raise) {
-                        l_sum *= alpha;
-                        m_used = mx;
-                    }
-                    // ---- P = 2^(s - m_used + kLift), written over S
-                    const float base = (m_used == -INFINITY ? 0.f : m_used) - B::kLift;
-                    float sum = 0.f;
-                    uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-#pragma unroll
-                    for (int c = 0; c < kTok / 32; ++c) {
-                        uint32_t sv[32];
-                        tmem_ld32(scol + 32u * c, sv);
-                        float p[32];
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            float mk, ev;
-                            block(2 * c + q, mk, ev);
-                            const uint64_t mk2 = f2_pack(mk, mk), off2 = f2_pack(ev - base, ev - base);
-#pragma unroll
-                            for (int k = 16 * q; k < 16 * q + 16; k += 2) {
-                                float x0, x1;
-                                f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), mk2, off2),
-                                          x0, x1);
-                                if (!all) {
-                                    x0 = 32 * c + k < vis ? x0 : -INFINITY;
-                                    x1 = 32 * c + k + 1 < vis ? x1 : -INFINITY;
-                                }
-                                p[k] = fast_exp2(x0);
-                                p[k + 1] = fast_exp2(x1);
-                                sum2[(k >> 1) & 1] = f2_add(sum2[(k >> 1) & 1], f2_pack(p[k], p[k + 1]));
-                            }
-                            if constexpr (kBlocks) {       // a block's weights, times 2^-ev
-                                float s0, s1, s2, s3;
-                                f2_unpack(sum2[0], s0, s1);
-                                f2_unpack(sum2[1], s2, s3);
-                                sum = fmaf((s0 + s1) + (s2 + s3), __int_as_float((127 - static_cast<int>(ev)) << 23), sum);
-                                sum2[0] = sum2[1] = f2_pack(0.f, 0.f);
-                            }
-                        }
-                        // the terms of P, each what the rounding of those before it dropped
-#pragma unroll
-                        for (int t = 0; t < B::kTerms; ++t) {
-                            uint32_t h[16];
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                h[k] = B::kConvert ? f32x2_to_f16x2(p[2 * k], p[2 * k + 1])
-                                                   : f32x2_to_bf16x2(p[2 * k], p[2 * k + 1]);
-                                if (t + 1 < B::kTerms) {
-                                    const float2 f = B::kConvert ? f16x2_to_f32x2(h[k]) : bf16x2_to_f32x2(h[k]);
-                                    p[2 * k] -= f.x;
-                                    p[2 * k + 1] -= f.y;
-                                }
-                            }
-                            tmem_st16(scol + p_column<B::kTerms>(c, t), h);
-                        }
-                    }
-                    if constexpr (!kBlocks) {
-                        float s0, s1, s2, s3;
-                        f2_unpack(sum2[0], s0, s1);
-                        f2_unpack(sum2[1], s2, s3);
-                        sum = (s0 + s1) + (s2 + s3);
-                    }
-                    l_sum += sum;
-                    tmem_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&bar.p_full[gr]);
                 }
-                // the last tile's O += P V
-                if (mine > 0 && !*abort_flag)
-                    wait_or_abort(&bar.o_done[gr], (group_done + mine - 1) & 1, kCopyWaitLimitNs, abort_flag, 4u);
+                if (raise) {
+                    sums_mul *= alpha;
+                    l_sum *= alpha;
+                    m_used = mx;
+                }
+                // ---- P = 2^(s - m_used + kLift), written over S
+                const float base = (m_used == -INFINITY ? 0.f : m_used) - B::kLift;
+                float sum = 0.f;
+                uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float p[32];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float mq = kBlocks ? mk[2 * c + q] : mul, off = kBlocks ? ev[2 * c + q] - base : -base;
+                        const uint64_t mq2 = f2_pack(mq, mq), off2 = f2_pack(off, off);
+#pragma unroll
+                        for (int k = 16 * q; k < 16 * q + 16; k += 2) {
+                            float x0, x1;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[32 * c + k]), __uint_as_float(sv[32 * c + k + 1])),
+                                             mq2, off2), x0, x1);
+                            p[k] = fast_exp2(x0);
+                            p[k + 1] = fast_exp2(x1);
+                            sum2[(k >> 1) & 1] = f2_add(sum2[(k >> 1) & 1], f2_pack(p[k], p[k + 1]));
+                        }
+                        if constexpr (kBlocks) {       // a block's weights, times 2^-ev
+                            float s0, s1, s2, s3;
+                            f2_unpack(sum2[0], s0, s1);
+                            f2_unpack(sum2[1], s2, s3);
+                            sum = fmaf((s0 + s1) + (s2 + s3),
+                                       __int_as_float((127 - static_cast<int>(ev[2 * c + q])) << 23), sum);
+                            sum2[0] = sum2[1] = f2_pack(0.f, 0.f);
+                        }
+                    }
+                    // the terms of P, each what the rounding of those before it dropped
+#pragma unroll
+                    for (int t = 0; t < B::kTerms; ++t) {
+                        uint32_t h[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            h[k] = B::kConvert ? f32x2_to_f16x2(p[2 * k], p[2 * k + 1])
+                                               : f32x2_to_bf16x2(p[2 * k], p[2 * k + 1]);
+                            if (t + 1 < B::kTerms) {
+                                const float2 f = B::kConvert ? f16x2_to_f32x2(h[k]) : bf16x2_to_f32x2(h[k]);
+                                p[2 * k] -= f.x;
+                                p[2 * k + 1] -= f.y;
+                            }
+                        }
+                        tmem_st16(col + p_column<B::kTerms>(c, t), h);
+                    }
+                }
+                if constexpr (!kBlocks) {
+                    float s0, s1, s2, s3;
+                    f2_unpack(sum2[0], s0, s1);
+                    f2_unpack(sum2[1], s2, s3);
+                    sum = (s0 + s1) + (s2 + s3);
+                }
+                l_sum += sum;
+                tmem_fence_before_sync();
                 __syncwarp();
-                tmem_fence_after_sync();
-            } else if (warp >= B::kIssue) {
-                // ------------------------------------------ S = Q K^T and O += P V of one group
-                named_barrier_sync(1, 320);
-                if (lane == 0) {
-                    constexpr uint32_t idesc_s = idesc<!B::kConvert>(kTok, false), idesc_o = idesc<!B::kConvert>(128, true);
-                    const uint64_t dq = umma_desc(smem_addr(sm + kOffQ + (wide ? gr : 0) * kQBytes), 0, 1024);
-                    const uint64_t dk = umma_desc(smem_addr(sm + kOffBufs), 0, 1024);
-                    const uint64_t dv = umma_desc(smem_addr(sm + kOffBufs), B::kSliceBytes, 1024);
-                    const uint32_t scol = tmem + kColS + 128u * gr, ocol = tmem + kColO + 128u * gr;
-                    const uint64_t limit = B::kConvert ? kCopyWaitLimitNs : a.copy_wait_ns;
-                    const unsigned bit = B::kConvert ? 4u : 1u;
-                    int i = 0;                             // the group's tiles
-                    for (int j = 0; j < n_tiles; ++j) {
-                        const uint32_t k_item = items_done + 2 * j, v_item = k_item + 1;
-                        uint64_t *k_free = &bar.free[k_item % kBufs], *v_free = &bar.free[v_item % kBufs];
-                        if (!wide && (j & 1) != gr) {      // the other group's tile: nothing to read
-                            if (!wait_or_abort(&bar.full[k_item % kBufs], (k_item / kBufs) & 1, limit, abort_flag, bit))
-                                break;
-                            mbar_arrive(k_free);
-                            if (!wait_or_abort(&bar.full[v_item % kBufs], (v_item / kBufs) & 1, limit, abort_flag, bit))
-                                break;
-                            mbar_arrive(v_free);
-                            continue;
-                        }
-                        // S goes where P of the last tile was read from
-                        if (i > 0 && !wait_or_abort(&bar.o_done[gr], (group_done + i - 1) & 1, kCopyWaitLimitNs,
-                                                    abort_flag, 4u))
-                            break;
-                        if (!wait_or_abort(&bar.full[k_item % kBufs], (k_item / kBufs) & 1, limit, abort_flag, bit))
-                            break;
-                        tmem_fence_after_sync();
-                        const uint64_t kb = dk + (((k_item % kBufs) * B::kHalfBytes) >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            umma_f16(scol, dq + (((kk >> 2) * (kQBytes / 2) + (kk & 3) * 32) >> 4),
-                                     kb + (((kk >> 2) * B::kSliceBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
-                        umma_commit(&bar.s_full[gr]);
-                        umma_commit(k_free);
-                        if (!wait_or_abort(&bar.full[v_item % kBufs], (v_item / kBufs) & 1, limit, abort_flag, bit))
-                            break;
-                        if (!wait_or_abort(&bar.p_full[gr], (group_done + i) & 1, kCopyWaitLimitNs, abort_flag, 4u))
-                            break;
-                        tmem_fence_after_sync();
-                        const uint64_t vb = dv + (((v_item % kBufs) * B::kHalfBytes) >> 4);
-                        const bool onto = kPrecise ? i % kFlush != 0 : i > 0;
-#pragma unroll
-                        for (int t = 0; t < B::kTerms; ++t)
-#pragma unroll
-                            for (int kk = 0; kk < kTok / 16; ++kk)
-                                umma_f16_ts(ocol, scol + p_column<B::kTerms>(kk >> 1, t) + 8u * (kk & 1),
-                                            vb + static_cast<uint64_t>((kk * 2048) >> 4), idesc_o,
-                                            onto || t > 0 || kk > 0);
-                        umma_commit(&bar.o_done[gr]);
-                        umma_commit(v_free);
-                        ++i;
-                    }
-                    // nothing this lane issued may still run when the job ends
-                    umma_commit(&bar.drain[gr]);
-                    if (!mbar_wait_bounded(&bar.drain[gr], jobs_done & 1, kCopyWaitLimitNs))
-                        atomicOr(&g_umma_error, 4u);
-                }
-                __syncwarp();
-            } else if (warp == B::kCopy) {
-                // ------------------------------------------ copies of K's and V's rows
-                const uint64_t policy = l2_policy_evict_normal();
-                // boxes of a tile: one lane each; a box does not cross a page
-                constexpr int kMaxBox = B::kConvert ? kChunkTokens : kTok;
-                const int box = min(a.page_size, kMaxBox), boxes = kTok / box;
-                const int64_t outside = -256;              // rows no copy finds: zeros
-                const auto page_at = [&](int tile) {
-                    const int tok = tile * kTok + lane * box;
-                    return lane < boxes && tile < tile1 && tok < w.len ? __ldcg(bt + (tok >> ps_shift)) : -1;
-                };
-                int page = page_at(tile0);
-                bool ok = true;
-                for (int tile = tile0; ok && tile < tile1; ++tile) {
-                    const int tok = tile * kTok + lane * box;
-                    const bool held = lane < boxes && tok < w.len, fine = held && page >= 0 && page < a.num_pages;
-                    if (held && !fine)
-                        atomicMin(&s.bad_from, tok);
-                    const int y = static_cast<int>(
-                        fine ? (static_cast<int64_t>(page) * hkv + kvh) * a.page_size + (tok & (a.page_size - 1)) : outside);
-                    page = page_at(tile + 1);
-                    if constexpr (B::kConvert) {
-                        uint64_t *landed = wide ? bar.wide_landed : bar.narrow_landed;
-                        uint64_t *empty = wide ? bar.wide_empty : bar.narrow_empty;
-                        uint8_t *ring = sm + (wide ? kOffRingWide : kOffRingNarrow);
-                        const uint32_t before = wide ? wide_done : narrow_done;
-                        const int per = kStageTok / box;   // boxes of a stage
-                        for (int q = 0; ok && q < 2 * kTok / kStageTok; ++q) {
-                            const uint32_t n = before + issued;
-                            const uint32_t st = wide ? n % kWideStages : n % kNarrowStages;
-                            const uint32_t round = wide ? n / kWideStages : n / kNarrowStages;
-                            if (round > 0 && !__all_sync(0xFFFFFFFFu, wait_or_abort(&empty[st], (round - 1) & 1,
-                                                                                    kCopyWaitLimitNs, abort_flag, 4u))) {
-                                ok = false;
-                                break;
-                            }
-                            const bool is_v = q >= kTok / kStageTok;
-                            const int part0 = (is_v ? q - kTok / kStageTok : q) * per;
-                            if (lane == 0)
-                                mbar_arrive_expect_tx(&landed[st], kRingStage);
-                            __syncwarp();
-                            if (lane >= part0 && lane < part0 + per)
-                                tma_load_2d(ring + st * kRingStage + (lane - part0) * box * 128,
-                                            is_v ? static_cast<const void *>(&v_map) : static_cast<const void *>(&k_map),
-                                            0, y, &landed[st], policy);
-                            ++issued;
-                        }
-                    } else {
-                        for (int q = 0; q < 2; ++q) {
-                            const uint32_t item = items_done + issued, b = item % kBufs;
-                            if (item >= kBufs && !__all_sync(0xFFFFFFFFu, wait_or_abort(&bar.free[b], (item / kBufs - 1) & 1,
-                                                                                        kCopyWaitLimitNs, abort_flag, 4u))) {
-                                ok = false;
-                                break;
-                            }
-                            if (lane == 0)
-                                mbar_arrive_expect_tx(&bar.full[b], B::kHalfBytes);
-                            __syncwarp();
-                            if (lane < boxes)
-#pragma unroll
-                                for (int half = 0; half < 2; ++half)
-                                    tma_load_2d(sm + kOffBufs + b * B::kHalfBytes + half * B::kSliceBytes + lane * box * 128,
-                                                q ? static_cast<const void *>(&v_map) : static_cast<const void *>(&k_map),
-                                                64 * half, y, &bar.full[b], policy);
-                            ++issued;
-                        }
-                    }
-                }
-            } else if constexpr (B::kConvert) {
-                // ------------------------------------------ e4m3 -> f16 (exact)
-                const int ct = tid - 32 * B::kConv;        // 0 .. 127
-                const int c = ct & 7;                      // 16-byte chunk (16 dims) of a row
-                uint64_t *landed = wide ? bar.wide_landed : bar.narrow_landed;
-                uint64_t *empty = wide ? bar.wide_empty : bar.narrow_empty;
-                const uint8_t *ring = sm + (wide ? kOffRingWide : kOffRingNarrow);
-                const uint32_t before = wide ? wide_done : narrow_done;
-                constexpr int kPer = kTok / kStageTok;     // stages of an item
-                bool ok = true;
-                for (int it = 0; ok && it < 2 * n_tiles; ++it) {
-                    const uint32_t item = items_done + it, b = item % kBufs;
-                    uint8_t *to = sm + kOffBufs + b * B::kHalfBytes;
-#pragma unroll
-                    for (int part_of = 0; part_of < kPer; ++part_of) {
-                        const uint32_t n = before + it * kPer + part_of;
-                        const uint32_t st = wide ? n % kWideStages : n % kNarrowStages;
-                        const uint32_t round = wide ? n / kWideStages : n / kNarrowStages;
-                        // every lane polls; the warp goes on or gives up as one
-                        if (!__all_sync(0xFFFFFFFFu, wait_or_abort(&landed[st], round & 1, a.copy_wait_ns, abort_flag, 1u))) {
-                            ok = false;
-                            break;
-                        }
-                        if (part_of == 0 && item >= kBufs &&
-                            !__all_sync(0xFFFFFFFFu, wait_or_abort(&bar.free[b], (item / kBufs - 1) & 1, kCopyWaitLimitNs,
-                                                                   abort_flag, 4u))) {
-                            ok = false;
-                            break;
-                        }
-                        const uint8_t *from = ring + st * kRingStage;
-                        uint4 x[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int t = (ct >> 3) + 16 * k;
-                            x[k] = *reinterpret_cast<const uint4 *>(from + t * 128 + ((c ^ (t & 7)) << 4));
-                        }
-                        // chunk c of row t goes to the operand's chunks 2 c, 2 c + 1;
-                        // lanes with c >= 4 (the other slice, the same banks)
-                        // store theirs in the other order
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int t = (ct >> 3) + 16 * k + part_of * kStageTok;
-                            const uint32_t slice = static_cast<uint32_t>((c >> 2) * B::kSliceBytes);
-                            const uint32_t o0 = slice + sw128_chunk(t, 2 * (c & 3));
-                            const uint32_t o1 = slice + sw128_chunk(t, 2 * (c & 3) + 1);
-                            const bool swap = c >= 4;
-                            const uint32_t a0 = swap ? x[k].z : x[k].x, a1 = swap ? x[k].w : x[k].y;
-                            const uint32_t b0 = swap ? x[k].x : x[k].z, b1 = swap ? x[k].y : x[k].w;
-                            *reinterpret_cast<uint4 *>(to + (swap ? o1 : o0)) =
-                                make_uint4(lo16_e4m3x2_to_f16x2(a0), hi16_e4m3x2_to_f16x2(a0),
-                                           lo16_e4m3x2_to_f16x2(a1), hi16_e4m3x2_to_f16x2(a1));
-                            *reinterpret_cast<uint4 *>(to + (swap ? o0 : o1)) =
-                                make_uint4(lo16_e4m3x2_to_f16x2(b0), hi16_e4m3x2_to_f16x2(b0),
-                                           lo16_e4m3x2_to_f16x2(b1), hi16_e4m3x2_to_f16x2(b1));
-                        }
-                        fence_proxy_async_smem();          // the writes, for the tensor core;
-                        __syncwarp();                      // the ring reads, for the next copy
-                        if (lane == 0) {
-                            mbar_arrive(&empty[st]);
-                            if (part_of == kPer - 1)
-                                mbar_arrive(&bar.full[b]);
-                        }
-                    }
-                }
+                if (lane == 0)
+                    mbar_arrive(&bar.p_full[gr][sb]);
             }
+            // the last tile's O += P V
+            if (mine > 0 && !*abort_flag)
+                wait_or_abort(&bar.o_done[gr], (group_done + mine - 1) & 1, kCopyWaitLimitNs, abort_flag, 4u);
+            __syncwarp();
         }
-        tmem_fence_before_sync();
-        __syncthreads();                                   // every role has finished or given up
-        tmem_fence_after_sync();
+        end_job();
         const bool failed = s.abort != 0;
-        if (failed && !failed_before && warp == B::kCopy && lane == 0) {
-            // none of the copies in flight may land after the CTA has moved on
-            bool drained = true;
-            if constexpr (B::kConvert) {
-                const uint32_t n_st = wide ? kWideStages : kNarrowStages, all = (wide ? wide_done : narrow_done) + issued;
-                uint64_t *landed = wide ? bar.wide_landed : bar.narrow_landed;
-                for (uint32_t n = all - min(n_st, static_cast<uint32_t>(issued)); n < all; ++n)
-                    drained &= mbar_wait_bounded(&landed[n % n_st], (n / n_st) & 1, kCopyWaitLimitNs);
-            } else {
-                const uint32_t all = items_done + issued;
-                for (uint32_t n = all - min(static_cast<uint32_t>(kBufs), static_cast<uint32_t>(issued)); n < all; ++n)
-                    drained &= mbar_wait_bounded(&bar.full[n % kBufs], (n / kBufs) & 1, kCopyWaitLimitNs);
-            }
-            if (!drained)
-                atomicOr(&g_umma_error, 2u);
-        }
-        // ---------------------------------------------- the rows' results
-        if (warp < 8) {
+        {
             const int64_t place = 256ll * blockIdx.x + place0 + m;
             if (row_valid) {
                 float lse = l_sum == 0.f ? -INFINITY : l_sum == l_sum ? m_used + __log2f(l_sum) - B::kLift : INFINITY;
@@ -939,7 +716,6 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             if (!failed && mine > 0) {
                 const float vs = B::kConvert && !kBlocks ? a.v_scale[kvh] : 1.f;
                 const float wgt = l_sum == 0.f ? 0.f : vs / l_sum;
-                const uint32_t ocol = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kColO + 128u * gr;
 #pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
                     uint32_t o[16];
@@ -962,14 +738,389 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                         }
                 }
             }
-            tmem_fence_before_sync();
         }
-        (wide ? wide_done : narrow_done) += 2 * n_tiles * (kTok / (B::kConvert ? kStageTok : kTok));
-        items_done += 2 * n_tiles;
-        group_done += mine;
-        ++jobs_done;
-        __syncthreads();                                   // the job's numbers have been read
-        tmem_fence_after_sync();
+        tmem_fence_before_sync();
+        done.add(job, gr);
+    }
+}
+
+// ------------------------------------------------------------------ S = Q K^T and O += P V of one group
+
+template <int kKind, bool kPrecise>
+__device__ __forceinline__ void issue_role(const PrefixArgs &a, Shared &s, uint8_t *sm, uint32_t tmem, int gr)
+{
+    using B = Build<kKind, kPrecise>;
+    constexpr int kSBufs = B::kSBufs, kSlots = B::kSlots;
+    Bars &bar = s.bars;
+    volatile int *abort_flag = &s.abort;
+    Done done;
+    while (open_job(s)) {
+        const Job job(a, s);
+        const bool wide = job.wide;
+        const int step = job.step(), mine0 = job.first_tile(gr), mine = job.tiles(gr);
+        const uint32_t group_done = done.group, tiles_done = done.tiles;
+        if (s.abort == 0) {
+            named_barrier_sync(5, 320);                    // Q is there
+            tmem_fence_after_sync();
+            if (elect_one()) {
+                constexpr uint32_t idesc_s = idesc<!B::kConvert>(kTok, false), idesc_o = idesc<!B::kConvert>(128, true);
+                const uint64_t dq = umma_desc(smem_addr(sm + kOffQ + (wide ? gr : 0) * kQBytes), 0, 1024);
+                const uint64_t dk = umma_desc(smem_addr(sm + B::kOffBufs), 0, 1024);
+                const uint64_t dv = umma_desc(smem_addr(sm + B::kOffBufs + kHalfBytes), kSliceBytes, 1024);
+                const uint32_t scol = tmem + kColS + 128u * gr, ocol = tmem + kColO + 128u * gr;
+                const uint64_t limit = B::kConvert ? kCopyWaitLimitNs : a.copy_wait_ns;
+                const unsigned bit = B::kConvert ? 4u : 1u;
+                // S of the group's tile i, into its S buffer
+                const auto scores = [&](int i) {
+                    const uint32_t gi = group_done + i, tile = tiles_done + mine0 + i * step, slot = tile % kSlots;
+                    // P of the tile before was read from there
+                    if (i >= kSBufs && !wait_or_abort(&bar.o_done[gr], (gi - kSBufs) & 1, kCopyWaitLimitNs, abort_flag, 4u))
+                        return false;
+                    if (!wait_or_abort(&bar.full[2 * slot], (tile / kSlots) & 1, limit, abort_flag, bit))
+                        return false;
+                    tmem_fence_after_sync();
+                    const uint64_t kb = dk + ((slot * 2 * kHalfBytes) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_f16(scol + 64u * (gi % kSBufs), dq + (((kk >> 2) * (kQBytes / 2) + (kk & 3) * 32) >> 4),
+                                 kb + (((kk >> 2) * kSliceBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+                    umma_commit(&bar.s_full[gr][gi % kSBufs]);
+                    umma_commit(&bar.free[2 * slot]);
+                    if (!wide)                         // the other group does not read it
+                        umma_commit(&bar.free[2 * slot]);
+                    return true;
+                };
+                bool ok = true;
+                for (int i = 0; i < kSBufs && i < mine; ++i)
+                    ok = ok && scores(i);
+                for (int i = 0; ok && i < mine; ++i) {
+                    const uint32_t gi = group_done + i, tile = tiles_done + mine0 + i * step, slot = tile % kSlots;
+                    if (!wait_or_abort(&bar.full[2 * slot + 1], (tile / kSlots) & 1, limit, abort_flag, bit))
+                        break;
+                    if (!wait_or_abort(&bar.p_full[gr][gi % kSBufs], (gi / kSBufs) & 1, kCopyWaitLimitNs, abort_flag, 4u))
+                        break;
+                    tmem_fence_after_sync();
+                    const uint64_t vb = dv + ((slot * 2 * kHalfBytes) >> 4);
+                    const uint32_t pcol = scol + 64u * (gi % kSBufs);
+                    const bool onto = kPrecise ? i % kFlush != 0 : i > 0;
+#pragma unroll
+                    for (int t = 0; t < B::kTerms; ++t)
+#pragma unroll
+                        for (int kk = 0; kk < kTok / 16; ++kk)
+                            umma_f16_ts(ocol, pcol + p_column<B::kTerms>(kk >> 1, t) + 8u * (kk & 1),
+                                        vb + static_cast<uint64_t>((kk * 2048) >> 4), idesc_o,
+                                        onto || t > 0 || kk > 0);
+                    umma_commit(&bar.o_done[gr]);
+                    umma_commit(&bar.free[2 * slot + 1]);
+                    if (!wide)
+                        umma_commit(&bar.free[2 * slot + 1]);
+                    ok = i + kSBufs >= mine || scores(i + kSBufs);
+                }
+                // nothing this lane issued may still run when the job ends
+                umma_commit(&bar.drain[gr]);
+                if (!mbar_wait_bounded(&bar.drain[gr], done.jobs & 1, kCopyWaitLimitNs))
+                    atomicOr(&g_umma_error, 4u);
+            }
+            __syncwarp();
+        }
+        end_job();
+        done.add(job, gr);
+    }
+}
+
+// ------------------------------------------------------------------ copies of K's and V's rows
+
+template <int kKind, bool kPrecise>
+__device__ __forceinline__ void copy_role(const PrefixArgs &a, Shared &s, uint8_t *sm, const CUtensorMap &k_map,
+                                          const CUtensorMap &v_map)
+{
+    using B = Build<kKind, kPrecise>;
+    constexpr int kSlots = B::kSlots;
+    Bars &bar = s.bars;
+    const int lane = threadIdx.x & 31, hkv = a.num_kv_heads;
+    const int ps_shift = __ffs(a.page_size) - 1;
+    volatile int *abort_flag = &s.abort;
+    Done done;
+    while (open_job(s)) {
+        const Job job(a, s);
+        const bool wide = job.wide, failed_before = s.abort != 0;
+        const int tile0 = job.tile0, tile1 = tile0 + job.n_tiles, kvh = job.kvh;
+        const int32_t *bt = job.bt;
+        const uint32_t wide_done = done.wide, narrow_done = done.narrow, tiles_done = done.tiles;
+        uint32_t issued = 0;                               // stages or buffers in this job
+        if (!failed_before) {
+            const uint64_t policy = l2_policy_evict_normal();
+            // boxes of a tile: one lane each; a box does not cross a page
+            const int box = min(a.page_size, B::kConvert ? kChunkTokens : kTok), boxes = kTok / box;
+            const int64_t outside = -256;              // rows no copy finds: zeros
+            const auto page_at = [&](int tile) {
+                const int tok = tile * kTok + lane * box;
+                return lane < boxes && tile < tile1 && tok < job.len ? __ldcg(bt + (tok >> ps_shift)) : -1;
+            };
+            int page = page_at(tile0);
+            bool ok = true;
+            for (int tile = tile0; ok && tile < tile1; ++tile) {
+                const int tok = tile * kTok + lane * box;
+                const bool held = lane < boxes && tok < job.len, fine = held && page >= 0 && page < a.num_pages;
+                if (held && !fine)
+                    atomicMin(&s.bad_from, tok);
+                const int y = static_cast<int>(
+                    fine ? (static_cast<int64_t>(page) * hkv + kvh) * a.page_size + (tok & (a.page_size - 1)) : outside);
+                page = page_at(tile + 1);
+                const uint32_t t = tiles_done + (tile - tile0), slot = t % kSlots;
+                for (int q = 0; ok && q < 2; ++q) {    // K, then V
+                    const void *map = q ? static_cast<const void *>(&v_map) : static_cast<const void *>(&k_map);
+                    if constexpr (B::kConvert) {
+                        uint64_t *landed = wide ? bar.wide_landed : bar.narrow_landed;
+                        uint64_t *empty = wide ? bar.wide_empty : bar.narrow_empty;
+                        const uint32_t n = (wide ? wide_done : narrow_done) + issued;
+                        const uint32_t st = wide ? n % kWideStages : n % kNarrowStages;
+                        const uint32_t round = wide ? n / kWideStages : n / kNarrowStages;
+                        if (round > 0)
+                            ok = __all_sync(0xFFFFFFFFu, wait_or_abort(&empty[st], (round - 1) & 1, kCopyWaitLimitNs,
+                                                                       abort_flag, 4u));
+                        if (!ok)
+                            break;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(&landed[st], kRingStage);
+                        __syncwarp();
+                        if (lane < boxes)
+                            tma_load_2d(sm + (wide ? kOffRingWide : kOffRingNarrow) + st * kRingStage + lane * box * 128,
+                                        map, 0, y, &landed[st], policy);
+                    } else {
+                        const uint32_t b = 2 * slot + q;
+                        if (t >= kSlots)
+                            ok = __all_sync(0xFFFFFFFFu, wait_or_abort(&bar.free[b], (t / kSlots - 1) & 1,
+                                                                       kCopyWaitLimitNs, abort_flag, 4u));
+                        if (!ok)
+                            break;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(&bar.full[b], kHalfBytes);
+                        __syncwarp();
+                        if (lane < boxes)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half)
+                                tma_load_2d(sm + B::kOffBufs + b * kHalfBytes + half * kSliceBytes + lane * box * 128, map,
+                                            64 * half, y, &bar.full[b], policy);
+                    }
+                    ++issued;
+                }
+            }
+        }
+        end_job();
+        if (s.abort != 0 && !failed_before && lane == 0) {
+            // none of the copies in flight may land after the CTA has moved on
+            bool drained = true;
+            if constexpr (B::kConvert) {
+                const uint32_t n_st = wide ? kWideStages : kNarrowStages, all = (wide ? wide_done : narrow_done) + issued;
+                uint64_t *landed = wide ? bar.wide_landed : bar.narrow_landed;
+                for (uint32_t n = all - min(n_st, issued); n < all; ++n)
+                    drained &= mbar_wait_bounded(&landed[n % n_st], (n / n_st) & 1, kCopyWaitLimitNs);
+            } else {
+                const uint32_t all = 2 * tiles_done + issued;
+                for (uint32_t n = all - min(2u * kSlots, issued); n < all; ++n)
+                    drained &= mbar_wait_bounded(&bar.full[n % (2 * kSlots)], (n / (2 * kSlots)) & 1, kCopyWaitLimitNs);
+            }
+            if (!drained)
+                atomicOr(&g_umma_error, 2u);
+        }
+        __syncwarp();
+        done.add(job, 0);
+    }
+}
+
+// ------------------------------------------------------------------ e4m3 -> f16 (exact)
+
+template <int kKind, bool kPrecise>
+__device__ __forceinline__ void convert_role(const PrefixArgs &a, Shared &s, uint8_t *sm, int warp)
+{
+    using B = Build<kKind, kPrecise>;
+    constexpr int kSlots = B::kSlots;
+    Bars &bar = s.bars;
+    const int tid = threadIdx.x, lane = tid & 31;
+    volatile int *abort_flag = &s.abort;
+    Done done;
+    while (open_job(s)) {
+        const Job job(a, s);
+        const bool wide = job.wide;
+        const int n_tiles = job.n_tiles;
+        const uint32_t wide_done = done.wide, narrow_done = done.narrow, tiles_done = done.tiles;
+        if (s.abort == 0) {
+            // Warps 8 .. 11 convert K, 12 .. 15 V: what a warp waits for (the
+            // copy, the buffer, its own stores) the others do not.
+            const int ct = tid & 127, v = (warp - 8) >> 2;
+            const int c = ct & 7;                      // 16-byte chunk (16 dims) of a row
+            uint64_t *landed = wide ? bar.wide_landed : bar.narrow_landed;
+            uint64_t *empty = wide ? bar.wide_empty : bar.narrow_empty;
+            const uint8_t *ring = sm + (wide ? kOffRingWide : kOffRingNarrow);
+            const uint32_t before = wide ? wide_done : narrow_done;
+            // The next tile's rows are on their way while one's are
+            // converted.  Every lane polls; the warp goes on or gives up as one.
+            uint4 x[4], next[4];
+            const auto landed_at = [&](int j) {
+                const uint32_t n = before + 2 * j + v;
+                const uint32_t st = wide ? n % kWideStages : n % kNarrowStages;
+                const uint32_t round = wide ? n / kWideStages : n / kNarrowStages;
+                if (!__all_sync(0xFFFFFFFFu, wait_or_abort(&landed[st], round & 1, a.copy_wait_ns, abort_flag, 1u)))
+                    return false;
+                const uint8_t *from = ring + st * kRingStage;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int t = (ct >> 3) + 16 * k;
+                    next[k] = *reinterpret_cast<const uint4 *>(from + t * 128 + ((c ^ (t & 7)) << 4));
+                }
+                return true;
+            };
+            bool more = landed_at(0);
+            for (int j = 0; more && j < n_tiles; ++j) {
+                const uint32_t tile = tiles_done + j, b = 2 * (tile % kSlots) + v;
+                uint8_t *to = sm + B::kOffBufs + b * kHalfBytes;
+                const uint32_t n = before + 2 * j + v, st = wide ? n % kWideStages : n % kNarrowStages;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    x[k] = next[k];
+                if (j + 1 < n_tiles)
+                    more = landed_at(j + 1);
+                if (tile >= kSlots && !__all_sync(0xFFFFFFFFu, wait_or_abort(&bar.free[b], (tile / kSlots - 1) & 1,
+                                                                             kCopyWaitLimitNs, abort_flag, 4u)))
+                    break;
+                // chunk c of row t goes to the operand's chunks 2 c, 2 c + 1;
+                // lanes with c >= 4 (the other slice, the same banks) store
+                // theirs in the other order
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int t = (ct >> 3) + 16 * k;
+                    const uint32_t slice = static_cast<uint32_t>((c >> 2) * kSliceBytes);
+                    const uint32_t o0 = slice + sw128_chunk(t, 2 * (c & 3));
+                    const uint32_t o1 = slice + sw128_chunk(t, 2 * (c & 3) + 1);
+                    const bool swap = c >= 4;
+                    const uint32_t a0 = swap ? x[k].z : x[k].x, a1 = swap ? x[k].w : x[k].y;
+                    const uint32_t b0 = swap ? x[k].x : x[k].z, b1 = swap ? x[k].y : x[k].w;
+                    *reinterpret_cast<uint4 *>(to + (swap ? o1 : o0)) =
+                        make_uint4(lo16_e4m3x2_to_f16x2(a0), hi16_e4m3x2_to_f16x2(a0),
+                                   lo16_e4m3x2_to_f16x2(a1), hi16_e4m3x2_to_f16x2(a1));
+                    *reinterpret_cast<uint4 *>(to + (swap ? o0 : o1)) =
+                        make_uint4(lo16_e4m3x2_to_f16x2(b0), hi16_e4m3x2_to_f16x2(b0),
+                                   lo16_e4m3x2_to_f16x2(b1), hi16_e4m3x2_to_f16x2(b1));
+                }
+                fence_proxy_async_smem();              // the writes, for the tensor core;
+                __syncwarp();                          // the ring reads, for the next copy
+                if (lane == 0) {
+                    mbar_arrive(&empty[st]);
+                    mbar_arrive(&bar.full[b]);
+                }
+            }
+        }
+        end_job();
+        done.add(job, 0);
+    }
+}
+
+template <int kKind, bool kPrecise>
+__global__ void __launch_bounds__(Build<kKind, kPrecise>::kThreads, 1)
+prefix_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                   const PrefixArgs a)
+{
+    using B = Build<kKind, kPrecise>;
+    constexpr int kThreads = B::kThreads;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    Shared &s = *reinterpret_cast<Shared *>(sm + kData);
+    Scratch &scratch = *reinterpret_cast<Scratch *>(sm + kOffQ);
+    Bars &bar = s.bars;
+    const int tid = threadIdx.x;
+    const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // the same register for the whole warp
+    const int ps_shift = __ffs(a.page_size) - 1;
+
+    if (tid == 0) {
+        prefetch_tensor_map(&k_map);
+        prefetch_tensor_map(&v_map);
+        for (int i = 0; i < kWideStages; ++i) {
+            mbar_init(&bar.wide_landed[i], 1);
+            mbar_init(&bar.wide_empty[i], 4);
+        }
+        for (int i = 0; i < kNarrowStages; ++i) {
+            mbar_init(&bar.narrow_landed[i], 1);
+            mbar_init(&bar.narrow_empty[i], 4);
+        }
+        for (int i = 0; i < 2 * B::kSlots; ++i) {
+            mbar_init(&bar.full[i], B::kConvert ? 4 : 1);
+            mbar_init(&bar.free[i], 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            for (int k = 0; k < 2; ++k) {
+                mbar_init(&bar.s_full[i][k], 1);
+                mbar_init(&bar.p_full[i][k], 4);
+            }
+            mbar_init(&bar.o_done[i], 1);
+            mbar_init(&bar.drain[i], 1);
+        }
+        fence_mbar_init();
+        s.abort = 0;
+        s.bad_from = 0x7FFFFFFF;
+    }
+    grid_dependency_wait();
+    // The own pages' kernel may start beside this one: it reads nothing of it, and
+    // what was there before is there (decode_split_kernel, kSharing).
+    grid_launch_dependents();
+
+    // ---------------------------------------------- this CTA's stretch of the line
+    const int n_blocks = (a.batch + kBlockReq - 1) / kBlockReq;
+    constexpr int kTeams = kThreads / 128 < 3 ? kThreads / 128 : 3;
+    const int team = tid / 128;
+    for (int b = team; team < kTeams && b < n_blocks; b += kTeams)
+        find_runs(a, s, scratch, team, b, ps_shift, n_blocks == 1);
+    __syncthreads();
+    if (tid == 0) {
+        Walk &w = s.w;
+        w.total = 0;
+        for (int b = 0; b < n_blocks; ++b)
+            w.total += scratch.total[b];
+        const int64_t even = quotient(w.total + gridDim.x - 1, gridDim.x);
+        w.share = max(even, static_cast<int64_t>(kMinTiles * kWideCost));
+        w.x = min(w.total, w.share * blockIdx.x);
+        w.end = min(w.total, w.x + w.share);
+        int b = 0;
+        int64_t start = 0;
+        if (w.x < w.end)
+            while (w.x >= start + scratch.total[b])
+                start += scratch.total[b++];
+        w.block = b;
+        w.block_start = start;
+    }
+    __syncthreads();
+    if (s.w.x >= s.w.end)
+        return;
+    if (warp == 0)
+        tmem_alloc(&s.tmem_slot, kTmemCols);
+    if (n_blocks > 1 && tid < 128)                         // the runs of the block in which the stretch begins
+        find_runs(a, s, scratch, 0, s.w.block, ps_shift, true);
+    tmem_fence_before_sync();
+    __syncthreads();
+    tmem_fence_after_sync();
+    const uint32_t tmem = s.tmem_slot;
+
+    static_assert(!B::kConvert || 256 * 136 + 256 * 72 + 128 * 56 <= 640 * 96, "what the launch has");
+    if (warp < 8) {
+        if constexpr (B::kConvert)
+            more_registers<136>();
+        softmax_role<kKind, kPrecise>(a, s, sm, tmem, warp);
+    } else if (B::kConvert && warp < B::kCopy) {
+        if constexpr (B::kConvert) {
+            fewer_registers<72>();
+            convert_role<kKind, kPrecise>(a, s, sm, warp);
+        }
+    } else {
+        if constexpr (B::kConvert)
+            fewer_registers<56>();
+        if (warp == B::kCopy)
+            copy_role<kKind, kPrecise>(a, s, sm, k_map, v_map);
+        else if (warp < B::kIssue + 2)
+            issue_role<kKind, kPrecise>(a, s, sm, tmem, warp - B::kIssue);
+        else                                               // fills the warpgroup
+            while (open_job(s))
+                end_job();
     }
     tmem_fence_before_sync();
     __syncthreads();
@@ -982,41 +1133,44 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
 // ------------------------------------------------------------------ combine
 
 // out = sum_s w_s o_s / sum_s w_s with w_s = 2^(lse_s - max lse), over the parts
-// of the shared pages and of the row's own.  A warp takes two rows, even lanes
-// one and odd lanes the other, so that a load of the shared pages' parts, which
-// lie row beside row, uses whole sectors.  Zeros where any part is invalid
-// (lse NaN); a NaN sum (lse +inf) makes the row NaN.
+// of the shared pages and of the row's own.  A CTA takes two rows, even lanes one
+// and odd lanes the other, so that a load of the shared pages' parts, which lie
+// row beside row, uses whole sectors; its warps take the parts in turn, four of
+// any 16 in one trip.  Zeros where any part is invalid (lse NaN); a NaN sum (lse
+// +inf) makes the row NaN.
 constexpr int kCombineWarps = 4;
 __global__ void __launch_bounds__(32 * kCombineWarps)
 combine_prefix_kernel(const PrefixArgs a)
 {
-    const int lane = threadIdx.x % 32, col = lane >> 1;
-    const int64_t row = 2 * (static_cast<int64_t>(blockIdx.x) * kCombineWarps + threadIdx.x / 32) + (lane & 1);
+    __shared__ float4 s_sum[kCombineWarps][2][32];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, col = lane >> 1;
+    const int64_t row = 2 * static_cast<int64_t>(blockIdx.x) + (lane & 1);
     const int64_t per_request = static_cast<int64_t>(a.n_query) * a.num_q_heads;
     const int ps_shift = __ffs(a.page_size) - 1;
-    grid_dependency_wait();
     const bool real_row = row < a.batch * per_request;
+    const int b = real_row ? static_cast<int>(row / per_request) : 0;
+    const int in = static_cast<int>(row - b * per_request), hq = in % a.num_q_heads;
+    const int kvh = hq / a.group, r = in / a.num_q_heads * a.group + hq % a.group;
+    const int per = a.n_query > 1 ? kMultiRowsPerCta : kMaxGroup;
+    grid_dependency_wait();
     int np = 0, ns = 0;                                    // parts of the shared pages, and of the row's own
     bool narrow = false;
     int4 rec = make_int4(0, 0, 0, 0);
     int64_t own_at = 0;
-    const int per = a.n_query > 1 ? kMultiRowsPerCta : kMaxGroup;
     if (real_row) {
-        const int b = static_cast<int>(row / per_request);
+        // the row's records beside the request's numbers: one trip
+        rec = __ldcg(a.pre_rec + row);
+        const int2 pair =
+            __ldcg(a.ws_pairs + (static_cast<int64_t>(b) * a.num_kv_heads + kvh) * a.row_blocks + r / per);
         const int64_t real = __ldcg(a.seq_lens + b);
         const bool aborted = a.abort_flags != nullptr && __ldcg(a.abort_flags + b) != 0;
+        const int shared = shared_tokens(a, b, ps_shift);
         if (!aborted && real > 0 && real <= static_cast<int64_t>(a.max_pages_per_seq) << ps_shift) {
-            const int shared = shared_tokens(a, b, ps_shift);
             if (shared > 0) {
-                rec = __ldcg(a.pre_rec + row);
                 narrow = rec.y < 0;
                 np = narrow ? -2 * rec.y : rec.y;
             }
             if (real > shared) {
-                const int in = static_cast<int>(row % per_request), hq = in % a.num_q_heads;
-                const int kvh = hq / a.group, r = in / a.num_q_heads * a.group + hq % a.group;
-                const int2 pair =
-                    __ldcg(a.ws_pairs + (static_cast<int64_t>(b) * a.num_kv_heads + kvh) * a.row_blocks + r / per);
                 own_at = static_cast<int64_t>(pair.x) * per + r % per;
                 ns = pair.y;
             }
@@ -1030,73 +1184,78 @@ combine_prefix_kernel(const PrefixArgs a)
         return q < np ? __ldcg(a.pre_lse + place(q) + rec.w) : __ldcg(a.ws_lse + own_at + static_cast<int64_t>(q - np) * per);
     };
     const int most = max(nt, __shfl_xor_sync(0xFFFFFFFFu, nt, 1));
-    float M = -INFINITY;
-    bool bad = false;
-    for (int q = col; q < nt; q += 16) {
+    const float y0 = col < nt ? lse_of(col) : -INFINITY;
+    float M = y0;
+    int bad = y0 != y0;
+    for (int q = col + 16; q < nt; q += 16) {
         const float y = lse_of(q);
         bad |= y != y;
         M = fmaxf(M, y);
     }
-    int flag = bad;
 #pragma unroll
     for (int off = 2; off < 32; off <<= 1) {
         M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
-        flag |= __shfl_xor_sync(0xFFFFFFFFu, flag, off);
+        bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, off);
     }
-    float sum = 0.f;
-    for (int q = col; q < nt; q += 16) {
-        const float y = lse_of(q);
-        sum += y == -INFINITY ? 0.f : fast_exp2(y - M);
-    }
+    const auto weight = [&](float y) { return y == -INFINITY ? 0.f : fast_exp2(y - M); };
+    float sum = weight(y0);
+    for (int q = col + 16; q < nt; q += 16)
+        sum += weight(lse_of(q));
 #pragma unroll
     for (int off = 2; off < 32; off <<= 1)
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-    const float inv = flag || sum == 0.f ? 0.f : 1.f / sum;      // NaN stays
+    const float inv = bad || sum == 0.f ? 0.f : 1.f / sum;       // NaN stays
     float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     for (int q0 = 0; q0 < most; q0 += 16) {
         float wq = 0.f;
-        if (q0 + col < nt && inv != 0.f) {
-            const float y = lse_of(q0 + col);
-            wq = y == -INFINITY ? 0.f : fast_exp2(y - M) * inv;
-        }
-        const int n = min(16, most - q0);
-        for (int k0 = 0; k0 < n; k0 += 4) {
-            float4 v[4][2];
-            float wk[4];
+        if (q0 + col < nt && inv != 0.f)
+            wq = weight(q0 == 0 ? y0 : lse_of(q0 + col)) * inv;
+        float4 v[4][2];
+        float wk[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int q = q0 + k0 + k;
-                wk[k] = __shfl_sync(0xFFFFFFFFu, wq, (2 * (k0 + k) + (lane & 1)) & 31);
-                v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (q < nt && wk[k] != 0.f) {              // a part without weight may hold anything
-                    if (q < np) {
-                        const float4 *from = a.pre_o + place(q) * 32 + rec.w + static_cast<int64_t>(col) * rec.z;
-                        v[k][0] = __ldcg(from);
-                        v[k][1] = __ldcg(from + 16ll * rec.z);
-                    } else {
-                        const float4 *from = reinterpret_cast<const float4 *>(
-                                                 a.ws_o + (own_at + static_cast<int64_t>(q - np) * per) * kHeadDim) + col;
-                        v[k][0] = __ldcg(from);
-                        v[k][1] = __ldcg(from + 16);
-                    }
+        for (int k = 0; k < 4; ++k) {
+            const int i = kCombineWarps * k + warp, q = q0 + i;
+            wk[k] = __shfl_sync(0xFFFFFFFFu, wq, 2 * i + (lane & 1));
+            v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (q < nt && wk[k] != 0.f) {                  // a part without weight may hold anything
+                if (q < np) {
+                    const float4 *from = a.pre_o + place(q) * 32 + rec.w + static_cast<int64_t>(col) * rec.z;
+                    v[k][0] = __ldcg(from);
+                    v[k][1] = __ldcg(from + 16ll * rec.z);
+                } else {
+                    const float4 *from = reinterpret_cast<const float4 *>(
+                                             a.ws_o + (own_at + static_cast<int64_t>(q - np) * per) * kHeadDim) + col;
+                    v[k][0] = __ldcg(from);
+                    v[k][1] = __ldcg(from + 16);
                 }
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (wk[k] != 0.f)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        acc[h].x += wk[k] * v[k][h].x;
-                        acc[h].y += wk[k] * v[k][h].y;
-                        acc[h].z += wk[k] * v[k][h].z;
-                        acc[h].w += wk[k] * v[k][h].w;
-                    }
         }
-    }
-    if (real_row)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            store_row_value4(a.out, row * kHeadDim + 4 * col + 64 * h, acc[h], a.out_fp32);
+        for (int k = 0; k < 4; ++k)
+            if (wk[k] != 0.f)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    acc[h].x += wk[k] * v[k][h].x;
+                    acc[h].y += wk[k] * v[k][h].y;
+                    acc[h].z += wk[k] * v[k][h].z;
+                    acc[h].w += wk[k] * v[k][h].w;
+                }
+    }
+    s_sum[warp][lane & 1][col] = acc[0];
+    s_sum[warp][lane & 1][col + 16] = acc[1];
+    __syncthreads();
+    if (threadIdx.x >= 64)
+        return;
+    const int64_t to = 2 * static_cast<int64_t>(blockIdx.x) + warp;
+    if (to >= a.batch * per_request)
+        return;
+    float4 t = s_sum[0][warp][lane];
+#pragma unroll
+    for (int w = 1; w < kCombineWarps; ++w) {
+        const float4 u = s_sum[w][warp][lane];
+        t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+    }
+    store_row_value4(a.out, to * kHeadDim + 4 * lane, t, a.out_fp32);
 }
 
 cudaLaunchConfig_t dependent(dim3 grid, int threads, size_t smem, cudaStream_t stream, cudaLaunchAttribute (&attr)[1])
@@ -1153,10 +1312,10 @@ cudaError_t launch_prefix_rows(const PrefixArgs &a, const CUtensorMap &k_map, co
 
 cudaError_t launch_combine_prefix(const PrefixArgs &a, cudaStream_t stream)
 {
-    const int64_t rows = static_cast<int64_t>(a.batch) * a.n_query * a.num_q_heads, per = 2 * kCombineWarps;
+    const int64_t rows = static_cast<int64_t>(a.batch) * a.n_query * a.num_q_heads;
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg =
-        dependent(dim3(static_cast<unsigned>((rows + per - 1) / per)), 32 * kCombineWarps, 0, stream, attr);
+        dependent(dim3(static_cast<unsigned>((rows + 1) / 2)), 32 * kCombineWarps, 0, stream, attr);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, combine_prefix_kernel, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
