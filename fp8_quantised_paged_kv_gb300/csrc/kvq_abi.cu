@@ -491,12 +491,17 @@ kvq_status prepare_decode(const kvq_cache_desc *desc, const void *q, int32_t bat
                           int32_t max_pages_per_seq, const int32_t *seq_lens, float softmax_scale,
                           const uint8_t *abort_flags, void *out, int32_t out_dtype,
                           void *workspace, size_t workspace_bytes, int32_t num_splits,
-                          DecodeCall *call, int32_t n_query = 1, const View *view = nullptr)
+                          DecodeCall *call, int32_t n_query = 1, const View *view = nullptr,
+                          const Plan *given = nullptr, size_t given_bytes = 0)
 {
-    kvq_status st = make_plan(desc, batch, num_q_heads, max_pages_per_seq, num_splits, &call->plan,
-                              n_query, view);
-    if (st != KVQ_OK)
-        return st;
+    if (given != nullptr) {                          // a call over shared prefixes has made its plan
+        call->plan = *given;
+    } else {
+        const kvq_status st = make_plan(desc, batch, num_q_heads, max_pages_per_seq, num_splits, &call->plan,
+                                        n_query, view);
+        if (st != KVQ_OK)
+            return st;
+    }
     if (out_dtype != KVQ_OUT_BF16 && out_dtype != KVQ_OUT_FP32)
         return KVQ_ERR_INVALID_ARG;
     if (!std::isfinite(softmax_scale))
@@ -513,7 +518,7 @@ kvq_status prepare_decode(const kvq_cache_desc *desc, const void *q, int32_t bat
     }
     if (batch > 65535)
         return KVQ_ERR_UNSUPPORTED;
-    const size_t need = call->plan.bytes();
+    const size_t need = given != nullptr ? given_bytes : call->plan.bytes();
     if (workspace == nullptr || workspace_bytes < need)
         return KVQ_ERR_WORKSPACE;
     if (!aligned16(workspace))
@@ -1050,14 +1055,26 @@ kvq_status kvq_copy_pages(const kvq_cache_desc *desc, void *const *caches, int32
     return KVQ_OK;
 }
 
-// The plan of a call over shared prefixes: the requests' own pages as one
-// balanced launch whose every split goes to the workspace, and a place per
-// (CTA, row) that can meet for the parts of the shared pages.  No arrival
-// counters.
+// The plan of a call over shared prefixes.  Small ones run as the same call
+// without a window, each request over its own row: the shared pages' launch and the
+// joining of its parts cost 15 us before they gain anything.  Else the requests' own
+// pages are one balanced launch whose every split goes to the workspace, and
+// there is a place per (CTA, row) that can meet for the parts of the shared pages.
+// No form needs arrival counters.
+//
+// The border goes by what the tables allow, per 16 query rows (each 16 read the
+// pages again without sharing).  4 requests x 8 KV heads x 528 tokens (4 MB): 6.0 us
+// apart, 20.7 shared; 13 x 4 x 5,203, three query tokens (69 MB): 24.4 against 31.0;
+// 33 x 4 x 9,701 behind five prompts (328 MB): 31.4 against 36.9; 16 x 2 x 16,901
+// over a bf16 cache, 40 rows (277 MB, three times): 75 against 39; 24 x 8 x 9,000,
+// bf16, three prompts (885 MB): 54 against 58; 64 x 8 x 10,192 (1.3 GB): 124 against 52.
+constexpr int64_t kSharingMinBytes = 512ll << 20;
+
 struct PrefixPlan {
     Plan own;
+    bool sharing;
     int64_t places;
-    size_t lse_at, pairs_at, rec_at, pre_lse_at, pre_o_at, bytes;
+    size_t lse_at, pairs_at, rec_at, takers_at, kinds_at, pre_lse_at, pre_o_at, bytes;
     int32_t ctas;
 };
 
@@ -1071,11 +1088,20 @@ static kvq_status make_prefix_plan(const kvq_cache_desc *d, int32_t batch, int32
     const int g = num_q_heads / d->num_kv_heads;
     const bool bf16 = d->cache_dtype == KVQ_CACHE_BF16, multi = n_query > 1;
     Plan &own = p->own;
+    const int32_t row_blocks = multi ? (n_query * g + kvq::kMultiRowsPerCta - 1) / kvq::kMultiRowsPerCta : 1;
+    const int64_t max_ctx = static_cast<int64_t>(max_pages) * d->page_size;
+    const int64_t pairs = static_cast<int64_t>(batch > 0 ? batch : 1) * d->num_kv_heads * row_blocks;
+    p->sharing = static_cast<double>(pairs) * static_cast<double>(max_ctx) * (bf16 ? 512 : 256) >= kSharingMinBytes;
+    if (!p->sharing) {
+        if (own.resident_ctas > 0)                         // balanced: a launch of its own joins the splits
+            own.pair_bytes = static_cast<size_t>(pairs) * sizeof(int2);
+        p->bytes = own.bytes();
+        return KVQ_OK;
+    }
     own.umma = false;
     own.cluster = 0;
-    own.row_blocks = multi ? (n_query * g + kvq::kMultiRowsPerCta - 1) / kvq::kMultiRowsPerCta : 1;
-    const int64_t pairs = static_cast<int64_t>(batch > 0 ? batch : 1) * d->num_kv_heads * own.row_blocks;
-    if (!plan_balanced(pairs, static_cast<int64_t>(max_pages) * d->page_size, d->page_size, bf16, multi, &own))
+    own.row_blocks = row_blocks;
+    if (!plan_balanced(pairs, max_ctx, d->page_size, bf16, multi, &own))
         return KVQ_ERR_UNSUPPORTED;
     p->ctas = kvq::device_sm_count();
     const int64_t rows = static_cast<int64_t>(batch) * n_query * num_q_heads;
@@ -1091,6 +1117,8 @@ static kvq_status make_prefix_plan(const kvq_cache_desc *d, int32_t batch, int32
     p->lse_at = take(own.lse_bytes + own.o_bytes);
     p->pairs_at = take(static_cast<size_t>(pairs) * sizeof(int2));
     p->rec_at = take(static_cast<size_t>(rows) * sizeof(int4));
+    p->takers_at = take(sizeof(int32_t));
+    p->kinds_at = take(static_cast<size_t>(batch));
     p->pre_lse_at = take(static_cast<size_t>(p->places) * sizeof(float));
     p->pre_o_at = take(static_cast<size_t>(p->places) * kHeadDim * sizeof(float));
     p->bytes = at;
@@ -1119,73 +1147,43 @@ static kvq_status decode_prefix(const kvq_cache_desc *desc, const void *q, int32
     kvq_status st = make_prefix_plan(desc, batch, num_query_tokens, num_q_heads, max_pages_per_seq, blocks, &p);
     if (st != KVQ_OK)
         return st;
-    if (out_dtype != KVQ_OUT_BF16 && out_dtype != KVQ_OUT_FP32)
+    if (batch > 0 && (!prefix_of || !prefix_lens))
         return KVQ_ERR_INVALID_ARG;
-    if (!std::isfinite(softmax_scale))
-        return KVQ_ERR_INVALID_ARG;
-    if (batch == 0)
-        return KVQ_OK;
-    const bool bf16 = desc->cache_dtype == KVQ_CACHE_BF16;
-    if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !prefix_of || !prefix_lens || !out)
-        return KVQ_ERR_INVALID_ARG;
-    if (blocks ? !k_exp || !v_exp : !bf16 && (!k_scale || !v_scale))
-        return KVQ_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
-        return KVQ_ERR_INVALID_ARG;
-    if (workspace == nullptr || workspace_bytes < p.bytes)
-        return KVQ_ERR_WORKSPACE;
-    if (!aligned16(workspace))
-        return KVQ_ERR_INVALID_ARG;
+    const View view = {0, 0, blocks, k_exp, v_exp};
+    DecodeCall call;
+    st = prepare_decode(desc, q, batch, num_q_heads, k_cache, v_cache, k_scale, v_scale, block_table,
+                        max_pages_per_seq, seq_lens, softmax_scale, abort_flags, out, out_dtype, workspace,
+                        workspace_bytes, 0, &call, num_query_tokens, &view, &p.own, p.bytes);
+    if (st != KVQ_OK || batch == 0)
+        return st;
+    CUtensorMap km, vm, pk, pv;
+    if (!make_cache_map(&km, desc, k_cache) || !make_cache_map(&vm, desc, v_cache))
+        return KVQ_ERR_CUDA;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (!p.sharing)
+        return to_status(p.own.umma ? kvq::launch_decode_umma_view(call.args, km, vm, s)
+                         : blocks   ? kvq::launch_decode_blocks(call.args, km, vm, s)
+                                    : kvq::launch_decode_window(call.args, km, vm, s));
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     kvq::PrefixArgs a = {};
-    a.q = q;
-    a.k_scale = k_scale;
-    a.v_scale = v_scale;
-    a.k_exp = k_exp;
-    a.v_exp = v_exp;
-    a.block_table = block_table;
-    a.seq_lens = seq_lens;
-    a.abort_flags = abort_flags;
-    a.out = out;
+    static_cast<kvq::ViewArgs &>(a) = call.args;
+    a.counters = nullptr;
     a.ws_lse = reinterpret_cast<float *>(ws + p.lse_at);
     a.ws_o = reinterpret_cast<float *>(ws + p.lse_at + p.own.lse_bytes);
     a.ws_pairs = reinterpret_cast<int2 *>(ws + p.pairs_at);
     a.combine_apart = true;
-    a.batch = batch;
-    a.num_q_heads = num_q_heads;
-    a.num_kv_heads = desc->num_kv_heads;
-    a.group = num_q_heads / desc->num_kv_heads;
-    a.page_size = desc->page_size;
-    a.num_pages = desc->num_pages;
-    a.max_pages_per_seq = max_pages_per_seq;
-    a.split_tokens = p.own.split_tokens;
-    a.max_splits = p.own.max_splits;
-    a.resident_ctas = p.own.resident_ctas;
-    a.balanced_ctas = p.own.balanced_ctas;
-    a.unit_shift = p.own.unit_shift;
-    a.min_split_units = p.own.min_split_units;
-    a.pair_cost = p.own.pair_cost;
-    a.n_query = num_query_tokens;
-    a.row_blocks = p.own.row_blocks;
-    a.qk_scale_log2 = softmax_scale * 1.4426950408889634f;
-    a.copy_wait_ns = kvq::decode_copy_wait_ns();
-    a.out_fp32 = out_dtype == KVQ_OUT_FP32;
-    a.bf16_cache = bf16;
     a.prefix_of = prefix_of;
     a.prefix_lens = prefix_lens;
     a.pre_rec = reinterpret_cast<int4 *>(ws + p.rec_at);
+    a.own_takers = reinterpret_cast<int32_t *>(ws + p.takers_at);
+    a.kinds = ws + p.kinds_at;
     a.pre_lse = reinterpret_cast<float *>(ws + p.pre_lse_at);
     a.pre_o = reinterpret_cast<float4 *>(ws + p.pre_o_at);
     a.pre_ctas = p.ctas;
-    CUtensorMap km, vm, pk, pv;
-    if (!make_cache_map(&km, desc, k_cache) || !make_cache_map(&vm, desc, v_cache))
+    const bool bf16 = desc->cache_dtype == KVQ_CACHE_BF16;
+    const int box = kvq::prefix_box_tokens(desc->page_size, bf16);
+    if (bf16 && (!make_half_row_map(&pk, desc, k_cache, box) || !make_half_row_map(&pv, desc, v_cache, box)))
         return KVQ_ERR_CUDA;
-    if (bf16) {
-        const int box = kvq::prefix_box_tokens(desc->page_size, true);
-        if (!make_half_row_map(&pk, desc, k_cache, box) || !make_half_row_map(&pv, desc, v_cache, box))
-            return KVQ_ERR_CUDA;
-    }
-    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = kvq::launch_prefix_rows(a, bf16 ? pk : km, bf16 ? pv : vm, s);
     if (e == cudaSuccess)
         e = blocks ? kvq::launch_decode_own_blocks(a, km, vm, s) : kvq::launch_decode_own(a, km, vm, s);

@@ -733,6 +733,7 @@ template <bool kMulti>
 struct Share {
     int lines;                               // pairs (KV head x row block) per request
     int share, x, end;                       // S, the next place, the end of the CTA's places
+    int number;                              // of the share: the CTA's, but for kSharing
     int acc, u;                              // places before request r, places of each of its pairs
     int r;
     int64_t real;                            // tokens of request r
@@ -740,18 +741,19 @@ struct Share {
     Job job;                                 // the split at x
 
     // Places of each pair of request r.
-    __device__ __forceinline__ int places(const CallArgs &a, int r, int ps_shift, int64_t &real, int &shared) const
+    __device__ __forceinline__ int places(const CallArgs &a, int r, int ps_shift, int64_t &real, int &shared, Work &work) const
     {
         real = __ldcg(a.seq_lens + r);
         const bool aborted = a.abort_flags != nullptr && __ldcg(a.abort_flags + r) != 0;
-        shared = shared_tokens(a, r, ps_shift);
+        shared = shared_tokens(a, r, ps_shift, work);
         const int n = shown_units(a, real, aborted, shared, ps_shift);
         return n > 0 ? n + a.pair_cost : 0;
     }
 
     // False if the CTA has none.  Also writes the zeros of the requests that
-    // show nothing, one CTA each.  Called by the whole block.
-    __device__ __forceinline__ bool find(const CallArgs &a, int ps_shift)
+    // show nothing, one CTA each.  Called by the whole block.  kSharing: of the
+    // CTA's shares the turn-th; *past if there are none after it.
+    __device__ __forceinline__ bool find(const CallArgs &a, int ps_shift, int turn = 0, bool *past = nullptr)
     {
         __shared__ int s_sum[kWarps];
         __shared__ bool s_some;
@@ -763,8 +765,9 @@ struct Share {
         int64_t real = 0;
         int shared = 0;
         int mine = 0, first = 0;
+        Work work = {0, 0};
         for (int i = r0; i < r1; ++i) {
-            const int n = places(a, i, ps_shift, real, shared);
+            const int n = places(a, i, ps_shift, real, shared, work);
             first = i == r0 ? n : first;
             mine += n;
         }
@@ -778,6 +781,25 @@ struct Share {
             s_sum[warp] = upto;
         if (threadIdx.x == 0)
             s_some = false;
+        if constexpr (kSharing) {
+            __shared__ long long s_work[2][kWarps];
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                work.shared += __shfl_xor_sync(0xFFFFFFFFu, work.shared, off);
+                work.own += __shfl_xor_sync(0xFFFFFFFFu, work.own, off);
+            }
+            if (lane == 0) {
+                s_work[0][warp] = work.shared;
+                s_work[1][warp] = work.own;
+            }
+            __syncthreads();
+            work = {0, 0};
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                work.shared += s_work[0][w];
+                work.own += s_work[1][w];
+            }
+        }
         __syncthreads();
         int before = upto - mine, total = 0;
 #pragma unroll
@@ -788,25 +810,34 @@ struct Share {
         for (int64_t i = blockIdx.x; !kSharing && i < a.batch; i += gridDim.x) {
             int64_t unused;
             int unshared;
-            if (places(a, static_cast<int>(i), ps_shift, unused, unshared) == 0) {
+            if (places(a, static_cast<int>(i), ps_shift, unused, unshared, work) == 0) {
                 const int64_t n = static_cast<int64_t>(a.n_query) * a.num_q_heads * kHeadDim;
                 for (int64_t j = threadIdx.x; j < n; j += kThreads)
                     store_out(a.out, i * n + j, 0.f, a.out_fp32);
             }
         }
         const int all = total * lines;
-        const int wave = a.resident_ctas * (kMaxShareTokens >> a.unit_shift);
-        const int parts = a.resident_ctas * max((all + wave - 1) / wave, 1);
+        // (kSharing: the grid is what all SMs hold, its first `ctas` CTAs take the
+        // shares in turn, and the workspace has places for balanced_ctas of them)
+        const int ctas = own_ctas(a, work);
+        const int wave = ctas * (kMaxShareTokens >> a.unit_shift);
+        int parts = ctas * max((all + wave - 1) / wave, 1);
+        if constexpr (kSharing)
+            parts = min(parts, a.balanced_ctas);
         const int share = max(a.min_split_units, (all + parts - 1) / parts);
-        const int x = static_cast<int>(blockIdx.x) * share, end = min(all, x + share);
+        const int64_t mine_at = kSharing ? blockIdx.x + static_cast<int64_t>(turn) * ctas : blockIdx.x;
+        const bool none = mine_at * share >= all || (kSharing && static_cast<int>(blockIdx.x) >= ctas);
+        if constexpr (kSharing)
+            *past = none || (mine_at + ctas) * share >= all;
+        const int x = static_cast<int>(mine_at) * share, end = min(all, x + share);
         // the one thread whose requests hold place x
-        if (static_cast<int64_t>(blockIdx.x) * share < all && x >= before * lines && x < (before + mine) * lines) {
+        if (!none && x >= before * lines && x < (before + mine) * lines) {
             int sum = before, n = first, i = r0;
             if (m > 1)
-                for (n = places(a, i, ps_shift, real, shared); x >= (sum + n) * lines;
-                     n = places(a, ++i, ps_shift, real, shared))
+                for (n = places(a, i, ps_shift, real, shared, work); x >= (sum + n) * lines;
+                     n = places(a, ++i, ps_shift, real, shared, work))
                     sum += n;
-            *this = {lines, share, x, end, sum, n, i, real, shared, {}};
+            *this = {lines, share, x, end, static_cast<int>(mine_at), sum, n, i, real, shared, {}};
             s_some = set_job(a);
         }
         __syncthreads();
@@ -826,7 +857,7 @@ struct Share {
         job.b = r;
         job.kvh = kMulti ? line / a.row_blocks : line;
         job.rb = kMulti ? line % a.row_blocks : 0;
-        job.split = static_cast<int>(blockIdx.x) - c0;
+        job.split = (kSharing ? number : static_cast<int>(blockIdx.x)) - c0;
         job.nsplit = (start - a.pair_cost + u - 1) / share - c0 + 1;
         job.t0 = static_cast<int64_t>(from - start) << a.unit_shift;
         job.span = (to - from) << a.unit_shift;
@@ -860,7 +891,8 @@ struct Share {
             do {
                 if (++r >= a.batch)
                     return false;                          // only if the lengths changed meanwhile
-                u = places(a, r, ps_shift, real, shared);
+                Work unused;
+                u = places(a, r, ps_shift, real, shared, unused);
             } while (u == 0);
         }
         return set_job(a);
@@ -889,6 +921,10 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
                 prefetch_tensor_map(&v_map);
             }
             grid_launch_dependents();
+            // one thread looks for all: CTA 0 may write the number at any moment
+            if constexpr (kWindow)
+                if (__syncthreads_or(threadIdx.x == 0 && nothing_left(a)))
+                    return;
         } else {
             start_dependent(k_map, v_map);
         }
@@ -906,20 +942,29 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
             const bool balanced = a.resident_ctas > 0;
             const int ps_shift = __ffs(a.page_size) - 1;
             __shared__ Share<kMulti> share;
-            if (balanced && !share.find(a, ps_shift)) {
-                if (kSharing && blockIdx.x == 0)
+            if constexpr (kSharing) {
+                bool first = true, past = false;
+                for (int turn = 0; !past; ++turn) {
+                    if (share.find(a, ps_shift, turn, &past))
+                        do {
+                            job = share.job;
+                            run_split<kBf16Cache, kPreciseP, kCluster, kMulti, kWindow, kBlocks>(k_map, v_map, a, job,
+                                                                                                 first);
+                            first = false;
+                        } while (share.next(a, ps_shift));
+                }
+                if (blockIdx.x == 0)
                     grid_dependency_wait();
                 return;
             }
+            if (balanced && !share.find(a, ps_shift))
+                return;
             for (bool first = true;; first = false) {
                 if (balanced)
                     job = share.job;
                 run_split<kBf16Cache, kPreciseP, kCluster, kMulti, kWindow, kBlocks>(k_map, v_map, a, job, first);
-                if (!balanced || !share.next(a, ps_shift)) {
-                    if (kSharing && blockIdx.x == 0)
-                        grid_dependency_wait();
+                if (!balanced || !share.next(a, ps_shift))
                     return;
-                }
             }
         } else {
             run_split<kBf16Cache, kPreciseP, kCluster, kMulti, kWindow, kBlocks>(k_map, v_map, a, job, true);
@@ -981,7 +1026,7 @@ cudaError_t launch_split(const ArgsOf<kWindow> &a, const CUtensorMap &k_map, con
               static_cast<unsigned>(a.batch));
     if constexpr (kWindow && !kCluster)
         if (a.resident_ctas > 0)
-            grid = dim3(static_cast<unsigned>(a.balanced_ctas));
+            grid = dim3(static_cast<unsigned>(kSharing ? a.resident_ctas : a.balanced_ctas));
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = launch_config<kBf16, kCluster, kMulti, kWindow>(a, grid, stream, attr);
     e = cudaLaunchKernelEx(&cfg, decode_split_kernel<kBf16, kPrecise, kCluster, kMulti, kWindow, kBlocks>, k_map,

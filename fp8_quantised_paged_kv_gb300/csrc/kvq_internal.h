@@ -222,9 +222,13 @@ struct PrefixArgs : ViewArgs {
     // partials of the shared pages (kvq_prefix.cu)
     float *pre_lse;                          // a place per (CTA, row)
     float4 *pre_o;                           // 32 of each place
-    int4 *pre_rec;                           // [B][n][Hq]: first place, parts, the tile's rows, the row among them
+    int4 *pre_rec;                           // [B][n][Hq]: place of the first part; the CTAs that have one, negative
+                                             // if each has two; how far apart those are
+    uint8_t *kinds;                          // [B]: kSharedPart, kOwnPart
+    int32_t *own_takers;                     // CTAs of the own pages' kernel that have work; 0: not known yet
     int32_t pre_ctas;
 };
+constexpr int kSharedPart = 1, kOwnPart = 2;   // a request has parts of shared pages, of its own
 constexpr int kPrefixRows = 256;     // most rows of a CTA's job over shared pages
 // Over the shared pages (box heights of k_map and v_map: prefix_box_tokens),
 // over the requests' own pages past them, and the parts of both joined.

@@ -50,6 +50,8 @@ constexpr int kOffRingNarrow = kOffQ2, kOffRingWide = kOffQ2 + kQBytes;
 constexpr int kOffRingEnd = kOffRingWide + kWideStages * kRingStage;
 static_assert(kOffRingNarrow + kNarrowStages * kRingStage == kOffRingEnd, "both rings end where the buffers start");
 constexpr int kData = kOffRingEnd + 2 * 2 * kHalfBytes;
+constexpr int kStageStride = 132;                          // floats of a row on its way out
+static_assert(256 * kStageStride * 4 <= kData, "every row has room");
 
 // The most that differs between the builds.
 template <int kKind, bool kPrecise>
@@ -71,17 +73,21 @@ struct Build {
     // With converters whole warpgroups, which divide the launch's registers
     // (640 x 96) otherwise: 136 for the softmax, 72 for the converters, 56 for the rest.
     static constexpr int kThreads = kConvert ? 640 : 32 * (kIssue + 2);
+    // places of a tile of tokens for one row tile (0.91 us against 1.20 for two over
+    // e4m3, 0.99 against 1.60 with block scales, 0.98 against 1.03 over a bf16 cache;
+    // fp32 output 1.32 against 1.87, 1.41 against 2.28, 1.60 against 3.0)
+    static constexpr int kNarrowCost = kKind == kBf16 ? (kPrecise ? 4 : 7) : kKind == kFp8 ? 6 : 5;
     static constexpr float kLift = kConvert ? 7.f : -8.f;  // log2 of what P, l and O are larger by
 };
 
 constexpr int kBlockReq = 128;                             // a run does not cross a multiple of it
 constexpr int kMaxBlocks = 512;                            // of up to 65,535 requests
 constexpr int kMinTiles = 4;                               // of a CTA's share, in wide tiles
-constexpr int kWideCost = 8, kNarrowCost = 7;              // places of a tile of tokens by the row tiles served
+constexpr int kWideCost = 8;                               // places of a tile of tokens for two row tiles
 constexpr int kBorderCost = 40;                            // and of a border between two jobs
 
 constexpr uint32_t kColS = 0, kColO = 256;                 // + 128 for the second group
-constexpr int kFlush = 16;                                 // fp32 output: tiles between O's ways out of tensor memory
+constexpr int kFlush = 32;                                 // fp32 output: tiles between O's ways out of tensor memory
 
 // Column, from its S buffer's first, of term t of P for tokens 32 c .. 32 c + 31
 // of a tile.  P is written over scores that have been read.
@@ -124,6 +130,7 @@ struct Shared {
     uint32_t tmem_slot;
     int abort, bad_from;                                   // bad_from: first token whose page is out of range
     int search, job_there;                                 // for the next job: what find_job found
+    int skip;                                              // an earlier job met an error: nothing more is computed
     Walk w;
     Run runs[kBlockReq];
     int len[kBlockReq];                                    // shared tokens of each request of the block
@@ -137,6 +144,7 @@ struct Scratch {
     int heads[3][4];
     int64_t warp_sum[3][4];
     int64_t total[kMaxBlocks];
+    unsigned long long work[2];
 };
 static_assert(sizeof(Scratch) <= kQBytes, "the scratch fits in Q's place");
 
@@ -168,6 +176,17 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64])
                  : "r"(taddr)
                  : "memory");
 }
+
+// 16 columns stored; tmem_wait_put waits for all that this thread has stored.
+__device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 "
+                 "[%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                   "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_put() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // One thread of a whole warp.  What it alone issues needs no vote over the
 // operands, which a branch on the lane would cost the tensor-core instructions.
@@ -212,16 +231,20 @@ __device__ __forceinline__ void flush_sums(uint32_t ocol, float4 *part, int rows
 // The runs of a block of requests and their places on the line, worked out by
 // the 128 threads of a team.  c.total[block]: all its places.  list: also the
 // runs themselves and every request's shared tokens, into s.
+template <int kNarrowCost>
 __device__ __forceinline__ void find_runs(const PrefixArgs &a, Shared &s, Scratch &c, int team, int block, int ps_shift,
-                                          bool list)
+                                          bool list, Work *work = nullptr)
 {
     const int i = threadIdx.x & 127, lane = threadIdx.x & 31, quarter = i >> 5;
     const uint32_t bar = 2 + team;
     const int r = block * kBlockReq + i;
     int lead = -1, len = 0;
     if (r < a.batch) {
-        len = shared_tokens(a, r, ps_shift);
-        lead = len > 0 ? __ldcg(a.prefix_of + r) : -1;
+        const Tokens t = tokens_of(a, r, ps_shift);
+        len = t.shared;
+        lead = t.lead;
+        if (work != nullptr)
+            work->add(a, t);
     }
     c.lead[team][i] = lead;
     c.most[team][i] = 0;
@@ -315,6 +338,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
 
 // The job at place x of the line, by one thread; moves x past what this CTA does
 // of it.  False if that is nothing (x lies in the border).
+template <int kNarrowCost>
 __device__ __forceinline__ bool set_job(const PrefixArgs &a, Shared &s)
 {
     Walk &w = s.w;
@@ -408,6 +432,7 @@ __device__ __forceinline__ void end_job()
 }
 
 // The next job, found by the softmax warps.
+template <int kNarrowCost>
 __device__ __forceinline__ void find_job(const PrefixArgs &a, Shared &s, Scratch &scratch, int ps_shift)
 {
     named_barrier_sync(1, 256);              // the last job's numbers have been read
@@ -416,9 +441,12 @@ __device__ __forceinline__ void find_job(const PrefixArgs &a, Shared &s, Scratch
     for (;;) {
         if (threadIdx.x == 0) {
             Walk &w = s.w;
-            s.search = w.x >= w.end ? 0 : w.x >= w.block_start + w.block_total ? 2 : set_job(a, s) ? 1 : 3;
+            s.search = w.x >= w.end ? 0 : w.x >= w.block_start + w.block_total ? 2 : set_job<kNarrowCost>(a, s) ? 1 : 3;
             s.bad_from = 0x7FFFFFFF;
             s.job_there = s.search == 1;
+            // as the last job left it: a warp of the next one may raise the flag
+            // before others have looked, and all have to meet at its barriers
+            s.skip = s.abort;
         }
         named_barrier_sync(2, 128);
         const int found = s.search, block = s.w.block + 1;
@@ -428,7 +456,7 @@ __device__ __forceinline__ void find_job(const PrefixArgs &a, Shared &s, Scratch
         if (found == 2) {
             if (threadIdx.x == 0)
                 s.w.block_start += s.w.block_total;
-            find_runs(a, s, scratch, 0, block, ps_shift, true);
+            find_runs<kNarrowCost>(a, s, scratch, 0, block, ps_shift, true);
             named_barrier_sync(2, 128);
         }
     }
@@ -452,7 +480,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
     volatile int *abort_flag = &s.abort;
     Done done;
     for (;;) {
-        find_job(a, s, scratch, ps_shift);
+        find_job<B::kNarrowCost>(a, s, scratch, ps_shift);
         if (!open_job(s))
             return;
         const Walk &w = s.w;
@@ -478,58 +506,61 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
             lim = s.len[first % kBlockReq + req];
         }
         float m_used = -INFINITY, l_sum = 0.f;
-        // fp32 output: this row's sums so far are in its place, behind m_used by sums_mul
+        // fp32 output: this row's sums so far (four dims of all the tile's rows side
+        // by side, in the rows' places) are behind m_used by sums_mul
         [[maybe_unused]] float sums_mul = 1.f;
-        float4 *const part = a.pre_o + (256ll * blockIdx.x + place0) * 32 + m;
+        [[maybe_unused]] float4 *const sums = a.pre_o + (256ll * blockIdx.x + place0) * 32 + m;
 
-        if (s.abort == 0) {                                // after an error nothing more is computed
+        if (!s.skip) {
             const float kv_scale = B::kConvert && !kBlocks ? a.k_scale[kvh] : 1.f;
             const float signed_mul = a.qk_scale_log2 * kv_scale;
-            uint32_t qw[64];
-            int e = 0;
-            {
-                uint32_t mx = 0;
-                if (row_valid) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + id * kHeadDim);
+            // A warp's 32 rows, two at a time: 16 lanes read a row (a row per lane
+            // touches 32 sectors a load: 4 us).  Over an FP8 cache a row is scaled by
+            // the power of two that puts its largest element in [2^14, 2^15).
+            // The scores' multiplier is not negative: a negative one turns q.
+            uint4 qv[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint4 v = __ldcg(src + i);
-                        qw[4 * i] = v.x; qw[4 * i + 1] = v.y; qw[4 * i + 2] = v.z; qw[4 * i + 3] = v.w;
+            for (int i = 0; i < 16; ++i) {
+                const int from = 2 * i + (lane >> 4);
+                const int64_t at = __shfl_sync(0xFFFFFFFFu, row_valid ? id : -1, from);
+                qv[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (at >= 0)
+                    qv[i] = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at * kHeadDim) +
+                                   (lane & 15));
+            }
+            int e = 0;
+            uint8_t *qs = sm + kOffQ + (wide ? gr : 0) * kQBytes + ((lane & 15) >> 3) * (kQBytes / 2);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int from = 2 * i + (lane >> 4), row = 32 * (warp & 3) + from;
+                uint32_t h[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+                if constexpr (B::kConvert) {
+                    uint32_t mx = 0;                       // of both halves
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mx = __vmaxu2(mx, h[k] & 0x7FFF7FFFu);
+                    mx = max(mx & 0xFFFFu, mx >> 16);
+#pragma unroll
+                    for (int off = 1; off < 16; off <<= 1)
+                        mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
+                    const int ei = q_row_exponent(mx), mine_e = __shfl_sync(0xFFFFFFFFu, ei, 16 * (lane & 1));
+                    e = lane >> 1 == i ? mine_e : e;
+                    const float q_mul = __int_as_float(((127 + ei) << 23) | (signed_mul < 0.f ? 0x80000000u : 0u));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = bf16x2_to_f32x2(h[k]);
+                        h[k] = f32x2_to_f16x2(f.x * q_mul, f.y * q_mul);
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        qw[i] = 0u;
+                    for (int k = 0; k < 4; ++k)
+                        h[k] ^= signed_mul < 0.f ? 0x80008000u : 0u;
                 }
-                if constexpr (B::kConvert) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        mx = max(mx, max(qw[i] & 0x7FFFu, (qw[i] >> 16) & 0x7FFFu));
-                    e = q_row_exponent(mx);
-                }
+                if (wide || gr == 0)
+                    *reinterpret_cast<uint4 *>(qs + sw128_chunk(row, lane & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
             }
-            // the scores' multiplier is not negative: a negative one turns q
             const float mul = fabsf(signed_mul) * __int_as_float((127 - e) << 23);
-            if (wide || gr == 0) {
-                uint8_t *qs = sm + kOffQ + gr * kQBytes;
-                const float q_mul = signed_mul < 0.f ? -__int_as_float((127 + e) << 23) : __int_as_float((127 + e) << 23);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    uint32_t h[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if constexpr (B::kConvert) {
-                            const float2 f = bf16x2_to_f32x2(qw[4 * i + k]);
-                            h[k] = f32x2_to_f16x2(f.x * q_mul, f.y * q_mul);
-                        } else {
-                            h[k] = qw[4 * i + k] ^ (signed_mul < 0.f ? 0x80008000u : 0u);
-                        }
-                    }
-                    *reinterpret_cast<uint4 *>(qs + (i >> 3) * (kQBytes / 2) + sw128_chunk(m, i & 7)) =
-                        make_uint4(h[0], h[1], h[2], h[3]);
-                }
-                fence_proxy_async_smem();
-            }
+            fence_proxy_async_smem();
             named_barrier_sync(5, 320);                // the softmax and the issuing warps
 
             // block-scaled: lane i has the exponents of the tile's block i,
@@ -617,7 +648,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
                         break;
                     tmem_fence_after_sync();
                     if (flush) {
-                        flush_sums(ocol, part, tile_rows, row_valid, i > kFlush, sums_mul);
+                        flush_sums(ocol, sums, tile_rows, row_valid, i > kFlush, sums_mul);
                         sums_mul = 1.f;
                     } else {
                         const float f = rescale ? alpha : 1.f;
@@ -680,7 +711,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
                                 p[2 * k + 1] -= f.y;
                             }
                         }
-                        tmem_st16(col + p_column<B::kTerms>(c, t), h);
+                        tmem_put16(col + p_column<B::kTerms>(c, t), h);
                     }
                 }
                 if constexpr (!kBlocks) {
@@ -690,6 +721,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
                     sum = (s0 + s1) + (s2 + s3);
                 }
                 l_sum += sum;
+                tmem_wait_put();
                 tmem_fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
@@ -710,33 +742,44 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
                     lse = __uint_as_float(0x7FC00000u);
                 a.pre_lse[place] = lse;
                 if (w.c0 == static_cast<int>(blockIdx.x) && (wide || gr == 0))
-                    a.pre_rec[id] = make_int4(static_cast<int>(256ll * w.c0 + place0), wide ? w.nsplit : -w.nsplit,
-                                              tile_rows, m);
+                    a.pre_rec[id] = make_int4(static_cast<int>(256ll * w.c0 + place0) + m, wide ? w.nsplit : -w.nsplit,
+                                              tile_rows, 0);
             }
             if (!failed && mine > 0) {
+                // O, weighted, through shared memory (the operands' place), so that
+                // a row's values leave as 512 bytes in a row
                 const float vs = B::kConvert && !kBlocks ? a.v_scale[kvh] : 1.f;
                 const float wgt = l_sum == 0.f ? 0.f : vs / l_sum;
+                float *stage = reinterpret_cast<float *>(sm) + warp * 32 * kStageStride;
 #pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
                     uint32_t o[16];
                     tmem_ld16(ocol + 16u * c, o);
-                    if (row_valid)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            float4 v = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                                   __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-                            float4 *at = part + (4 * c + k) * tile_rows;
-                            if (kPrecise && mine > kFlush) {
-                                const float4 u = *at;
-                                v.x = fmaf(u.x, sums_mul, v.x);
-                                v.y = fmaf(u.y, sums_mul, v.y);
-                                v.z = fmaf(u.z, sums_mul, v.z);
-                                v.w = fmaf(u.w, sums_mul, v.w);
-                            }
-                            *at = wgt != 0.f ? make_float4(v.x * wgt, v.y * wgt, v.z * wgt, v.w * wgt)
-                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k = 0; k < 4; ++k) {
+                        float4 v = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                               __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                        if (kPrecise && mine > kFlush && row_valid) {
+                            const float4 u = sums[(4 * c + k) * tile_rows];
+                            v.x = fmaf(u.x, sums_mul, v.x);
+                            v.y = fmaf(u.y, sums_mul, v.y);
+                            v.z = fmaf(u.z, sums_mul, v.z);
+                            v.w = fmaf(u.w, sums_mul, v.w);
                         }
+                        *reinterpret_cast<float4 *>(stage + lane * kStageStride + 16 * c + 4 * k) =
+                            wgt != 0.f ? make_float4(v.x * wgt, v.y * wgt, v.z * wgt, v.w * wgt)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
                 }
+                if (kPrecise && mine > kFlush)             // the sums lie where the rows go
+                    named_barrier_sync(6 + gr, 128);
+                __syncwarp();
+                float4 *to = a.pre_o + (256ll * blockIdx.x + place0 + 32 * (warp & 3)) * 32 + lane;
+                const int n = min(32, tile_rows - 32 * (warp & 3));
+#pragma unroll 4
+                for (int r = 0; r < n; ++r)
+                    to[32 * r] = *reinterpret_cast<const float4 *>(stage + r * kStageStride + 4 * lane);
+                fence_proxy_async_smem();                  // the reads, for the next job's copies
             }
         }
         tmem_fence_before_sync();
@@ -759,7 +802,7 @@ __device__ __forceinline__ void issue_role(const PrefixArgs &a, Shared &s, uint8
         const bool wide = job.wide;
         const int step = job.step(), mine0 = job.first_tile(gr), mine = job.tiles(gr);
         const uint32_t group_done = done.group, tiles_done = done.tiles;
-        if (s.abort == 0) {
+        if (!s.skip) {
             named_barrier_sync(5, 320);                    // Q is there
             tmem_fence_after_sync();
             if (elect_one()) {
@@ -843,7 +886,7 @@ __device__ __forceinline__ void copy_role(const PrefixArgs &a, Shared &s, uint8_
     Done done;
     while (open_job(s)) {
         const Job job(a, s);
-        const bool wide = job.wide, failed_before = s.abort != 0;
+        const bool wide = job.wide, failed_before = s.skip != 0;
         const int tile0 = job.tile0, tile1 = tile0 + job.n_tiles, kvh = job.kvh;
         const int32_t *bt = job.bt;
         const uint32_t wide_done = done.wide, narrow_done = done.narrow, tiles_done = done.tiles;
@@ -945,7 +988,7 @@ __device__ __forceinline__ void convert_role(const PrefixArgs &a, Shared &s, uin
         const bool wide = job.wide;
         const int n_tiles = job.n_tiles;
         const uint32_t wide_done = done.wide, narrow_done = done.narrow, tiles_done = done.tiles;
-        if (s.abort == 0) {
+        if (!s.skip) {
             // Warps 8 .. 11 convert K, 12 .. 15 V: what a warp waits for (the
             // copy, the buffer, its own stores) the others do not.
             const int ct = tid & 127, v = (warp - 8) >> 2;
@@ -1061,23 +1104,42 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         s.bad_from = 0x7FFFFFFF;
     }
     grid_dependency_wait();
-    // The own pages' kernel may start beside this one: it reads nothing of it, and
-    // what was there before is there (decode_split_kernel, kSharing).
+    // The own pages' kernel may start beside this one: it reads nothing of it but
+    // this zero, and what was there before is there (decode_split_kernel, kSharing).
+    // It may start as soon as one thread of each CTA has said so: the zero comes
+    // before any thread of its CTA does.
+    if (blockIdx.x == 0) {
+        if (tid == 0) {
+            __stcg(a.own_takers, 0);
+            __threadfence();
+        }
+        __syncthreads();
+    }
     grid_launch_dependents();
 
     // ---------------------------------------------- this CTA's stretch of the line
     const int n_blocks = (a.batch + kBlockReq - 1) / kBlockReq;
     constexpr int kTeams = kThreads / 128 < 3 ? kThreads / 128 : 3;
     const int team = tid / 128;
+    Work work = {0, 0};
+    if (tid == 0)
+        scratch.work[0] = scratch.work[1] = 0;
+    __syncthreads();
     for (int b = team; team < kTeams && b < n_blocks; b += kTeams)
-        find_runs(a, s, scratch, team, b, ps_shift, n_blocks == 1);
+        find_runs<B::kNarrowCost>(a, s, scratch, team, b, ps_shift, n_blocks == 1, &work);
+    if (work.shared + work.own != 0) {
+        atomicAdd(&scratch.work[0], static_cast<unsigned long long>(work.shared));
+        atomicAdd(&scratch.work[1], static_cast<unsigned long long>(work.own));
+    }
     __syncthreads();
     if (tid == 0) {
         Walk &w = s.w;
         w.total = 0;
         for (int b = 0; b < n_blocks; ++b)
             w.total += scratch.total[b];
-        const int64_t even = quotient(w.total + gridDim.x - 1, gridDim.x);
+        work = {static_cast<long long>(scratch.work[0]), static_cast<long long>(scratch.work[1])};
+        const int ctas = max(work.sms(gridDim.x), 1);
+        const int64_t even = quotient(w.total + ctas - 1, ctas);
         w.share = max(even, static_cast<int64_t>(kMinTiles * kWideCost));
         w.x = min(w.total, w.share * blockIdx.x);
         w.end = min(w.total, w.x + w.share);
@@ -1095,7 +1157,7 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     if (warp == 0)
         tmem_alloc(&s.tmem_slot, kTmemCols);
     if (n_blocks > 1 && tid < 128)                         // the runs of the block in which the stretch begins
-        find_runs(a, s, scratch, 0, s.w.block, ps_shift, true);
+        find_runs<B::kNarrowCost>(a, s, scratch, 0, s.w.block, ps_shift, true);
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
@@ -1133,129 +1195,131 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
 // ------------------------------------------------------------------ combine
 
 // out = sum_s w_s o_s / sum_s w_s with w_s = 2^(lse_s - max lse), over the parts
-// of the shared pages and of the row's own.  A CTA takes two rows, even lanes one
-// and odd lanes the other, so that a load of the shared pages' parts, which lie
-// row beside row, uses whole sectors; its warps take the parts in turn, four of
-// any 16 in one trip.  Zeros where any part is invalid (lse NaN); a NaN sum (lse
-// +inf) makes the row NaN.
-constexpr int kCombineWarps = 4;
-__global__ void __launch_bounds__(32 * kCombineWarps)
+// of the shared pages and of the row's own.  A lane has four dims of a row and
+// the log-sum-exps of every 32nd part; eight parts' values are in flight at a time.
+// Each trip to L2 depends on the one before (what parts there are, their
+// log-sum-exps, their values), so the first two are made for the next row beside
+// the third for this one.  Zeros where any part is invalid (lse NaN); a NaN sum
+// (lse +inf) makes the row NaN.
+//
+// kTogether warps share a row and take its parts in turn: all four of a CTA while
+// a CTA has no more than two rows, and so few trips to hide a row's behind (1,280
+// rows of 40 parts: 15 us after the parts are there with one warp), else one.
+constexpr int kCombineWarps = 4, kCombineCtas = 5;         // resident per SM
+struct Parts {
+    int4 rec;                                // of the shared pages: as in PrefixArgs
+    int64_t own_at;                          // place of the first own part's log-sum-exp
+    int np, nt;                              // parts of the shared pages, and all
+    float lse0, lse1;                        // of parts `lane` and lane + 32
+};
+template <int kTogether>
+__global__ void __launch_bounds__(32 * kCombineWarps, kCombineCtas)
 combine_prefix_kernel(const PrefixArgs a)
 {
-    __shared__ float4 s_sum[kCombineWarps][2][32];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, col = lane >> 1;
-    const int64_t row = 2 * static_cast<int64_t>(blockIdx.x) + (lane & 1);
-    const int64_t per_request = static_cast<int64_t>(a.n_query) * a.num_q_heads;
-    const int ps_shift = __ffs(a.page_size) - 1;
-    const bool real_row = row < a.batch * per_request;
-    const int b = real_row ? static_cast<int>(row / per_request) : 0;
-    const int in = static_cast<int>(row - b * per_request), hq = in % a.num_q_heads;
-    const int kvh = hq / a.group, r = in / a.num_q_heads * a.group + hq % a.group;
+    __shared__ float4 s_sum[kTogether][32];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    constexpr int kRows = kCombineWarps / kTogether;       // of a CTA at a time
+    static_assert(kTogether == 1 || kRows == 1, "a CTA's warps work together or alone");
+    const int64_t per_request = static_cast<int64_t>(a.n_query) * a.num_q_heads, rows = a.batch * per_request;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
     const int per = a.n_query > 1 ? kMultiRowsPerCta : kMaxGroup;
     grid_dependency_wait();
-    int np = 0, ns = 0;                                    // parts of the shared pages, and of the row's own
-    bool narrow = false;
-    int4 rec = make_int4(0, 0, 0, 0);
-    int64_t own_at = 0;
-    if (real_row) {
-        // the row's records beside the request's numbers: one trip
-        rec = __ldcg(a.pre_rec + row);
-        const int2 pair =
-            __ldcg(a.ws_pairs + (static_cast<int64_t>(b) * a.num_kv_heads + kvh) * a.row_blocks + r / per);
-        const int64_t real = __ldcg(a.seq_lens + b);
-        const bool aborted = a.abort_flags != nullptr && __ldcg(a.abort_flags + b) != 0;
-        const int shared = shared_tokens(a, b, ps_shift);
-        if (!aborted && real > 0 && real <= static_cast<int64_t>(a.max_pages_per_seq) << ps_shift) {
-            if (shared > 0) {
-                narrow = rec.y < 0;
-                np = narrow ? -2 * rec.y : rec.y;
-            }
-            if (real > shared) {
-                own_at = static_cast<int64_t>(pair.x) * per + r % per;
-                ns = pair.y;
-            }
+    const auto place = [&](const Parts &p, int q) -> int64_t {     // of part q < np
+        return static_cast<int64_t>(p.rec.x) + (p.rec.y < 0 ? 256ll * (q >> 1) + (q & 1) * p.rec.z : 256ll * q);
+    };
+    const auto lse_of = [&](const Parts &p, int q) {
+        return q < p.np ? __ldcg(a.pre_lse + place(p, q))
+                        : __ldcg(a.ws_lse + p.own_at + static_cast<int64_t>(q - p.np) * per);
+    };
+    const auto parts_of = [&](int64_t row) {
+        Parts p = {};
+        if (row < rows) {
+            const int b = static_cast<int>(row / per_request), in = static_cast<int>(row - b * per_request);
+            const int hq = in % a.num_q_heads, kvh = hq / a.group, r = in / a.num_q_heads * a.group + hq % a.group;
+            const int kind = __ldcg(a.kinds + b);
+            p.rec = __ldcg(a.pre_rec + row);
+            const int2 pair =
+                __ldcg(a.ws_pairs + (static_cast<int64_t>(b) * a.num_kv_heads + kvh) * a.row_blocks + r / per);
+            p.np = !(kind & kSharedPart) ? 0 : p.rec.y < 0 ? -2 * p.rec.y : p.rec.y;
+            p.nt = p.np + (kind & kOwnPart ? pair.y : 0);
+            p.own_at = static_cast<int64_t>(pair.x) * per + r % per;
         }
-    }
-    const int nt = np + ns;
-    const auto place = [&](int q) -> int64_t {             // of part q < np, its tile's first row
-        return static_cast<int64_t>(rec.x) + (narrow ? 256ll * (q >> 1) + (q & 1) * rec.z : 256ll * q);
+        return p;
     };
-    const auto lse_of = [&](int q) {
-        return q < np ? __ldcg(a.pre_lse + place(q) + rec.w) : __ldcg(a.ws_lse + own_at + static_cast<int64_t>(q - np) * per);
+    const auto fetch_lse = [&](Parts &p) {
+        p.lse0 = lane < p.nt ? lse_of(p, lane) : -INFINITY;
+        p.lse1 = lane + 32 < p.nt ? lse_of(p, lane + 32) : -INFINITY;
     };
-    const int most = max(nt, __shfl_xor_sync(0xFFFFFFFFu, nt, 1));
-    const float y0 = col < nt ? lse_of(col) : -INFINITY;
-    float M = y0;
-    int bad = y0 != y0;
-    for (int q = col + 16; q < nt; q += 16) {
-        const float y = lse_of(q);
-        bad |= y != y;
-        M = fmaxf(M, y);
-    }
+    int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + warp / kTogether;
+    Parts p = parts_of(row);
+    fetch_lse(p);
+    for (; row < rows; row += step) {
+        Parts next = parts_of(row + step);
+        float M = fmaxf(p.lse0, p.lse1);
+        bool bad = p.lse0 != p.lse0 || p.lse1 != p.lse1;
+        for (int q = lane + 64; q < p.nt; q += 32) {
+            const float y = lse_of(p, q);
+            bad |= y != y;
+            M = fmaxf(M, y);
+        }
+        bad = __any_sync(0xFFFFFFFFu, bad);
 #pragma unroll
-    for (int off = 2; off < 32; off <<= 1) {
-        M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
-        bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, off);
-    }
-    const auto weight = [&](float y) { return y == -INFINITY ? 0.f : fast_exp2(y - M); };
-    float sum = weight(y0);
-    for (int q = col + 16; q < nt; q += 16)
-        sum += weight(lse_of(q));
+        for (int off = 16; off > 0; off >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+        const auto weight = [&](float y) { return y == -INFINITY ? 0.f : fast_exp2(y - M); };
+        float sum = weight(p.lse0) + weight(p.lse1);
+        for (int q = lane + 64; q < p.nt; q += 32)
+            sum += weight(lse_of(p, q));
 #pragma unroll
-    for (int off = 2; off < 32; off <<= 1)
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-    const float inv = bad || sum == 0.f ? 0.f : 1.f / sum;       // NaN stays
-    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int q0 = 0; q0 < most; q0 += 16) {
-        float wq = 0.f;
-        if (q0 + col < nt && inv != 0.f)
-            wq = weight(q0 == 0 ? y0 : lse_of(q0 + col)) * inv;
-        float4 v[4][2];
-        float wk[4];
+        for (int off = 16; off > 0; off >>= 1)
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+        const float inv = bad || sum == 0.f ? 0.f : 1.f / sum;       // NaN stays
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q0 = 0; q0 < p.nt; q0 += 8 * kTogether) {
+            float4 v[8];
+            float wk[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int i = kCombineWarps * k + warp, q = q0 + i;
-            wk[k] = __shfl_sync(0xFFFFFFFFu, wq, 2 * i + (lane & 1));
-            v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (q < nt && wk[k] != 0.f) {                  // a part without weight may hold anything
-                if (q < np) {
-                    const float4 *from = a.pre_o + place(q) * 32 + rec.w + static_cast<int64_t>(col) * rec.z;
-                    v[k][0] = __ldcg(from);
-                    v[k][1] = __ldcg(from + 16ll * rec.z);
-                } else {
-                    const float4 *from = reinterpret_cast<const float4 *>(
-                                             a.ws_o + (own_at + static_cast<int64_t>(q - np) * per) * kHeadDim) + col;
-                    v[k][0] = __ldcg(from);
-                    v[k][1] = __ldcg(from + 16);
+            for (int k = 0; k < 8; ++k) {
+                const int q = q0 + kTogether * k + warp % kTogether;
+                float y = __shfl_sync(0xFFFFFFFFu, q < 32 ? p.lse0 : p.lse1, q % 32);
+                if (q >= 64)
+                    y = q < p.nt ? lse_of(p, q) : -INFINITY;
+                wk[k] = q < p.nt && inv != 0.f ? weight(y) * inv : 0.f;
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (wk[k] != 0.f)                          // a part without weight may hold anything
+                    v[k] = __ldcg((q < p.np ? a.pre_o + place(p, q) * 32
+                                            : reinterpret_cast<const float4 *>(a.ws_o) +
+                                                  (p.own_at + static_cast<int64_t>(q - p.np) * per) * 32) + lane);
+            }
+            if (q0 == 0)
+                fetch_lse(next);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (wk[k] != 0.f) {
+                    acc.x += wk[k] * v[k].x;
+                    acc.y += wk[k] * v[k].y;
+                    acc.z += wk[k] * v[k].z;
+                    acc.w += wk[k] * v[k].w;
+                }
+        }
+        if (p.nt == 0)
+            fetch_lse(next);
+        if constexpr (kTogether > 1) {
+            s_sum[warp][lane] = acc;
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int w = 1; w < kTogether; ++w) {
+                    const float4 u = s_sum[w][lane];
+                    acc.x += u.x; acc.y += u.y; acc.z += u.z; acc.w += u.w;
                 }
             }
+            __syncthreads();
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (wk[k] != 0.f)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    acc[h].x += wk[k] * v[k][h].x;
-                    acc[h].y += wk[k] * v[k][h].y;
-                    acc[h].z += wk[k] * v[k][h].z;
-                    acc[h].w += wk[k] * v[k][h].w;
-                }
+        if (kTogether == 1 || warp == 0)
+            store_row_value4(a.out, row * kHeadDim + 4 * lane, acc, a.out_fp32);
+        p = next;
     }
-    s_sum[warp][lane & 1][col] = acc[0];
-    s_sum[warp][lane & 1][col + 16] = acc[1];
-    __syncthreads();
-    if (threadIdx.x >= 64)
-        return;
-    const int64_t to = 2 * static_cast<int64_t>(blockIdx.x) + warp;
-    if (to >= a.batch * per_request)
-        return;
-    float4 t = s_sum[0][warp][lane];
-#pragma unroll
-    for (int w = 1; w < kCombineWarps; ++w) {
-        const float4 u = s_sum[w][warp][lane];
-        t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
-    }
-    store_row_value4(a.out, to * kHeadDim + 4 * lane, t, a.out_fp32);
 }
 
 cudaLaunchConfig_t dependent(dim3 grid, int threads, size_t smem, cudaStream_t stream, cudaLaunchAttribute (&attr)[1])
@@ -1313,10 +1377,14 @@ cudaError_t launch_prefix_rows(const PrefixArgs &a, const CUtensorMap &k_map, co
 cudaError_t launch_combine_prefix(const PrefixArgs &a, cudaStream_t stream)
 {
     const int64_t rows = static_cast<int64_t>(a.batch) * a.n_query * a.num_q_heads;
+    const int64_t most = kCombineCtas * device_sm_count();
+    const bool alone = rows > 2 * most;
+    const int64_t ctas = alone ? (rows + kCombineWarps - 1) / kCombineWarps : rows;
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg =
-        dependent(dim3(static_cast<unsigned>((rows + 1) / 2)), 32 * kCombineWarps, 0, stream, attr);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, combine_prefix_kernel, a);
+        dependent(dim3(static_cast<unsigned>(ctas < most ? ctas : most)), 32 * kCombineWarps, 0, stream, attr);
+    const cudaError_t e = alone ? cudaLaunchKernelEx(&cfg, combine_prefix_kernel<1>, a)
+                                : cudaLaunchKernelEx(&cfg, combine_prefix_kernel<kCombineWarps>, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

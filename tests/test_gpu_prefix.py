@@ -1,6 +1,8 @@
 """GPU parity of the attention over shared prefixes against plain fp64, with the bounds of view_ref: every request over
-its own row.  Whatever no request sees -- K, V and exponents of other slots, table entries -- is poisoned, and so
-are, where the other row is read for them, the entries of a request's own shared pages."""
+its own row.  Whatever no request sees -- K, V and exponents of other slots, table entries -- is poisoned.
+
+Small calls run each request apart; tables padded past the border (``pad=WIDE``) make the call share.  Of those the
+entries of a request's own shared pages are poisoned too, where so many share that the other row is read."""
 import numpy as np
 import pytest
 import torch
@@ -14,6 +16,7 @@ DEV = "cuda"
 D = 128
 SCALE = float(np.float32(1 / np.sqrt(D)))
 KINDS = ("fp8", "bf16", "blocks")
+WIDE = "wide"                                               # tables that allow 512 MB of cache
 
 
 @pytest.fixture(autouse=True)
@@ -28,7 +31,8 @@ class Case:
     """Groups of requests that share whole pages: (prefix, [own tokens of each request]).  Request r of a group holds
     prefix + own[r] tokens; a group of one, or a prefix of None, shares nothing."""
 
-    def __init__(self, kind, groups, g, ps, n, hkv=2, seed=0, ev=(-10, 3), pad=0, poison_own=True, q_scale=1.0):
+    def __init__(self, kind, groups, g, ps, n, hkv=2, seed=0, ev=(-10, 3), pad=WIDE, poison_own=True,
+                 q_scale=1.0):
         rng = np.random.default_rng([seed, n, g, ps])
         self.kind, self.n, self.ps, self.g, self.hkv = kind, n, ps, g, hkv
         lens, lead, shared, rows, used = [], [], [], [], 0
@@ -50,6 +54,9 @@ class Case:
                 lead.append(first if not alone else rng.choice([-1, -7, len(groups) * 1000]))
                 shared.append(prefix if not alone else rng.choice([0, -3, 5]))
         B, N = len(lens), used + 3
+        if pad == WIDE:
+            pad = -(-(512 << 20) // (256 * B * hkv * ps))
+        self.sharing = pad > 0
         self.lens, self.lead, self.shared = (np.asarray(x, np.int32) for x in (lens, lead, shared))
         perm = rng.permutation(N).astype(np.int32)
         maxp = max(1, max(len(r[0]) for r in rows)) + pad
@@ -90,9 +97,9 @@ class Case:
         self.desc = kvq.CacheDesc(N, ps, hkv, D, kvq.KVQ_CACHE_BF16 if kind == "bf16" else kvq.KVQ_CACHE_FP8_E4M3)
         # what the call is given: own entries of shared pages may hold anything
         self.given = self.bt.copy()
-        if poison_own:
+        if poison_own and self.sharing:
             for r in range(B):
-                if 0 <= self.lead[r] < B and self.lead[r] != r:
+                if 0 <= self.lead[r] < B and self.lead[r] != r and (self.lead == self.lead[r]).sum() >= 8:
                     w = min(int(self.shared[r]), int(self.lens[self.lead[r]]), int(self.lens[r]) - n + 1) // ps
                     self.given[r, :max(0, w)] = N + 7
         self.upload()
@@ -137,17 +144,22 @@ class Case:
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("ps,g", [(16, 8), (64, 3), (128, 1)])
-def test_one_query_token(kind, ps, g):
-    """Prefixes of every kind of end, own parts from none to several pages, groups of one, empty requests."""
-    Case(kind, [(5 * ps, [1, 2, ps, 3 * ps + 1]), (None, [0]), (ps - 1, [1, 3]), (7 * ps + 5, [1, 40, 0, 300]),
-                (1000, [17]), (33 * ps, [0, 0, 1]), (0, [5, 0])], g, ps, 1).check()
+@pytest.mark.parametrize("pad", [0, WIDE])
+def test_one_query_token(kind, ps, g, pad):
+    """Prefixes of every kind of end, own parts from none to several pages, groups of one, two and more, empty
+    requests."""
+    Case(kind, [(5 * ps, [1, 2, ps, 3 * ps + 1, 0, 9, 1, 1, ps - 1]), (None, [0]), (ps - 1, [1, 3] * 5),
+                (7 * ps + 5, [1, 40, 0, 300, 5, 5, 5, ps]), (1000, [17]), (33 * ps, [0, 0, 1] * 3), (64, [7, 8]),
+                (0, [5, 0])], g, ps, 1, pad=pad).check()
 
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("n,g,ps", [(2, 1, 32), (4, 4, 16), (5, 8, 128), (16, 8, 16), (11, 7, 64)])
-def test_several_query_tokens(kind, n, g, ps):
+@pytest.mark.parametrize("pad", [0, WIDE])
+def test_several_query_tokens(kind, n, g, ps, pad):
     """Own parts shorter than the drafts, so that queries stand inside the shared pages; contexts shorter than them."""
-    Case(kind, [(5 * ps, [n, 1, 0, n - 1, 2 * ps]), (None, [1, n - 1, n, 100]), (400, [n, n + 1, 70])], g, ps, n).check()
+    Case(kind, [(5 * ps, [n, 1, 0, n - 1, 2 * ps, n, n, n + 1, 3]), (None, [1, n - 1, n, 100]), (400, [n, n + 1, 70])],
+         g, ps, n, pad=pad).check()
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -161,28 +173,29 @@ def test_rows_around_the_tiles(kind, m, g):
 @pytest.mark.parametrize("kind", KINDS)
 def test_long_prefixes(kind):
     """Shares of many tiles, so that fp32 sums leave tensor memory on the way, and several CTAs per row pair."""
-    Case(kind, [(70000, [1, 300]), (20000, [5, 5, 9000])], 4, 64, 1, hkv=1).check()
-    Case(kind, [(150000, [3] * 9)], 8, 16, 4, hkv=1).check(kinds=(True,))
+    Case(kind, [(70000, [1, 300] + [7] * 6), (20000, [5, 5, 9000, 1, 1, 1, 1, 1])], 2, 64, 1, hkv=1).check()
+    Case(kind, [(160000, [3] * 9)], 2, 16, 4, hkv=1).check(kinds=(True,))
 
 
 @pytest.mark.parametrize("kind", KINDS)
 def test_many_small_groups(kind):
+    """Runs that cross every 128th request, among them."""
     rng = np.random.default_rng(5)
-    groups = [(int(rng.integers(0, 300)), [int(x) for x in rng.integers(0, 60, rng.integers(1, 5))]) for _ in range(150)]
-    Case(kind, groups, 2, 16, 1, pad=3).check()
+    groups = [(int(rng.integers(0, 300)), [int(x) for x in rng.integers(0, 60, rng.integers(1, 12))]) for _ in range(100)]
+    Case(kind, groups, 2, 16, 1).check()
 
 
 @pytest.mark.parametrize("kind", KINDS)
 def test_requests_with_prefixes_of_their_own_lengths(kind):
     """One row serves requests that share more and less of it, and more than it or they hold."""
-    c = Case(kind, [(900, [1, 50, 9, 400, 2])], 5, 16, 1, poison_own=False)
-    c.shared[:] = (16, 900, 2**31 - 1, 333, 15)
+    c = Case(kind, [(900, [1, 50, 9, 400, 2] * 3)], 5, 16, 1, poison_own=False)
+    c.shared[:] = (16, 900, 2**31 - 1, 333, 15) * 3
     c.upload()
     c.check()
-    c.lead[:] = (0, 2, 2, 4, 0)                             # three runs
+    c.lead[:] = [0] * 5 + [12] * 9 + [-1]                   # two runs
     c.upload()
     c.check()
-    c.lead[:] = -1
+    c.lead[:] = 2**31 - 1
     c.upload()
     c.check()
 
@@ -190,54 +203,56 @@ def test_requests_with_prefixes_of_their_own_lengths(kind):
 @pytest.mark.parametrize("kind", KINDS)
 def test_aborted_requests_and_leaders(kind):
     """An aborted request gets zeros; requests whose leader is aborted read their own rows."""
-    groups = [(200, [3, 40, 7]), (100, [1, 20])]
-    for flags in ([0, 1, 0, 0, 0], [1, 0, 0, 0, 2], [1, 1, 1, 1, 1]):
-        abort = np.asarray(flags, np.uint8)
+    groups = [(200, [3, 40, 7] * 3), (100, [1, 20] * 4)]
+    for which in ([1, 5], [0, 16], [0, 9, 10], range(17)):
+        abort = np.zeros(17, np.uint8)
+        abort[list(which)] = 3
         Case(kind, groups, 4, 16, 1, poison_own=False).check(abort=abort)
 
 
 @pytest.mark.parametrize("kind", KINDS)
 def test_rows_that_are_too_short_and_bad_pages(kind):
-    c = Case(kind, [(640, [5, 70, 5, 30]), (300, [9, 9])], 4, 16, 2, poison_own=False)
+    c = Case(kind, [(640, [5, 70, 5, 30] * 3), (300, [9, 9] * 4)], 4, 16, 2, poison_own=False)
     c.given[0, 20] = -1                                     # a shared page of the first group
-    c.lens[5] = 10**6                                       # longer than its row
+    c.lens[13] = 10**7                                      # longer than its row
     c.given[3, 41] = c.desc.num_pages                       # a page of request 3's own
     c.shared[3] = 300                                       # 18 pages: below the bad one
     c.upload()
-    got = c.run(True)
-    keep = [4]
     ref, bound = c.ref(True)
-    R.assert_within(got[keep], ref[keep], bound[keep])
-    assert not got[[0, 1, 2, 3, 5]].any()
+    right = [12] + list(range(14, 20))
+    got = c.run(True)
+    R.assert_within(got[right], ref[right], bound[right])
+    assert not got[:12].any() and not got[13].any()
     c.given[3, 41] = c.bt[3, 41]
     c.upload()
+    right.append(3)
     got = c.run(True)
-    R.assert_within(got[[3, 4]], ref[[3, 4]], bound[[3, 4]])
-    assert not got[[0, 1, 2, 5]].any()
+    R.assert_within(got[right], ref[right], bound[right])
+    assert not np.delete(got, right, axis=0).any()
 
 
 @pytest.mark.parametrize("kind", KINDS)
 def test_nan_reaches_those_who_see_it(kind):
-    c = Case(kind, [(320, [20, 20, 20]), (160, [30, 1])], 2, 16, 1)
+    c = Case(kind, [(320, [20] * 9), (160, [30, 1] * 4)], 2, 16, 1)
     nan = 0x7FC0 if kind == "bf16" else R.NAN_CODE
     c.v[c.bt[0, 3], 0, 5, 7] = nan                          # a shared V row of the first group
-    c.v[c.bt[4, 10], 1, 0, 100] = nan                       # request 4's own
+    c.v[c.bt[9, 10], 1, 0, 100] = nan                       # request 9's own
     c.upload()
     for fp32 in (False, True):
         ref, bound = c.ref(fp32)
-        assert np.isnan(ref[:3, :, :2, 7]).all() and np.isnan(ref).sum() == 3 * 2 + 2
+        assert np.isnan(ref[:9, :, :2, 7]).all() and np.isnan(ref).sum() == 9 * 2 + 2
         R.assert_within(c.run(fp32), ref, bound, f"fp32={fp32}")
     c.k[c.bt[0, 4], 1, 2, 3] = nan                          # a shared K row: every weight of the other head's rows
     c.upload()
     got, (ref, bound) = c.run(True), c.ref(True)
-    assert np.isnan(got[:3, :, 2:]).all()
-    for at in ((slice(3), slice(None), slice(2)), (slice(3, 5),)):
+    assert np.isnan(got[:9, :, 2:]).all()
+    for at in ((slice(9), slice(None), slice(2)), (slice(9, 17),)):
         R.assert_within(got[at], ref[at], bound[at])
 
 
 def test_large_values_over_a_bf16_cache():
     """Values near bf16's largest, of one sign: sums of weights do not leave fp32."""
-    c = Case("bf16", [(3000, [10, 600])], 4, 16, 1, hkv=1)
+    c = Case("bf16", [(3000, [10, 600] * 4)], 4, 16, 1, hkv=1)
     big = W.f32_to_bf16_bits(np.full(c.v.shape, 2.0 ** 120, np.float32))
     seen = c.v != 0x7FC0
     c.v = np.where(seen, big, c.v)
@@ -251,20 +266,22 @@ def test_large_values_over_a_bf16_cache():
 @pytest.mark.parametrize("scale,q_scale", [(-SCALE, 1.0), (0.0, 1.0), (SCALE, 300.0), (SCALE * 40, 1.0), (SCALE, 2.0 ** -100)])
 def test_scales(kind, scale, q_scale):
     """Negative and zero softmax scales, peaked and flat softmaxes (the maximum rises by thousands), tiny queries."""
-    Case(kind, [(1500, [3, 200, 50])], 3, 32, 1, q_scale=q_scale).check(scale=scale)
+    Case(kind, [(1500, [3, 200, 50] * 3)], 3, 32, 1, q_scale=q_scale).check(scale=scale)
 
 
 @pytest.mark.parametrize("ev", [(-48, 48), (-128, 127)])
 def test_far_value_exponents(ev):
-    c = Case("blocks", [(900, [3, 200, 50])], 3, 16, 1, ev=ev)
+    c = Case("blocks", [(900, [3, 200, 50] * 3)], 3, 16, 1, ev=ev)
     c.ve = np.clip(c.ve, -48, 48)                           # how they are read
     for fp32 in (False, True):
         R.assert_within(c.run(fp32), *c.ref(fp32), f"fp32={fp32}")
 
 
 @pytest.mark.parametrize("kind", KINDS)
-def test_calls_repeat_bit_for_bit_and_need_no_workspace_contents(kind):
-    c = Case(kind, [(3000, [10, 600, 1]), (700, [5, 5])], 8, 16, 1)
+@pytest.mark.parametrize("pad", [0, WIDE])
+@pytest.mark.parametrize("n", [1, 4])
+def test_calls_repeat_bit_for_bit_and_need_no_workspace_contents(kind, pad, n):
+    c = Case(kind, [(3000, [10, 600, 4] * 3), (700, [5, 5])], 8, 16, n, pad=pad)
     ws = c.workspace()
     a = c.call(c.out(True), ws).clone()
     b = c.call(c.out(True), ws)
@@ -274,9 +291,10 @@ def test_calls_repeat_bit_for_bit_and_need_no_workspace_contents(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-def test_a_graph_follows_lengths_and_another_stream(kind):
+@pytest.mark.parametrize("pad", [0, WIDE])
+def test_a_graph_follows_lengths_and_another_stream(kind, pad):
     """A captured call replayed after the lengths, flags and tables changed in place."""
-    c = Case(kind, [(640, [5, 70, 300]), (200, [9, 9, 400])], 4, 16, 1, poison_own=False)
+    c = Case(kind, [(640, [5, 70, 300] * 3), (200, [9, 9, 400] * 3)], 4, 16, 1, poison_own=False, pad=pad)
     ws, out = c.workspace(), c.out(True)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -287,7 +305,8 @@ def test_a_graph_follows_lengths_and_another_stream(kind):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         c.call(out, ws)
-    for lens, shared in (([100, 30, 1, 0, 209, 600], [90, 16, 0, 50, 48, 200]), ([645, 710, 940, 209, 209, 1], [640, 640, 640, 200, 200, 200])):
+    for lens, shared in (([100, 30, 1] * 3 + [0, 209, 600] * 3, [90, 16, 0] * 3 + [50, 48, 200] * 3),
+                         ([645, 710, 940] * 3 + [209, 209, 1] * 3, [640] * 9 + [200] * 9)):
         c.lens[:], c.shared[:] = lens, shared
         c.d["seq"].copy_(torch.from_numpy(c.lens))
         c.d["shared"].copy_(torch.from_numpy(c.shared))
@@ -299,7 +318,7 @@ def test_a_graph_follows_lengths_and_another_stream(kind):
 @pytest.mark.parametrize("kind", ["fp8", "bf16"])
 def test_two_calls_at_once(kind):
     """On two streams with a workspace each."""
-    cs = [Case(kind, [(2000 + 100 * i, [10, 60, 1])], 4, 16, 1, seed=i) for i in range(2)]
+    cs = [Case(kind, [(2000 + 100 * i, [10, 60, 1] * 3)], 4, 16, 1, seed=i) for i in range(2)]
     streams = [torch.cuda.Stream() for _ in cs]
     ws, outs = [c.workspace() for c in cs], [c.out(True) for c in cs]
     torch.cuda.synchronize()
@@ -312,7 +331,7 @@ def test_two_calls_at_once(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("m,n", [(2, 1), (40, 4)])
+@pytest.mark.parametrize("m,n", [(9, 1), (40, 4)])
 def test_copy_wait_timeout_zeroes_and_recovers(kind, m, n):
     """Every wait for a copy gives up at once: zeros for what was served, no copy left in flight, and the next call
     is right."""
@@ -328,14 +347,15 @@ def test_copy_wait_timeout_zeroes_and_recovers(kind, m, n):
     c.check()
 
 
-def test_an_empty_batch_and_no_sharing_at_all():
-    c = Case("fp8", [(None, [100]), (None, [1]), (None, [0])], 4, 16, 1)
+@pytest.mark.parametrize("pad", [0, WIDE])
+def test_an_empty_batch_and_no_sharing_at_all(pad):
+    c = Case("fp8", [(None, [100]), (None, [1]), (None, [0])], 4, 16, 1, pad=pad)
     c.check()
     c.lens[:] = 0
     c.upload()
     assert not c.run(True).any()
-    c2 = Case("fp8", [(64, [3, 3])], 1, 16, 1, hkv=1)
+    c2 = Case("fp8", [(64, [3, 3])], 1, 16, 1, hkv=1, pad=pad)
     e = lambda *s: torch.empty(s, dtype=torch.int32, device=DEV)  # noqa: E731
     q = torch.empty((0, 1, 1, D), dtype=torch.bfloat16, device=DEV)
     kvq.kvq_decode_attn_prefix(c2.desc, q, c2.d["k"], c2.d["v"], c2.d["s0"], c2.d["s1"], e(0, 4), e(0), e(0), e(0),
-                               SCALE, None, q.clone(), None)
+                               SCALE, None, q.clone(), c2.workspace())
