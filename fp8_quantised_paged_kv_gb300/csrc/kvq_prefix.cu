@@ -10,10 +10,9 @@
 // combine_prefix_kernel below joins the parts by their log-sum-exps.
 //
 // A CTA takes up to 256 rows, two tiles of 128, through a range of the run's
-// pages, 64 tokens at a time.  Its warps have one job
-// each: copies by TMA; over an FP8 cache the conversion of K and V to f16 (once
-// for all rows); per row tile a thread that issues S = Q K^T and O += P V, and
-// a softmax group of four warps, a row per thread, which reads S from tensor
+// pages, 64 tokens at a time.  Its warps have one job each: copies by TMA; over an
+// FP8 cache the conversion of K and V to f16 (once for all rows); per row tile a
+// thread that issues S = Q K^T and O += P V, and a softmax group of four warps, a row per thread, which reads S from tensor
 // memory, and writes P over it.  One tile's exponentials run beside the other's
 // products, and each group has the next tile's S while it works on one.  With
 // up to 128 rows both groups serve the same rows on alternate token tiles, and

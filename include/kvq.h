@@ -492,29 +492,35 @@ KVQ_API kvq_status kvq_decode_attn_blocks(const kvq_cache_desc *desc, const void
  *                  fine); negative or past the batch: r shares nothing.
  *   prefix_lens    int32 [batch]: the first prefix_lens[r] tokens of r are those
  *                  of request prefix_of[r].  Both rows must hold them, in the
- *                  same pages or in copies of them: the call looks up whole
- *                  pages of min(prefix_lens[r], seq_lens[prefix_of[r]],
- *                  seq_lens[r] - n + 1) tokens in the other row, the rest in
- *                  r's, and all of them in r's if request prefix_of[r] is
- *                  aborted or longer than its row.
+ *                  same pages or in copies of them, and either may be read: of
+ *                  the other row at most the whole pages of min(prefix_lens[r],
+ *                  seq_lens[prefix_of[r]], seq_lens[r] - n + 1) tokens, and
+ *                  none if request prefix_of[r] is aborted or longer than its
+ *                  row.
  *                  Consecutive requests with one value of prefix_of are served
  *                  together, whatever their lengths; the same value again
- *                  further on starts over, as does every 128th request.  A
- *                  request that shares with no other is best given a
- *                  prefix_lens of 0.
+ *                  further on starts over, as does every 128th request.
  *   num_query_tokens, q, out, seq_lens, abort_flags and every other argument
  *                  as in kvq_decode_attn_mt, with either cache type; n = 1 to 16.
  *   workspace      of at least the plan's size, on the plan's device.  It needs
  *                  no contents, and holds nothing once the call is done.  Two
  *                  calls in flight at once must not share it.
- * A request is zeroed as in kvq_decode_attn_mt; so is one whose shared pages the
- * other row gives an id outside [0, num_pages).  A NaN that some query of a
- * request sees may reach the other queries of that request and, in the V row of
- * a position below the longest prefix_lens of those served together, theirs.
- * Three launches: the shared pages on the 5th-generation tensor cores, up to
- * 256 query rows (request, token, head) of a KV head at a time; the requests'
- * own pages; the parts of both joined.  Each shares its work out evenly on the
- * device, whatever the lengths.
+ * A request is zeroed as in kvq_decode_attn_mt; so is one whose shared pages,
+ * where the other row is read, have an id outside [0, num_pages) there.  A NaN
+ * that some query of a request sees may reach the other queries of that request
+ * and, in the V row of a position below the longest prefix_lens of those served
+ * together, theirs.
+ *
+ * Sharing has to gain something.  Where the table's rows allow less than 512 MB
+ * of K and V (batch * max_pages_per_seq pages, once per 16 query rows of a KV
+ * head), every request reads its own row, in the launches of
+ * kvq_decode_attn_window; else the other row serves where so many consecutive
+ * requests name it that one pass of the tensor cores costs less than theirs
+ * (three with one query token over e4m3).  Then there are three launches: the shared
+ * pages on the 5th-generation tensor cores, up to 256 query rows (request, token,
+ * head) of a KV head at a time; the requests' own pages beside it; the parts of
+ * both joined.  Each shares its work out evenly on the device, whatever the
+ * lengths.
  */
 KVQ_API kvq_status kvq_decode_plan_prefix(const kvq_cache_desc *desc, int32_t batch,
                                           int32_t num_query_tokens, int32_t num_q_heads,
