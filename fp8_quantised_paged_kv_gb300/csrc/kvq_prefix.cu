@@ -208,14 +208,14 @@ __device__ __forceinline__ void fewer_registers()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-// The row's O, out of tensor memory onto its sums (from zero, the first time).
-__device__ __forceinline__ void flush_sums(uint32_t ocol, float4 *part, int rows, bool valid, bool onto, float mul)
+// O of the rows that are `wanted`, out of tensor memory onto their sums (from zero, the first time).
+__device__ __forceinline__ void flush_sums(uint32_t ocol, float4 *part, int rows, bool wanted, bool onto, float mul)
 {
 #pragma unroll 1
     for (int c = 0; c < 8; ++c) {
         uint32_t o[16];
         tmem_ld16(ocol + 16u * c, o);
-        if (valid)
+        if (wanted)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 float4 *at = part + (4 * c + k) * rows;
@@ -505,10 +505,14 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
             lim = s.len[first % kBlockReq + req];
         }
         float m_used = -INFINITY, l_sum = 0.f;
-        // fp32 output: this row's sums so far (four dims of all the tile's rows side
-        // by side, in the rows' places) are behind m_used by sums_mul
-        [[maybe_unused]] float sums_mul = 1.f;
-        [[maybe_unused]] float4 *const sums = a.pre_o + (256ll * blockIdx.x + place0) * 32 + m;
+        // This row's sums so far (four dims of all the tile's rows side by side, in the
+        // rows' places) are behind m_used by sums_mul.  With fp32 output O goes there
+        // now and then.  Else, and then for good (`saved`), it goes there when the
+        // row's tokens end before the others' do: the others' further values are not
+        // the row's, and a NaN or an infinity among them, times its weights of 0, would be.
+        float sums_mul = 1.f;
+        bool saved = false;
+        float4 *const sums = a.pre_o + (256ll * blockIdx.x + place0) * 32 + m;
 
         if (!s.skip) {
             const float kv_scale = B::kConvert && !kBlocks ? a.k_scale[kvh] : 1.f;
@@ -599,11 +603,14 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
                 const uint32_t col = scol + 64u * sb;
                 uint32_t sv[kTok];
                 tmem_ld64(col, sv);
-                const int vis = lim - tile * kTok;     // columns below it are visible
-                if (!__all_sync(0xFFFFFFFFu, vis >= kTok)) {
+                const int vis = lim - tile * kTok;     // > 0: the row sees the tile
+                bool ending = false, save = false;
+                if (!__all_sync(0xFFFFFFFFu, vis >= kTok)) {   // a row's tokens end between tiles
 #pragma unroll
                     for (int k = 0; k < kTok; ++k)
-                        sv[k] = k < vis ? sv[k] : 0xFF800000u;
+                        sv[k] = vis > 0 ? sv[k] : 0xFF800000u;
+                    ending = vis <= 0 && !saved && l_sum != 0.f;
+                    save = __any_sync(0xFFFFFFFFu, ending);
                 }
                 // block q (16 columns) of the tile: its multiplier and its ev
                 [[maybe_unused]] float mk[4], ev[4];
@@ -640,16 +647,20 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
                 // to a large accumulator towards zero).
                 const bool flush = kPrecise && i > 0 && i % kFlush == 0;
                 const bool rescale = raise && m_used != -INFINITY && i > 0 && !flush;
-                if (__any_sync(0xFFFFFFFFu, rescale) || flush) {
+                const bool scale = __any_sync(0xFFFFFFFFu, rescale);
+                if (scale || save || flush) {
                     // O holds the group's earlier tiles once O += P V of the last one is done
                     if (!__all_sync(0xFFFFFFFFu, wait_or_abort(&bar.o_done[gr], (gi - 1) & 1, kCopyWaitLimitNs,
                                                                abort_flag, 4u)))
                         break;
                     tmem_fence_after_sync();
-                    if (flush) {
-                        flush_sums(ocol, sums, tile_rows, row_valid, i > kFlush, sums_mul);
-                        sums_mul = 1.f;
-                    } else {
+                    if (save || flush) {
+                        flush_sums(ocol, sums, tile_rows, row_valid && !saved && (flush || ending),
+                                   kPrecise && i > kFlush, sums_mul);
+                        sums_mul = flush || ending ? 1.f : sums_mul;
+                        saved = saved || ending;
+                    }
+                    if (scale) {
                         const float f = rescale ? alpha : 1.f;
 #pragma unroll 1
                         for (int c = 0; c < 8; ++c) {
@@ -758,8 +769,9 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
                     for (int k = 0; k < 4; ++k) {
                         float4 v = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
                                                __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-                        if (kPrecise && mine > kFlush && row_valid) {
+                        if (saved || (kPrecise && mine > kFlush && row_valid)) {
                             const float4 u = sums[(4 * c + k) * tile_rows];
+                            v = saved ? make_float4(0.f, 0.f, 0.f, 0.f) : v;
                             v.x = fmaf(u.x, sums_mul, v.x);
                             v.y = fmaf(u.y, sums_mul, v.y);
                             v.z = fmaf(u.z, sums_mul, v.z);
@@ -770,8 +782,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
                                        : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
                 }
-                if (kPrecise && mine > kFlush)             // the sums lie where the rows go
-                    named_barrier_sync(6 + gr, 128);
+                named_barrier_sync(6 + gr, 128);           // the sums lie where the rows go
                 __syncwarp();
                 float4 *to = a.pre_o + (256ll * blockIdx.x + place0 + 32 * (warp & 3)) * 32 + lane;
                 const int n = min(32, tile_rows - 32 * (warp & 3));

@@ -21,8 +21,8 @@ struct Costs {
     }
 };
 
-// A request's tokens by where they come from: whole pages of row prefix_of[r], as
-// many as all its query tokens see and the other row holds, and its own row
+// A request's tokens by where they come from: whole pages, in whole 64 tokens, of row
+// prefix_of[r], as many as all its query tokens see and the other row holds, and its own row
 // (both 0: its outputs are zeros).  The other row serves only where so many
 // consecutive requests (up to eight are counted) name it that this costs less than each
 // reading its own: three of one query token over e4m3, two over a bf16 cache.
@@ -66,7 +66,8 @@ __device__ __forceinline__ Tokens tokens_of(const PrefixArgs &a, int r, int ps_s
     if (held > cap || (a.abort_flags != nullptr && __ldcg(a.abort_flags + lead) != 0))
         return {0, real, -1, joins};
     const int n = min(min(want, held), real - a.n_query + 1);
-    const int shared = n > 0 ? n >> ps_shift << ps_shift : 0;
+    const int whole = max(ps_shift, 6);                    // (of tiles, too: kvq_prefix.cu)
+    const int shared = n > 0 ? n >> whole << whole : 0;
     return {shared, real - shared, shared > 0 ? lead : -1, joins};
 }
 

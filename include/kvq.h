@@ -507,9 +507,8 @@ KVQ_API kvq_status kvq_decode_attn_blocks(const kvq_cache_desc *desc, const void
  *                  calls in flight at once must not share it.
  * A request is zeroed as in kvq_decode_attn_mt; so is one whose shared pages,
  * where the other row is read, have an id outside [0, num_pages) there.  A NaN
- * that some query of a request sees may reach the other queries of that request
- * and, in the V row of a position below the longest prefix_lens of those served
- * together, theirs.
+ * that some query of a request sees may reach the other queries of that request,
+ * but no other request.
  *
  * Sharing has to gain something.  Where the table's rows allow less than 512 MB
  * of K and V (batch * max_pages_per_seq pages, once per 16 query rows of a KV

@@ -100,8 +100,8 @@ class Case:
         if poison_own and self.sharing:
             for r in range(B):
                 if 0 <= self.lead[r] < B and self.lead[r] != r and (self.lead == self.lead[r]).sum() >= 8:
-                    w = min(int(self.shared[r]), int(self.lens[self.lead[r]]), int(self.lens[r]) - n + 1) // ps
-                    self.given[r, :max(0, w)] = N + 7
+                    w = min(int(self.shared[r]), int(self.lens[self.lead[r]]), int(self.lens[r]) - n + 1)
+                    self.given[r, :max(0, w) // max(ps, 64) * max(ps, 64) // ps] = N + 7
         self.upload()
 
     def upload(self):
@@ -248,6 +248,41 @@ def test_nan_reaches_those_who_see_it(kind):
     assert np.isnan(got[:9, :, 2:]).all()
     for at in ((slice(9), slice(None), slice(2)), (slice(9, 17),)):
         R.assert_within(got[at], ref[at], bound[at])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("ps,m,g,n", [(16, 1, 3, 1), (64, 2, 8, 1), (128, 1, 5, 4)])
+def test_no_request_meets_what_stands_behind_its_end(kind, ps, m, g, n):
+    """Requests that end inside the others' prefix, one and two row tiles: NaN and infinities in V past their ends."""
+    own = ([10] * 4 + [-100, -700, -1500, -2000, 0, -2100]) * m
+    c = Case(kind, [(2112, own)], g, ps, n)
+    nan, inf = (0x7FC0, 0x7F80) if kind == "bf16" else (R.NAN_CODE, R.NAN_CODE)
+    for x, places in ((nan, ((2105, 0, 5), (2050, 1, 9), (1999, 0, 77), (1000, 1, 3), (100, 0, 2))),
+                      (inf, ((2100, 0, 6), (1200, 1, 8)))):
+        for pos, h, d in places:
+            c.v[c.bt[0, pos // ps], h, pos % ps, d] = x
+    c.upload()
+    for fp32 in (False, True):
+        got, (ref, bound) = c.run(fp32), c.ref(fp32)
+        spoilt = ~np.isfinite(ref)
+        # (a page that the prefix does not fill is request 0's alone)
+        seen = [7] + [7 if 2112 % ps == 0 else 4] * 3
+        assert spoilt[:4].any(axis=(1, 2)).sum(axis=1).tolist() == seen and not spoilt[9].any()
+        assert not np.isfinite(got[spoilt]).any()
+        R.assert_within(got[~spoilt], ref[~spoilt], bound[~spoilt], f"fp32={fp32}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_sums_that_leave_tensor_memory(kind):
+    """1,024 rows over one prefix, 37 tiles of both row tiles a CTA: fp32 sums go out on the way, and some rows' for good."""
+    own = [20, 40, -30000, 17, -60000, 20, -100, 33]
+    c = Case(kind, [(90000, own)], 8, 16, 16, hkv=1)
+    for pos in (89990, 80001, 59950, 45000):
+        c.v[c.bt[0, pos // 16], 0, pos % 16, pos % 128] = 0x7FC0 if kind == "bf16" else R.NAN_CODE
+    c.upload()
+    got, (ref, bound) = c.run(True), c.ref(True)
+    assert [np.isnan(x).any(axis=(0, 1)).sum() for x in ref] == [4, 4, 2, 4, 0, 4, 3, 4]
+    R.assert_within(got, ref, bound)
 
 
 def test_large_values_over_a_bf16_cache():
