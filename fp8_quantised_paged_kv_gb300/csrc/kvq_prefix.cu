@@ -74,8 +74,16 @@ struct Build {
     static constexpr int kThreads = kConvert ? 640 : 32 * (kIssue + 2);
     // places of a tile of tokens for one row tile (0.91 us against 1.20 for two over
     // e4m3, 0.99 against 1.60 with block scales, 0.98 against 1.03 over a bf16 cache;
-    // fp32 output 1.32 against 1.87, 1.41 against 2.28, 1.60 against 3.0)
+    // fp32 output 1.21 against 1.82, 1.45 against 2.28, 1.47 against 2.61)
     static constexpr int kNarrowCost = kKind == kBf16 ? (kPrecise ? 4 : 7) : kKind == kFp8 ? 6 : 5;
+    // and of a border between two jobs (a place is 0.15 to 0.2 us, with three terms 0.37)
+    static constexpr int kBorderCost = kTerms == 3 ? 20 : 40;
+    // fp32 output: tiles between O's ways out of tensor memory into fp32 sums that
+    // round.  The tensor core cuts each addition to a large accumulator towards zero, 4
+    // kTerms of them a tile: 11 tiles over a bf16 cache put 2.8e-6 on the outputs, 6 of them
+    // 1.2e-6 to 1.5e-6, 4 of them 1.05e-6 (2 to 10 % slower); 8 over e4m3 1.1e-6 to 1.2e-6,
+    // 16 1.4e-6 to 2.0e-6; 16 with block scales 0.4e-6 to 0.5e-6.
+    static constexpr int kFlush = kKind == kBf16 ? 6 : kKind == kFp8 ? 8 : 16;
     static constexpr float kLift = kConvert ? 7.f : -8.f;  // log2 of what P, l and O are larger by
 };
 
@@ -83,10 +91,8 @@ constexpr int kBlockReq = 128;                             // a run does not cro
 constexpr int kMaxBlocks = 512;                            // of up to 65,535 requests
 constexpr int kMinTiles = 4;                               // of a CTA's share, in wide tiles
 constexpr int kWideCost = 8;                               // places of a tile of tokens for two row tiles
-constexpr int kBorderCost = 40;                            // and of a border between two jobs
 
 constexpr uint32_t kColS = 0, kColO = 256;                 // + 128 for the second group
-constexpr int kFlush = 32;                                 // fp32 output: tiles between O's ways out of tensor memory
 
 // Column, from its S buffer's first, of term t of P for tokens 32 c .. 32 c + 31
 // of a tile.  P is written over scores that have been read.
@@ -196,6 +202,12 @@ __device__ __forceinline__ bool elect_one()
     return on != 0;
 }
 
+__device__ __forceinline__ void red_add_f32x4(float4 *at, float4 v)
+{
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1,%2,%3,%4};"
+                 ::"l"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
 // Registers of this warpgroup's threads from here on.
 template <int kRegs>
 __device__ __forceinline__ void more_registers()
@@ -208,9 +220,12 @@ __device__ __forceinline__ void fewer_registers()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-// O of the rows that are `wanted`, out of tensor memory onto their sums (from zero, the first time).
+// O of the rows that are `wanted`, out of tensor memory onto their sums (from
+// zero, the first time).  Sums that are not behind the maximum are added to by
+// reductions at L2, which nothing here waits for: a row's sums are its thread's alone.
 __device__ __forceinline__ void flush_sums(uint32_t ocol, float4 *part, int rows, bool wanted, bool onto, float mul)
 {
+    const bool behind = __any_sync(0xFFFFFFFFu, wanted && onto && mul != 1.f);
 #pragma unroll 1
     for (int c = 0; c < 8; ++c) {
         uint32_t o[16];
@@ -219,10 +234,17 @@ __device__ __forceinline__ void flush_sums(uint32_t ocol, float4 *part, int rows
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 float4 *at = part + (4 * c + k) * rows;
-                const float4 u = onto ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
-                *at = make_float4(fmaf(u.x, mul, __uint_as_float(o[4 * k])), fmaf(u.y, mul, __uint_as_float(o[4 * k + 1])),
-                                  fmaf(u.z, mul, __uint_as_float(o[4 * k + 2])),
-                                  fmaf(u.w, mul, __uint_as_float(o[4 * k + 3])));
+                float4 v = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                       __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                if (onto && !behind) {
+                    red_add_f32x4(at, v);
+                    continue;
+                }
+                if (onto) {
+                    const float4 u = __ldcg(at);
+                    v = make_float4(fmaf(u.x, mul, v.x), fmaf(u.y, mul, v.y), fmaf(u.z, mul, v.z), fmaf(u.w, mul, v.w));
+                }
+                __stcg(at, v);
             }
     }
 }
@@ -230,7 +252,7 @@ __device__ __forceinline__ void flush_sums(uint32_t ocol, float4 *part, int rows
 // The runs of a block of requests and their places on the line, worked out by
 // the 128 threads of a team.  c.total[block]: all its places.  list: also the
 // runs themselves and every request's shared tokens, into s.
-template <int kNarrowCost>
+template <int kNarrowCost, int kBorderCost>
 __device__ __forceinline__ void find_runs(const PrefixArgs &a, Shared &s, Scratch &c, int team, int block, int ps_shift,
                                           bool list, Work *work = nullptr)
 {
@@ -337,7 +359,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
 
 // The job at place x of the line, by one thread; moves x past what this CTA does
 // of it.  False if that is nothing (x lies in the border).
-template <int kNarrowCost>
+template <int kNarrowCost, int kBorderCost>
 __device__ __forceinline__ bool set_job(const PrefixArgs &a, Shared &s)
 {
     Walk &w = s.w;
@@ -431,7 +453,7 @@ __device__ __forceinline__ void end_job()
 }
 
 // The next job, found by the softmax warps.
-template <int kNarrowCost>
+template <int kNarrowCost, int kBorderCost>
 __device__ __forceinline__ void find_job(const PrefixArgs &a, Shared &s, Scratch &scratch, int ps_shift)
 {
     named_barrier_sync(1, 256);              // the last job's numbers have been read
@@ -440,7 +462,7 @@ __device__ __forceinline__ void find_job(const PrefixArgs &a, Shared &s, Scratch
     for (;;) {
         if (threadIdx.x == 0) {
             Walk &w = s.w;
-            s.search = w.x >= w.end ? 0 : w.x >= w.block_start + w.block_total ? 2 : set_job<kNarrowCost>(a, s) ? 1 : 3;
+            s.search = w.x >= w.end ? 0 : w.x >= w.block_start + w.block_total ? 2 : set_job<kNarrowCost, kBorderCost>(a, s) ? 1 : 3;
             s.bad_from = 0x7FFFFFFF;
             s.job_there = s.search == 1;
             // as the last job left it: a warp of the next one may raise the flag
@@ -455,7 +477,7 @@ __device__ __forceinline__ void find_job(const PrefixArgs &a, Shared &s, Scratch
         if (found == 2) {
             if (threadIdx.x == 0)
                 s.w.block_start += s.w.block_total;
-            find_runs<kNarrowCost>(a, s, scratch, 0, block, ps_shift, true);
+            find_runs<kNarrowCost, kBorderCost>(a, s, scratch, 0, block, ps_shift, true);
             named_barrier_sync(2, 128);
         }
     }
@@ -479,7 +501,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
     volatile int *abort_flag = &s.abort;
     Done done;
     for (;;) {
-        find_job<B::kNarrowCost>(a, s, scratch, ps_shift);
+        find_job<B::kNarrowCost, B::kBorderCost>(a, s, scratch, ps_shift);
         if (!open_job(s))
             return;
         const Walk &w = s.w;
@@ -642,10 +664,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
                     mx = mx == -INFINITY ? mx : mx * mul;
                 const bool raise = row_valid && mx > m_used + kRaiseThreshold;
                 const float alpha = raise ? (m_used == -INFINITY ? 0.f : fast_exp2(m_used - mx)) : 1.f;
-                // fp32 output: O goes out of tensor memory every kFlush tiles
-                // into fp32 sums that round (the tensor core cuts what it adds
-                // to a large accumulator towards zero).
-                const bool flush = kPrecise && i > 0 && i % kFlush == 0;
+                const bool flush = kPrecise && i > 0 && i % B::kFlush == 0;
                 const bool rescale = raise && m_used != -INFINITY && i > 0 && !flush;
                 const bool scale = __any_sync(0xFFFFFFFFu, rescale);
                 if (scale || save || flush) {
@@ -656,7 +675,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
                     tmem_fence_after_sync();
                     if (save || flush) {
                         flush_sums(ocol, sums, tile_rows, row_valid && !saved && (flush || ending),
-                                   kPrecise && i > kFlush, sums_mul);
+                                   kPrecise && i > B::kFlush, sums_mul);
                         sums_mul = flush || ending ? 1.f : sums_mul;
                         saved = saved || ending;
                     }
@@ -761,25 +780,34 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
                 const float vs = B::kConvert && !kBlocks ? a.v_scale[kvh] : 1.f;
                 const float wgt = l_sum == 0.f ? 0.f : vs / l_sum;
                 float *stage = reinterpret_cast<float *>(sm) + warp * 32 * kStageStride;
+                const bool onto = saved || (kPrecise && mine > B::kFlush && row_valid);
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t o[16];
-                    tmem_ld16(ocol + 16u * c, o);
+                for (int c = 0; c < 8; c += 2) {
+                    float4 u[8];                           // sums, a trip to L2 for two blocks
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float4 v = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                               __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-                        if (saved || (kPrecise && mine > kFlush && row_valid)) {
-                            const float4 u = sums[(4 * c + k) * tile_rows];
-                            v = saved ? make_float4(0.f, 0.f, 0.f, 0.f) : v;
-                            v.x = fmaf(u.x, sums_mul, v.x);
-                            v.y = fmaf(u.y, sums_mul, v.y);
-                            v.z = fmaf(u.z, sums_mul, v.z);
-                            v.w = fmaf(u.w, sums_mul, v.w);
+                    for (int k = 0; k < 8; ++k) {
+                        u[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (onto)
+                            u[k] = __ldcg(sums + (4 * c + k) * tile_rows);
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t o[16];
+                        tmem_ld16(ocol + 16u * (c + half), o);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float4 v = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                   __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                            if (onto) {
+                                v = saved ? make_float4(0.f, 0.f, 0.f, 0.f) : v;
+                                const float4 w = u[4 * half + k];
+                                v = make_float4(fmaf(w.x, sums_mul, v.x), fmaf(w.y, sums_mul, v.y),
+                                                fmaf(w.z, sums_mul, v.z), fmaf(w.w, sums_mul, v.w));
+                            }
+                            *reinterpret_cast<float4 *>(stage + lane * kStageStride + 16 * (c + half) + 4 * k) =
+                                wgt != 0.f ? make_float4(v.x * wgt, v.y * wgt, v.z * wgt, v.w * wgt)
+                                           : make_float4(0.f, 0.f, 0.f, 0.f);
                         }
-                        *reinterpret_cast<float4 *>(stage + lane * kStageStride + 16 * c + 4 * k) =
-                            wgt != 0.f ? make_float4(v.x * wgt, v.y * wgt, v.z * wgt, v.w * wgt)
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
                 }
                 named_barrier_sync(6 + gr, 128);           // the sums lie where the rows go
@@ -855,7 +883,7 @@ __device__ __forceinline__ void issue_role(const PrefixArgs &a, Shared &s, uint8
                     tmem_fence_after_sync();
                     const uint64_t vb = dv + ((slot * 2 * kHalfBytes) >> 4);
                     const uint32_t pcol = scol + 64u * (gi % kSBufs);
-                    const bool onto = kPrecise ? i % kFlush != 0 : i > 0;
+                    const bool onto = kPrecise ? i % B::kFlush != 0 : i > 0;
 #pragma unroll
                     for (int t = 0; t < B::kTerms; ++t)
 #pragma unroll
@@ -1136,7 +1164,7 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         scratch.work[0] = scratch.work[1] = 0;
     __syncthreads();
     for (int b = team; team < kTeams && b < n_blocks; b += kTeams)
-        find_runs<B::kNarrowCost>(a, s, scratch, team, b, ps_shift, n_blocks == 1, &work);
+        find_runs<B::kNarrowCost, B::kBorderCost>(a, s, scratch, team, b, ps_shift, n_blocks == 1, &work);
     if (work.shared + work.own != 0) {
         atomicAdd(&scratch.work[0], static_cast<unsigned long long>(work.shared));
         atomicAdd(&scratch.work[1], static_cast<unsigned long long>(work.own));
@@ -1167,7 +1195,7 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     if (warp == 0)
         tmem_alloc(&s.tmem_slot, kTmemCols);
     if (n_blocks > 1 && tid < 128)                         // the runs of the block in which the stretch begins
-        find_runs<B::kNarrowCost>(a, s, scratch, 0, s.w.block, ps_shift, true);
+        find_runs<B::kNarrowCost, B::kBorderCost>(a, s, scratch, 0, s.w.block, ps_shift, true);
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();

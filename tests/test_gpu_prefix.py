@@ -394,3 +394,64 @@ def test_an_empty_batch_and_no_sharing_at_all(pad):
     q = torch.empty((0, 1, 1, D), dtype=torch.bfloat16, device=DEV)
     kvq.kvq_decode_attn_prefix(c2.desc, q, c2.d["k"], c2.d["v"], c2.d["s0"], c2.d["s1"], e(0, 4), e(0), e(0), e(0),
                                SCALE, None, q.clone(), c2.workspace())
+
+
+def _against_the_unshared_call(desc, q, k, v, bt, lens, lead, shared, sample):
+    """All rows against kvq_decode_attn_window (both are within 2e-4 + 2e-4 |o|), some against 64 bits."""
+    n, hq = q.shape[1], q.shape[2]
+    s = torch.full((desc.num_kv_heads,), 0.011, device=DEV)
+    out, plain = (torch.full(q.shape, 7.0, dtype=torch.float32, device=DEV) for _ in range(2))
+    ws = kvq.workspace_for_prefix(desc, len(lens), n, hq, bt.shape[1])
+    kvq.kvq_decode_attn_prefix(desc, q, k, v, s, s, bt, lens, lead, shared, SCALE, None, out, ws)
+    ws = kvq.workspace_for_window(desc, len(lens), n, hq, bt.shape[1], 0)
+    kvq.kvq_decode_attn_window(desc, q, k, v, s, s, bt, lens, SCALE, 0, 0, None, plain, ws)
+    assert ((out - plain).abs() <= 4e-4 * (1 + plain.abs())).all()
+    bits = lambda x: x.view(torch.int16).cpu().numpy().view(np.uint16)  # noqa: E731
+    for r in sample:
+        pages = bt[r, :-(-int(lens[r]) // desc.page_size)].long()
+        kc, vc = k[pages], v[pages]
+        kc, vc = (bits(x) if x.dtype == torch.bfloat16 else x.cpu().numpy() for x in (kc, vc))
+        ref, bound = R.attention(bits(q[r:r + 1]), kc, vc, np.arange(len(pages), dtype=np.int32)[None],
+                                 lens[r:r + 1].cpu().numpy(), SCALE, 0, 0, ks=s.cpu().numpy(), vs=s.cpu().numpy(),
+                                 fp32=True, cut=2.0 ** -32)
+        R.assert_within(out[r:r + 1].cpu().numpy().astype(np.float64), ref, bound, f"request {r}")
+
+
+def test_the_largest_batch():
+    """65,535 requests in runs of 1,000, 64 shared tokens and up to 48 of their own each."""
+    B, N = 65535, 65535 * 3 + 4
+    g = torch.Generator(device=DEV).manual_seed(3)
+    desc = kvq.CacheDesc(N, 16, 1, D, kvq.KVQ_CACHE_FP8_E4M3)
+    k, v = (torch.randint(0, 120, (N, 1, 16, D), dtype=torch.uint8, device=DEV, generator=g) +
+            torch.randint(0, 2, (N, 1, 16, D), dtype=torch.uint8, device=DEV, generator=g) * 128 for _ in range(2))
+    q = torch.randn((B, 1, 2, D), device=DEV, generator=g).bfloat16() * 0.02
+    r = torch.arange(B, dtype=torch.int32, device=DEV)
+    bt = torch.full((B, 8), -1, dtype=torch.int32, device=DEV)
+    bt[:, :4] = torch.arange(4, dtype=torch.int32, device=DEV)
+    bt[:, 4:7] = 4 + 3 * r[:, None] + torch.arange(3, dtype=torch.int32, device=DEV)
+    lens = 64 + r % 49
+    assert kvq.kvq_decode_plan_prefix(desc, B, 1, 2, 8) > 152 * 256 * 512       # shared
+    _against_the_unshared_call(desc, q, k, v, bt, lens, r // 1000 * 1000, torch.full_like(r, 64), (0, 999, 1000, 33333, 65534))
+
+
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+def test_pages_past_four_gigabytes_of_a_cache(kind):
+    """Wide table rows, and pages whose places in the caches pass 32 bits."""
+    ps, hkv, B = 64, 2, 40
+    page_bytes = hkv * ps * D * (2 if kind == "bf16" else 1)
+    N = (5 << 30) // page_bytes
+    desc = kvq.CacheDesc(N, ps, hkv, D, kvq.KVQ_CACHE_BF16 if kind == "bf16" else kvq.KVQ_CACHE_FP8_E4M3)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    dtype = torch.bfloat16 if kind == "bf16" else torch.uint8
+    k, v = (torch.empty((N, hkv, ps, D), dtype=dtype, device=DEV) for _ in range(2))
+    used = 30 + 2 * B
+    for x in (k, v):
+        shape = (used, hkv, ps, D)
+        x[N - used:] = (torch.randn(shape, device=DEV, generator=g).bfloat16() if kind == "bf16" else
+                        torch.randint(0, 120, shape, dtype=torch.uint8, device=DEV, generator=g))
+    q = torch.randn((B, 1, 2 * hkv, D), device=DEV, generator=g).bfloat16() * 0.1
+    r = torch.arange(B, dtype=torch.int32, device=DEV)
+    bt = torch.full((B, 1 << 16), -1, dtype=torch.int32, device=DEV)
+    bt[:, :30] = N - 1 - torch.arange(30, dtype=torch.int32, device=DEV)
+    bt[:, 30:32] = N - used + 2 * r[:, None] + torch.arange(2, dtype=torch.int32, device=DEV)
+    _against_the_unshared_call(desc, q, k, v, bt, 30 * ps + 1 + r, r // 20 * 20, torch.full_like(r, 30 * ps), (0, 19, 20, 39))
