@@ -1067,7 +1067,7 @@ kvq_status kvq_copy_pages(const kvq_cache_desc *desc, void *const *caches, int32
 // apart, 20.7 shared; 13 x 4 x 5,203, three query tokens (69 MB): 24.4 against 31.0;
 // 33 x 4 x 9,701 behind five prompts (328 MB): 31.4 against 36.9; 16 x 2 x 16,901
 // over a bf16 cache, 40 rows (277 MB, three times): 75 against 39; 24 x 8 x 9,000,
-// bf16, three prompts (885 MB): 54 against 58; 64 x 8 x 10,192 (1.3 GB): 124 against 52.
+// bf16, three prompts (885 MB): 54 against 50; 64 x 8 x 10,192 (1.3 GB): 124 against 53.
 constexpr int64_t kSharingMinBytes = 512ll << 20;
 
 struct PrefixPlan {

@@ -8,9 +8,9 @@ namespace kvq {
 
 // What 64 tokens of a KV head cost, in 1/140 us of an SM, as measured in each
 // build: shared ones up to 128 query rows; a request's own, in the mma.sync kernel,
-// per 16 rows (0.36 us, over a bf16 cache 0.86).  (Over a bf16 cache with fp32 output
-// 1.47 us, counted as 2.3: 24 requests behind three prompts 61 us with 1.6, 53 so.)  A further request's rows cost
-// 11/16 of their share of the former.
+// per 16 rows (0.36 us, over a bf16 cache 0.86).  A further request's rows cost
+// 11/16 of their share of the former.  (Shared ones over a bf16 cache with fp32 output take 1.47 us
+// and count as 2.3: 24 requests behind three prompts 61 us with 1.6, 53 so.)
 struct Costs {
     int tile, join, own;
     __device__ __forceinline__ explicit Costs(const PrefixArgs &a)
