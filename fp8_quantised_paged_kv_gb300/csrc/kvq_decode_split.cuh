@@ -87,6 +87,25 @@ using CallArgs = PrefixArgs;
 constexpr bool kSharing = false;
 using CallArgs = ViewArgs;
 #endif
+// An input of the call.  Behind shared pages through L2: those builds run
+// without a wait for the grids before them (decode_split_kernel), so that what an
+// SM still holds of an input may be older than what was written to it.
+template <typename T>
+__device__ __forceinline__ T read_input(const T *p)
+{
+    if constexpr (kSharing)
+        return __ldcg(p);
+    else
+        return __ldg(p);
+}
+template <typename T>
+__device__ __forceinline__ T read_plain(const T *p)
+{
+    if constexpr (kSharing)
+        return __ldcg(p);
+    else
+        return *p;
+}
 template <bool kWindow>
 using ArgsOf = std::conditional_t<kWindow, CallArgs, DecodeArgs>;
 
@@ -913,9 +932,17 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
     } else {
         if constexpr (kSharing) {
             // Launched beside the kernel over the shared pages, once every CTA of
-            // that one has seen the launches before it end.  Nothing here
-            // reads what that kernel writes; CTA 0 ends after it, so that the
-            // combine, which waits for this launch, comes after both.
+            // that one has waited for the launches before it and said so.  Nothing
+            // here reads what that kernel writes but a number in own_takers; CTA 0
+            // ends after it, so that the combine, which waits for this launch,
+            // comes after both.
+            //
+            // A wait here would be one for that kernel's end.  In its place stands
+            // the number: that kernel releases it after its wait, one thread of
+            // each CTA here acquires it, and the barrier passes the order on to the
+            // others, the fence to their bulk copies.  What that leaves to the
+            // order in which the two start: that the number read is not an older one.
+            // Every input is read through L2 (read_input).
             if (threadIdx.x == 0) {
                 prefetch_tensor_map(&k_map);
                 prefetch_tensor_map(&v_map);
@@ -925,6 +952,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap k_map,
             if constexpr (kWindow)
                 if (__syncthreads_or(threadIdx.x == 0 && nothing_left(a)))
                     return;
+            fence_proxy_async_global();
         } else {
             start_dependent(k_map, v_map);
         }

@@ -84,7 +84,7 @@
                 static_cast<const uint16_t *>(a.q) + (R.id(a, nt * kMaxGroup + gq) * kHeadDim + 32 * tq));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint4 v = __ldg(src + i);
+                const uint4 v = read_input(src + i);
                 w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
             }
         } else {
@@ -119,7 +119,7 @@
     // without tokens to check is decided here.
     const bool step_check = !kWindow && a.expected_tags != nullptr;
     const bool reporter = step_check && split == 0 && kvh == 0 && threadIdx.x == 0;
-    const bool aborted = !step_check && a.abort_flags != nullptr && a.abort_flags[b] != 0;
+    const bool aborted = !step_check && a.abort_flags != nullptr && read_plain(a.abort_flags + b) != 0;
     const int64_t cap = static_cast<int64_t>(a.max_pages_per_seq) * ps;
     const bool zero_request = aborted || real_len <= 0 || real_len > cap;
     // Window: from here on `len` and every position count the shortened
@@ -137,7 +137,7 @@
                 const int i = threadIdx.x + k * kThreads;
                 const int64_t v = static_cast<int64_t>(first_page) + i;
                 const bool held = !zero_request && i < split_tokens / ps && (v << ps_shift) < len;
-                ids[k] = held ? __ldg(bt + i + (v < shown.sink_pages ? 0 : shown.hole)) : -1;
+                ids[k] = held ? read_input(bt + i + (v < shown.sink_pages ? 0 : shown.hole)) : -1;
             }
         }
     }
@@ -411,8 +411,8 @@
         }
     }
 
-    const float kscale = kBf16Cache || kBlocks ? 1.f : a.k_scale[kvh];
-    const float vscale = kBf16Cache || kBlocks ? 1.f : a.v_scale[kvh];
+    const float kscale = kBf16Cache || kBlocks ? 1.f : read_plain(a.k_scale + kvh);
+    const float vscale = kBf16Cache || kBlocks ? 1.f : read_plain(a.v_scale + kvh);
     // score multiplier (log2 domain) of the two query heads 2tq, 2tq + 1
     // whose scores this lane holds: the softmax scale, the K scale and the
     // undoing of their q rows' power-of-two scaling

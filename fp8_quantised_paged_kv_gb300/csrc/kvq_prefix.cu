@@ -1143,12 +1143,12 @@ prefix_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     }
     grid_dependency_wait();
     // The own pages' kernel may start beside this one: it reads nothing of it but
-    // this zero, and what was there before is there (decode_split_kernel, kSharing).
-    // It may start as soon as one thread of each CTA has said so: the zero comes
-    // before any thread of its CTA does.
+    // this zero, released behind what was written before the call (decode_split_kernel,
+    // kSharing).  It may start as soon as one thread of each CTA has said so: the zero
+    // comes before any thread of its CTA does.
     if (blockIdx.x == 0) {
         if (tid == 0) {
-            __stcg(a.own_takers, 0);
+            st_release_gpu(a.own_takers, 0);
             __threadfence();
         }
         __syncthreads();

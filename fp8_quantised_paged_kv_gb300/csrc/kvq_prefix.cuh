@@ -6,6 +6,27 @@
 
 namespace kvq {
 
+// Load and store that order what this thread reads after, or wrote and saw
+// before, at GPU scope.
+__device__ __forceinline__ int ld_acquire_gpu(const int *p)
+{
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_release_gpu(int *p, int v)
+{
+    asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// What this thread has come to see in global memory, before bulk copies that
+// it issues from here on.
+__device__ __forceinline__ void fence_proxy_async_global()
+{
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+
 // What 64 tokens of a KV head cost, in 1/140 us of an SM, as measured in each
 // build: shared ones up to 128 query rows; a request's own, in the mma.sync kernel,
 // per 16 rows (0.36 us, over a bf16 cache 0.86).  A further request's rows cost
@@ -122,15 +143,16 @@ __device__ __forceinline__ int own_ctas(const PrefixArgs &a, const Work &w)
     const int left = a.pre_ctas - w.sms(a.pre_ctas);
     const int ctas = left > 0 ? a.resident_ctas / a.pre_ctas * left : a.resident_ctas;
     if (blockIdx.x == 0 && threadIdx.x == 0)
-        __stcg(a.own_takers, ctas);
+        st_release_gpu(a.own_takers, ctas);
     return ctas;
 }
 __device__ __forceinline__ int own_ctas(const ViewArgs &a, const Work &) { return a.resident_ctas; }
 // Whether CTA 0 has found out that this one has nothing to do: the CTAs that find
-// room only when the shared pages are done leave at once.
+// room only when the shared pages are done leave at once.  (Acquires what was
+// written before the call: decode_split_kernel.)
 __device__ __forceinline__ bool nothing_left(const PrefixArgs &a)
 {
-    const int takers = __ldcg(a.own_takers);
+    const int takers = ld_acquire_gpu(a.own_takers);
     return takers > 0 && static_cast<int>(blockIdx.x) >= takers;
 }
 __device__ __forceinline__ bool nothing_left(const ViewArgs &) { return false; }
