@@ -626,6 +626,8 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
                 uint32_t sv[kTok];
                 tmem_ld64(col, sv);
                 const int vis = lim - tile * kTok;     // > 0: the row sees the tile
+                // a row that has ended has scores of -inf, times 1: the multiplier may be 0
+                const float row_mul = vis > 0 ? mul : 1.f;
                 bool ending = false, save = false;
                 if (!__all_sync(0xFFFFFFFFu, vis >= kTok)) {   // a row's tokens end between tiles
 #pragma unroll
@@ -640,7 +642,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const int x = __shfl_sync(0xFFFFFFFFu, exps, q);
-                        mk[q] = mul * __int_as_float((127 + static_cast<int8_t>(x & 0xFF)) << 23);
+                        mk[q] = row_mul * __int_as_float((127 + static_cast<int8_t>(x & 0xFF)) << 23);
                         ev[q] = static_cast<float>(x >> 8);
                     }
                 }
@@ -661,7 +663,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
                         mx = fmaxf(mx, t);
                 }
                 if constexpr (!kBlocks)
-                    mx = mx == -INFINITY ? mx : mx * mul;
+                    mx = mx == -INFINITY ? mx : mx * row_mul;
                 const bool raise = row_valid && mx > m_used + kRaiseThreshold;
                 const float alpha = raise ? (m_used == -INFINITY ? 0.f : fast_exp2(m_used - mx)) : 1.f;
                 const bool flush = kPrecise && i > 0 && i % B::kFlush == 0;
@@ -706,7 +708,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, Shared &s, uin
                     float p[32];
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const float mq = kBlocks ? mk[2 * c + q] : mul, off = kBlocks ? ev[2 * c + q] - base : -base;
+                        const float mq = kBlocks ? mk[2 * c + q] : row_mul, off = kBlocks ? ev[2 * c + q] - base : -base;
                         const uint64_t mq2 = f2_pack(mq, mq), off2 = f2_pack(off, off);
 #pragma unroll
                         for (int k = 16 * q; k < 16 * q + 16; k += 2) {
