@@ -7,8 +7,9 @@
 // held and d_r more wanted, request r takes places s_r = sum_{i < r} d_i up to
 // s_r + d_r of the free list, counted from its top; a request whose places
 // pass the list's end gets nothing, and because s does not descend, neither
-// does any later one that wants a page.  So who is served, and with which page,
-// goes by the lengths alone, not by the order in which CTAs run.
+// does any later one that wants a page.  A row whose partly filled last page has
+// other holders wants none and gets nothing.  So who is served, and with which page,
+// goes by the tables alone, not by the order in which CTAs run.
 //
 // What bounds them is latency: a step touches a few kilobytes, a batch of
 // prompts a few megabytes (its slots).  Every CTA sums the wants of the
@@ -105,7 +106,11 @@ struct Want {
     int have, need;                          // pages held, and more
     bool fits;
 };
-__device__ __forceinline__ Want want_of(const ExtendArgs &a, int r, int ps_shift)
+// tail: look whether the row may write its last, partly filled page.  One that
+// other rows hold too (kvq_trim_tables can leave it so behind a fork) is not its
+// own, and a slot in it would be one of theirs.  (Two more trips to L2 for such
+// rows, for their entry and its holders.)
+__device__ __forceinline__ Want want_of(const ExtendArgs &a, int r, int ps_shift, bool tail)
 {
     Want w;
     w.old = __ldcg(a.seq_lens + r);
@@ -118,6 +123,10 @@ __device__ __forceinline__ Want want_of(const ExtendArgs &a, int r, int ps_shift
     }
     w.fits = w.old >= 0 && w.n >= 0 && w.off >= 0 && w.off + w.n <= a.num_tokens &&
              w.old + w.n <= static_cast<int64_t>(a.max_pages_per_seq) << ps_shift;
+    if (tail && w.fits && w.n > 0 && (w.old & ((1 << ps_shift) - 1)) != 0) {
+        const int page = __ldcg(a.block_table + static_cast<int64_t>(r) * a.max_pages_per_seq + (w.old >> ps_shift));
+        w.fits = page < 0 || page >= a.pool.num_pages || __ldcg(a.pool.page_refs + page) <= 1;
+    }
     w.have = w.fits ? pages_of(w.old, ps_shift) : 0;
     w.need = w.fits ? pages_of(w.old + w.n, ps_shift) - w.have : 0;
     return w;
@@ -142,12 +151,12 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendArgs a)
     // the wants before this CTA's requests, then each of its own, in 64 bits:
     // those that no pool could fill may add up to more than 31
     int64_t mine = 0, base, all;
-    for (int r = threadIdx.x; r < r0; r += kThreads)
-        mine += want_of(a, r, ps_shift).need;
-    block_scan<kThreads>(mine, &base);
     Want w = {};
     if (static_cast<int>(threadIdx.x) < m)
-        w = want_of(a, r0 + threadIdx.x, ps_shift);
+        w = want_of(a, r0 + threadIdx.x, ps_shift, true);
+    for (int r = threadIdx.x; r < r0; r += kThreads)
+        mine += want_of(a, r, ps_shift, true).need;
+    block_scan<kThreads>(mine, &base);
     const int64_t upto = base + block_scan<kThreads>(static_cast<int64_t>(w.need), &all);
     if (static_cast<int>(threadIdx.x) < m) {
         const bool ok = w.fits && (w.need == 0 || upto <= count);
@@ -198,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendArgs a)
         return;
     int taken = 0, total;
     for (int r = threadIdx.x; r < a.batch; r += kThreads) {
-        const Want v = want_of(a, r, ps_shift);
+        const Want v = want_of(a, r, ps_shift, false);
         if (__ldcg(a.refused + r) == 0) {
             taken += v.need;
             a.seq_lens[r] = static_cast<int32_t>(v.old + v.n);

@@ -628,11 +628,11 @@ typedef struct {
  *                  length and tags are as before), else 0.  It may serve as
  *                  the step's abort_flags.
  * A request is refused if its length or number of tokens is negative, if its
- * offsets leave [0, num_tokens], if its row is too short, or if the pool runs
- * out: if the pages that it and all requests before it want, refused ones for
- * want of pages among them, are more than the list holds, and it wants one.
- * Two requests' offsets must not overlap.  A row's last, partly filled page
- * must be its own (kvq_fork_tables sees to that).
+ * offsets leave [0, num_tokens], if its row is too short, if it has new tokens
+ * and its last, partly filled page has other holders (kvq_trim_tables), or if
+ * the pool runs out: if the pages that it and all requests before it want,
+ * refused ones for want of pages among them, are more than the list holds, and
+ * it wants one.  Two requests' offsets must not overlap.
  */
 KVQ_API kvq_status kvq_extend_tables(const kvq_page_pool *pool, const int32_t *token_offsets,
                                      int32_t num_tokens, int32_t *seq_lens, int32_t batch,
@@ -680,6 +680,12 @@ KVQ_API kvq_status kvq_fork_tables(const kvq_page_pool *pool, const int32_t *par
  *                  entries given back -1.
  * Entries outside [0, num_pages) are dropped, and a page is given back no more
  * often than it is held.  A row longer than its table counts as full.
+ *
+ * A row that shares pages and is trimmed into one of them ends in a page that
+ * other rows read.  kvq_extend_tables refuses it, and the other holders where
+ * they end in that page too, until one holder is left.  What goes on from there at
+ * once is an empty row forked onto it at its length, which gets a page of its own
+ * and a pair to copy; the row itself is then trimmed to 0.
  */
 KVQ_API kvq_status kvq_trim_tables(const kvq_page_pool *pool, const int32_t *keep_lens,
                                    int32_t *seq_lens, int32_t batch, int32_t *block_table,
