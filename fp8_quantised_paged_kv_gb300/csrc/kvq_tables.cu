@@ -32,6 +32,7 @@ constexpr int kTrimThreads = 512;
 // is a chain of trips to L2 otherwise (60 rows of up to 1,711 entries forked,
 // extended by a token and trimmed: 21.6 us one at a time).
 constexpr int kBatch = 4;
+constexpr int64_t kMaxTokens = 0x7FFFFFFF;             // that an int32 length holds, whatever the row's width
 
 __device__ __forceinline__ int pages_of(int64_t tokens, int ps_shift)
 {
@@ -122,7 +123,7 @@ __device__ __forceinline__ Want want_of(const ExtendArgs &a, int r, int ps_shift
         w.off = w.n * r;
     }
     w.fits = w.old >= 0 && w.n >= 0 && w.off >= 0 && w.off + w.n <= a.num_tokens &&
-             w.old + w.n <= static_cast<int64_t>(a.max_pages_per_seq) << ps_shift;
+             w.old + w.n <= min(static_cast<int64_t>(a.max_pages_per_seq) << ps_shift, kMaxTokens);
     if (tail && w.fits && w.n > 0 && (w.old & ((1 << ps_shift) - 1)) != 0) {
         const int page = __ldcg(a.block_table + static_cast<int64_t>(r) * a.max_pages_per_seq + (w.old >> ps_shift));
         w.fits = page < 0 || page >= a.pool.num_pages || __ldcg(a.pool.page_refs + page) <= 1;

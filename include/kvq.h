@@ -628,11 +628,12 @@ typedef struct {
  *                  length and tags are as before), else 0.  It may serve as
  *                  the step's abort_flags.
  * A request is refused if its length or number of tokens is negative, if its
- * offsets leave [0, num_tokens], if its row is too short, if it has new tokens
- * and its last, partly filled page has other holders (kvq_trim_tables), or if
- * the pool runs out: if the pages that it and all requests before it want,
- * refused ones for want of pages among them, are more than the list holds, and
- * it wants one.  Two requests' offsets must not overlap.
+ * offsets leave [0, num_tokens], if its row is too short or its length would
+ * pass 2^31 - 1, if it has new tokens and its last, partly filled page has other
+ * holders (kvq_trim_tables), or if the pool runs out: if the pages that it and
+ * all requests before it want, refused ones for want of pages among them, are
+ * more than the list holds, and it wants one.  Two requests' offsets must not
+ * overlap.
  */
 KVQ_API kvq_status kvq_extend_tables(const kvq_page_pool *pool, const int32_t *token_offsets,
                                      int32_t num_tokens, int32_t *seq_lens, int32_t batch,
