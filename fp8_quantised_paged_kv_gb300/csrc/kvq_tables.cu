@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kTrimThreads) trim_kernel(const TrimArgs a)
     __shared__ uint32_t s_bits[kWords];
     __shared__ int s_place[kWords];
     int count = clamp_count(__ldcg(a.pool.free_count), a.pool.num_pages);
-    const int words = (a.pool.num_pages + 31) / 32;
+    const int words = static_cast<int>((static_cast<int64_t>(a.pool.num_pages) + 31) / 32);
     for (int w0 = 0; w0 < words; w0 += kWords) {
         uint32_t bits[4];
         int n = 0;
