@@ -46,8 +46,10 @@ struct Costs {
 // A request's tokens by where they come from: whole pages, in whole 64 tokens, of row
 // prefix_of[r], as many as all its query tokens see and the other row holds, and its own row
 // (both 0: its outputs are zeros).  The other row serves only where so many
-// consecutive requests (up to eight are counted) name it that this costs less than each
-// reading its own: three of one query token over e4m3, two over a bf16 cache.
+// consecutive requests (up to eight are counted) name it that this costs less, by Costs, than
+// each reading its own.  With one query token: over e4m3 three (block scales four from
+// seven heads a group on), with fp32 output four (five from five heads on, and with block
+// scales); over a bf16 cache two, with fp32 output three.
 // `joins`: the request before it names the same row.  (Through L2: whatever wrote
 // the numbers may have run on this SM beside this CTA.)
 struct Tokens {

@@ -514,8 +514,11 @@ KVQ_API kvq_status kvq_decode_attn_blocks(const kvq_cache_desc *desc, const void
  * of K and V (batch * max_pages_per_seq pages, once per 16 query rows of a KV
  * head), every request reads its own row, in the launches of
  * kvq_decode_attn_window; else the other row serves where so many consecutive
- * requests name it that one pass of the tensor cores costs less than theirs
- * (three with one query token over e4m3).  Then there are three launches: the shared
+ * requests name it that one pass of the tensor cores costs less than theirs.  With one
+ * query token that is, over e4m3, three requests with bf16 output (four with block
+ * scales and seven or eight heads per KV head), four with fp32 output (five with
+ * five heads and more, or block scales); over a bf16 cache two, with fp32 output
+ * three.  Then there are three launches: the shared
  * pages on the 5th-generation tensor cores, up to 256 query rows (request, token,
  * head) of a KV head at a time; the requests' own pages beside it; the parts of
  * both joined.  Each shares its work out evenly on the device, whatever the
