@@ -523,6 +523,19 @@ KVQ_API kvq_status kvq_decode_attn_blocks(const kvq_cache_desc *desc, const void
  * head) of a KV head at a time; the requests' own pages beside it; the parts of
  * both joined.  Each shares its work out evenly on the device, whatever the
  * lengths.
+ *
+ * The table's width decides, not the lengths in it: a few short requests in rows
+ * that allow 512 MB take the three launches too (15 us more than apart).
+ * The workspace of such a call has places for every query row twice and for 256
+ * rows of each SM, 516 bytes each, whatever the requests share.
+ * Beyond kvq_decode_attn_mt's limits it is KVQ_ERR_UNSUPPORTED where batch * KV heads *
+ * ceil(n * heads per KV head / 16) * (the table's tokens + 384) / max(page_size, 64)
+ * comes near 2^31 (2,048 requests of 8 KV heads, 128 query rows and 1 M tokens).
+ * With bf16 output a weight is rounded to 16 bits before it multiplies V, as in
+ * kvq_decode_attn_window: to f16 over e4m3 (2^-11 of itself), to bf16 over a bf16
+ * cache (2^-8: outputs behind 16,001 shared tokens are off by 2.3e-3 of their norm,
+ * where their own rounding alone is 1.7e-3).  With fp32 output weights keep 22
+ * bits and more.
  */
 KVQ_API kvq_status kvq_decode_plan_prefix(const kvq_cache_desc *desc, int32_t batch,
                                           int32_t num_query_tokens, int32_t num_q_heads,
