@@ -642,7 +642,8 @@ typedef struct {
  *                  no request's offsets name are left as they were.
  *   refused        uint8 [batch], OUT: 1 if the request got nothing (its row,
  *                  length and tags are as before), else 0.  It may serve as
- *                  the step's abort_flags.
+ *                  the step's abort_flags; kvq_append_blocks, which finds its
+ *                  places by the lengths, needs it among them.
  * A request is refused if its length or number of tokens is negative, if its
  * offsets leave [0, num_tokens], if its row is too short or its length would
  * pass 2^31 - 1, if it has new tokens and its last, partly filled page has other
