@@ -1063,11 +1063,19 @@ kvq_status kvq_copy_pages(const kvq_cache_desc *desc, void *const *caches, int32
 // No form needs arrival counters.
 //
 // The border goes by what the tables allow, per 16 query rows (each 16 read the
-// pages again without sharing).  4 requests x 8 KV heads x 528 tokens (4 MB): 6.0 us
-// apart, 20.7 shared; 13 x 4 x 5,203, three query tokens (69 MB): 24.4 against 31.0;
-// 33 x 4 x 9,701 behind five prompts (328 MB): 31.4 against 36.9; 16 x 2 x 16,901
-// over a bf16 cache, 40 rows (277 MB, three times): 75 against 39; 24 x 8 x 9,000,
-// bf16, three prompts (885 MB): 54 against 50; 64 x 8 x 10,192 (1.3 GB): 124 against 53.
+// pages again without sharing).  Apart and shared, us, 8 KV heads, 4 heads a group, own
+// parts of up to 500 tokens, tables as wide as the longest request (MB of 2^20):
+//                                        1,000 shared   2,000        4,000        8,000
+//   e4m3, 64 requests, one prompt        31  39 (192)   40  40 (312)   63  43 (568)  113  47 (1,064)
+//   e4m3, 64 requests, eight prompts     31  45 (192)   41  44 (312)   63  55 (568)  113  71 (1,064)
+//   e4m3, 24 requests, three prompts     13  34  (69)   18  37 (117)   28  40 (213)   47  45   (399)
+//   bf16, 32 requests, one prompt        20  33 (192)   30  32 (312)   46  30 (560)   80  32 (1,064)
+//   bf16, 24 requests, three prompts     20  32 (138)   24  32 (234)   42  33 (426)   79  46   (798)
+//   e4m3, 64 x 4 tokens, 32 rows         73  88 (384)  108  93 (640)  181 114 (1,136) 317 162 (2,128)
+// Of 96 such batches (block scales and fp32 output too) all from 512 MB on gained by
+// sharing, 4 to 72 %; from 280 to 430 MB it went either way, 36 % less to 35 % more; below,
+// all but one lost, up to 2.7 times.  What the border cannot see: tables wider than their
+// requests (4 requests of 528 tokens, 6.0 us apart, take 20.7 shared).
 constexpr int64_t kSharingMinBytes = 512ll << 20;
 
 struct PrefixPlan {

@@ -56,8 +56,10 @@ static_assert(256 * kStageStride * 4 <= kData, "every row has room");
 template <int kKind, bool kPrecise>
 struct Build {
     static constexpr bool kConvert = kKind != kBf16, kBlocks = kKind == kBlocksFp8;
-    // 16-bit terms of a weight: one for bf16 output; for fp32 output two of
-    // f16 (2^-22) or three of bf16 (2^-24)
+    // 16-bit terms of a weight: one for bf16 output (f16 2^-11; over a bf16 cache
+    // bf16 2^-8, which puts 1.6e-3 of their norm on outputs whose own rounding is
+    // 1.7e-3; the other builds round so too, kvq_decode_split_body.cuh); for fp32
+    // output two of f16 (2^-22) or three of bf16 (2^-24)
     static constexpr int kTerms = !kPrecise ? 1 : kConvert ? 2 : 3;
     // S buffers per group, of 64 columns; three terms of P need the place of both
     static constexpr int kSBufs = kTerms == 3 ? 1 : 2;
@@ -76,7 +78,8 @@ struct Build {
     // e4m3, 0.99 against 1.60 with block scales, 0.98 against 1.03 over a bf16 cache;
     // fp32 output 1.21 against 1.82, 1.45 against 2.28, 1.47 against 2.61)
     static constexpr int kNarrowCost = kKind == kBf16 ? (kPrecise ? 4 : 7) : kKind == kFp8 ? 6 : 5;
-    // and of a border between two jobs (a place is 0.15 to 0.2 us, with three terms 0.37)
+    // and of a border between two jobs: 6 to 8 us (a place is 0.15 to 0.2 us, with three
+    // terms 0.37; there 40 places took 1.3 % longer over the 18 batches at Costs)
     static constexpr int kBorderCost = kTerms == 3 ? 20 : 40;
     // fp32 output: tiles between O's ways out of tensor memory into fp32 sums that
     // round.  The tensor core cuts each addition to a large accumulator towards zero, 4

@@ -30,8 +30,11 @@ __device__ __forceinline__ void fence_proxy_async_global()
 // What 64 tokens of a KV head cost, in 1/140 us of an SM, as measured in each
 // build: shared ones up to 128 query rows; a request's own, in the mma.sync kernel,
 // per 16 rows (0.36 us, over a bf16 cache 0.86).  A further request's rows cost
-// 11/16 of their share of the former.  (Shared ones over a bf16 cache with fp32 output take 1.47 us
-// and count as 2.3: 24 requests behind three prompts 61 us with 1.6, 53 so.)
+// 11/16 of their share of the former.  Shared ones over a bf16 cache with fp32 output take
+// 1.47 us alone and count as 2.3, what they cost beside the own ones, whose copies
+// they wait for: 18 batches of 12 to 128 requests behind 1 to 16 prompts of 2,000 to
+// 14,000 tokens took 62.8 us so, in the geometric mean, and 67.8 with 1.47 (from 10 %
+// less, 30 requests of two query tokens behind three prompts, to 20 % more).
 struct Costs {
     int tile, join, own;
     __device__ __forceinline__ explicit Costs(const PrefixArgs &a)
