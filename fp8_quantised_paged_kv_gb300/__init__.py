@@ -553,7 +553,8 @@ def kvq_extend_tables(pool: PagePool, token_offsets, num_tokens: int, seq_lens, 
     num_tokens / B each).  ``seq_lens`` (int32 [B]) and ``block_table`` (int32
     [B][max_pages]) are brought up to date, ``expected_tags`` (32-bit, of the
     table's shape; None without tags) likewise; ``slot_mapping`` (int64
-    [num_tokens], or None) and ``refused`` (uint8 [B]) are written."""
+    [num_tokens], or None) and ``refused`` (uint8 [B]) are written.  A row whose
+    partly filled last page other rows hold too (kvq_trim_tables) is refused."""
     st = (_native or _load_native()).extend_tables(pool, token_offsets, num_tokens, seq_lens, block_table,
                                                    expected_tags, slot_mapping, refused, stream)
     if st:
@@ -575,7 +576,8 @@ def kvq_fork_tables(pool: PagePool, parents, fork_lens, seq_lens, block_table, e
 def kvq_trim_tables(pool: PagePool, keep_lens, seq_lens, block_table, stream=None):
     """Row r keeps its first keep_lens[r] tokens (int32 [B]; negative or not
     below its length: all); pages that no row holds any more go back to the
-    pool."""
+    pool.  A row that ends inside a shared page cannot be extended before it is
+    the page's only holder: fork an empty row onto it to go on at once."""
     st = (_native or _load_native()).trim_tables(pool, keep_lens, seq_lens, block_table, stream)
     if st:
         _check("kvq_trim_tables", st)
